@@ -119,7 +119,7 @@ size_t idx_latent_workspace_bytes(int64_t rows, int heads, int64_t max_keys);
 /*
  * Absorbed attention of every row over the records at its slots.
  *  ql_dev [rows, heads, 512], qp_dev [rows, heads, 64] bf16, 16-byte aligned,
- *  strides multiples of 8 (a transposed [heads, rows, 512] is fine).
+ *  strides positive multiples of 8 (a transposed [heads, rows, 512] is fine).
  *  slots_dev [rows, topk] int64 (row stride slots_stride): the out_slot of the
  *  score calls; negative entries anywhere are skipped, an entry beyond the
  *  pool is skipped and sets the status.  A slot listed twice counts twice.

@@ -18,26 +18,6 @@ using dsaidx::align_up;
 
 namespace {
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn get_encode_fn() {
-    static EncodeTiledFn fn = nullptr;
-    static bool tried = false;
-    if (!tried) {
-        tried = true;
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                             &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(p);
-    }
-    return fn;
-}
-
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 bool same_device(const idx_cache* c) {
@@ -99,6 +79,25 @@ std::atomic<unsigned long long> g_test_wait_ns{dsaidx::kWaitLimitNs};
 
 }  // namespace
 
+namespace dsaidx {
+
+EncodeTiledFn encode_tiled_fn() {
+    static EncodeTiledFn fn = nullptr;
+    static bool tried = false;
+    if (!tried) {
+        tried = true;
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                             &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiledFn>(p);
+    }
+    return fn;
+}
+
+}  // namespace dsaidx
+
 extern "C" {
 
 size_t idx_block_bytes(int key_dtype, int block_size, int head_dim) {
@@ -118,7 +117,7 @@ idx_status idx_cache_create(idx_cache** out, void* pool_dev, int64_t num_blocks,
     int dev = -1, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return IDX_ERR_CUDA;
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return IDX_ERR_CUDA;
-    EncodeTiledFn enc = get_encode_fn();
+    dsaidx::EncodeTiledFn enc = dsaidx::encode_tiled_fn();
     if (!enc) return IDX_ERR_CUDA;
     idx_cache* c = new (std::nothrow) idx_cache;
     if (!c) return IDX_ERR_CUDA;

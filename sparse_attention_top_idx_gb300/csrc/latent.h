@@ -56,7 +56,7 @@ struct AttendArgs {
     int32_t* status;
     void* ws;                    // behind the header
 };
-cudaError_t launch_attend(const AttendArgs& a, int sms, cudaStream_t st);
+cudaError_t launch_attend(const AttendArgs& a, cudaStream_t st);
 size_t attend_ws_bytes(int64_t rows, int heads, int64_t max_keys);
 
 struct ExpandedArgs {

@@ -42,6 +42,10 @@ idx_status attend_check(const idx_latent_pool* pool, const void* ql, int64_t ql_
     if (!ql || !qp || !out || !ws) return IDX_ERR_INVALID_ARG;
     if (!aligned(ql, 16) || !aligned(qp, 16) || !aligned(out, 16) || !aligned(ws, 256)) return IDX_ERR_INVALID_ARG;
     if (!mult8(ql_row) || !mult8(ql_head) || !mult8(qp_row) || !mult8(qp_head)) return IDX_ERR_INVALID_ARG;
+    // strides that are stepped over: positive and within a tensor map's range
+    const int64_t cap = int64_t(1) << 38;
+    if (rows > 1 && (ql_row < 1 || ql_row > cap || qp_row < 1 || qp_row > cap)) return IDX_ERR_INVALID_ARG;
+    if (heads > 1 && (ql_head < 1 || ql_head > cap || qp_head < 1 || qp_head > cap)) return IDX_ERR_INVALID_ARG;
     if (ws_bytes < idx_latent_workspace_bytes(rows, heads, max_keys)) return IDX_ERR_WORKSPACE_TOO_SMALL;
     return IDX_OK;
 }
@@ -137,8 +141,6 @@ idx_status idx_latent_attend_slots(const idx_latent_pool* pool, const void* ql_d
                                       workspace_dev, ws_bytes);
     if (c != IDX_OK || rows == 0) return c;
     if ((!slots_dev && topk > 0) || !aligned(slots_dev, 8)) return IDX_ERR_INVALID_ARG;
-    int sms = 0;
-    if (!sm_count(&sms)) return IDX_ERR_CUDA;
     AttendArgs a{};
     a.ql = ql_dev; a.qp = qp_dev;
     a.ql_row = ql_row_stride; a.ql_head = ql_head_stride; a.qp_row = qp_row_stride; a.qp_head = qp_head_stride;
@@ -148,7 +150,7 @@ idx_status idx_latent_attend_slots(const idx_latent_pool* pool, const void* ql_d
     a.out = out_dev; a.lse = lse_dev;
     a.status = static_cast<int32_t*>(workspace_dev);
     a.ws = static_cast<uint8_t*>(workspace_dev) + 256;
-    return status_of(launch_attend(a, sms, static_cast<cudaStream_t>(stream)));
+    return status_of(launch_attend(a, static_cast<cudaStream_t>(stream)));
 }
 
 idx_status idx_latent_attend_paged(const idx_latent_pool* pool, const void* ql_dev, int64_t ql_row_stride,
@@ -163,8 +165,6 @@ idx_status idx_latent_attend_paged(const idx_latent_pool* pool, const void* ql_d
     if (c != IDX_OK || batch == 0) return c;
     if (!block_table_dev || !seq_lens_dev || !aligned(block_table_dev, 4) || !aligned(seq_lens_dev, 4))
         return IDX_ERR_INVALID_ARG;
-    int sms = 0;
-    if (!sm_count(&sms)) return IDX_ERR_CUDA;
     AttendArgs a{};
     a.ql = ql_dev; a.qp = qp_dev;
     a.ql_row = ql_row_stride; a.ql_head = ql_head_stride; a.qp_row = qp_row_stride; a.qp_head = qp_head_stride;
@@ -174,7 +174,7 @@ idx_status idx_latent_attend_paged(const idx_latent_pool* pool, const void* ql_d
     a.out = out_dev; a.lse = lse_dev;
     a.status = static_cast<int32_t*>(workspace_dev);
     a.ws = static_cast<uint8_t*>(workspace_dev) + 256;
-    return status_of(launch_attend(a, sms, static_cast<cudaStream_t>(stream)));
+    return status_of(launch_attend(a, static_cast<cudaStream_t>(stream)));
 }
 
 idx_status idx_latent_attend_expanded(const void* q_dev, int64_t q_row_stride, int64_t q_head_stride,

@@ -1,104 +1,797 @@
 // latent_attend.cu -- absorbed latent attention over selected slots or a paged
-// context: one CTA a (row, head), keys in tiles of 128, one pass with the
-// running maximum and sum of the softmax in fp32.
+// context.
+//
+// Mathematics, for one row (a query of up to 64 heads) and tiles of 64 keys
+// with records [c | p]:
+//   S^T = K Q^T           [64 keys, heads],  K = [c | p], 36 steps of 16
+//   P   = 2^(S scale log2(e) - m)            per head, masked keys 0
+//   O^T = c^T P^T         [512, heads]       accumulated over the tiles
+// Keys are the rows of the score product and latent dimensions those of the
+// value product, so a call with few heads (16, 32) issues narrow products
+// instead of padding its heads to 64 or 128 rows, and the tile that the rows'
+// gather leaves in shared memory is the operand of both products: K-major for
+// the scores, MN-major for the values.
+//
+// One persistent CTA an SM, warp-specialised:
+//   warp 0     gathers records, four rows a TMA instruction, into a ring of
+//              16 KB chunk pairs (128 latent dimensions of 64 keys) and one of
+//              position chunks; a masked key is a row outside the map: zeros
+//   warp 1     one lane issues every MMA; the scores of tile i + 1 run while
+//              tile i is in softmax
+//   warp 2     loads a row's queries
+//   warps 4-7  softmax and epilogue
+// A chunk pair is freed by the value product that reads it last, so the next
+// tile's loads start while this tile's products run.
+//
+// The running maximum of a head moves only when a score passes it by 2^8
+// (weights stay below 256, in fp32 and in bf16 with the same relative error),
+// so most tiles need neither a maximum over keys nor a rescaled accumulator:
+// one barrier with an OR decides for all heads.  Weights are rounded to bf16
+// for the value product (relative 2^-9, as large as the rounding of the
+// result); their sums, the statistics and both accumulators are fp32.
+//
+// Few rows over many keys: the tiles of all rows form one line that is cut
+// into equal runs, one a CTA; a row that is cut leaves partial sums (fp32) in
+// the workspace, which a second kernel joins in the order of the keys.
 #include <cuda_bf16.h>
 
 #include <cmath>
+#include <utility>
 
-#include "common.cuh"
+#include "internal.h"
 #include "latent.h"
+#include "latent_mma.cuh"
 
 namespace dsaidx {
 
 namespace {
 
-constexpr int kTile = 128;
+constexpr int kKeys = 64;                  // keys a tile
+constexpr int kChunk = kKeys * 128;        // bytes of a chunk: 64 keys x 64 values
+constexpr int kPair = 2 * kChunk;
+constexpr int kAttThreads = 256;
+constexpr int kSoftThreads = 128;
+constexpr int kMaxCtas = 152;              // one an SM; CTAs never wait on one another
+constexpr float kNone = -3.0e38f;          // maximum of a head without a key so far
+constexpr float kGrow = 8.0f;              // log2 by which a score may pass the maximum
 
-__device__ __forceinline__ float bf(uint16_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
+// Shared memory: queries, weights, the pair ring, the position ring, then
+// masks, statistics and barriers.
+struct Plan {
+    int pairs, q_off, p_off, ring_off, pe_off, stat_off, mask_off, bar_off, total;
+};
+__host__ __device__ constexpr Plan plan_of(int N) {
+    Plan p{};
+    p.pairs = N == 64 ? 8 : N == 32 ? 10 : 11;
+    int o = 0;
+    p.q_off = o;    o += 9 * N * 128;
+    p.p_off = o;    o += kChunk;
+    p.ring_off = o; o += p.pairs * kPair;
+    p.pe_off = o;   o += 2 * kChunk;
+    p.stat_off = o; o += 5 * N * 4;        // four warps' values and one for all
+    p.mask_off = o; o += 4 * 8;
+    p.bar_off = o;  o += (2 * p.pairs + 16) * 8 + 32;
+    p.total = o + 1024;
+    return p;
+}
+static_assert(plan_of(64).total <= 232448 && plan_of(32).total <= 232448 && plan_of(16).total <= 232448,
+              "fits one SM's shared memory");
 
-// Slot of key j of a row, -1 where it is masked.
-__device__ __forceinline__ int64_t key_slot(const AttendArgs& a, int64_t row, int j) {
-    int64_t s;
-    if (a.block_table == nullptr) {
-        s = a.slots[row * a.slots_stride + j];
-        if (s < 0) return -1;
-    } else {
-        const int blk = a.block_table[row * a.mbps + j / a.block_size];
-        s = blk < 0 ? a.num_slots : static_cast<int64_t>(blk) * a.block_size + j % a.block_size;
+struct Params {
+    const int64_t* slots;
+    int64_t slots_stride;
+    const int32_t* block_table;
+    const int32_t* seq_lens;
+    int64_t rows, num_slots;
+    int block_size, mbps, heads, hgs, max_keys;
+    int split;                 // tiles of all rows in equal runs (else whole rows)
+    int ql_swap, qp_swap;      // the map's middle dimension is the row
+    float scale_log2;
+    __nv_bfloat16* out;
+    float* lse;
+    int32_t* status;
+    float* part_o;             // [2 ctas][N][512]
+    float2* part_ml;           // [2 ctas][N]
+};
+
+// Visible keys of a row: its length where that is in range, else 0.
+__device__ __forceinline__ int row_keys(const Params& p, int64_t row) {
+    if (p.block_table == nullptr) return p.max_keys;
+    const int n = __ldg(p.seq_lens + row);
+    if (n < 0 || n > p.max_keys || n > static_cast<int64_t>(p.mbps) * p.block_size) return 0;
+    return n;
+}
+// Tiles of a row; one for an empty row, which still writes its result.
+__device__ __forceinline__ int tiles_of(int keys) { return keys > 0 ? (keys - 1) / kKeys + 1 : 1; }
+
+// Where the run of CTA c of g begins in the line of tt tiles.
+__device__ __forceinline__ int64_t run_start(int64_t c, int64_t g, int64_t tt) { return c * tt / g; }
+
+// Row in whose tiles position x of the line lies, and where the row begins
+// (both scaled by the head groups); with x < 0 the length of the line.
+// Executed by a whole warp; paged contexts only.
+__device__ __forceinline__ void find_row(const Params& p, int64_t x, int64_t& row, int64_t& base) {
+    const int lane = lane_id();
+    int64_t acc = 0;
+    for (int64_t r0 = 0; r0 < p.rows; r0 += 32) {
+        const int64_t r = r0 + lane;
+        int64_t v = r < p.rows ? static_cast<int64_t>(tiles_of(row_keys(p, r))) * p.hgs : 0;
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t u = __shfl_up_sync(~0u, v, d);
+            if (lane >= d) v += u;
+        }
+        const unsigned in = __ballot_sync(~0u, x >= 0 && x < acc + v && r < p.rows);
+        if (in) {
+            const int k = __ffs(in) - 1;
+            const int64_t before = __shfl_sync(~0u, v, k > 0 ? k - 1 : 0);
+            row = r0 + k;
+            base = acc + (k > 0 ? before : 0);
+            return;
+        }
+        acc += __shfl_sync(~0u, v, 31);
     }
-    if (s >= a.num_slots) {
-        set_status(a.status, IDX_ERR_DEVICE_CHECK);
-        return -1;
-    }
-    return s;
+    row = p.rows;
+    base = acc;
 }
 
-__global__ void __launch_bounds__(kTile) attend_kernel(const AttendArgs a) {
-    __shared__ float q[IDX_LATENT_RECORD];
-    __shared__ float pr[kTile];
-    __shared__ int64_t sl[kTile];
-    __shared__ float red[4];
+// One piece of work: tiles [t0, t1) of a row's head group.
+struct Work {
+    int64_t row;
+    int hg, keys, t0, t1;
+    int slot;       // where its partial sums go; -1: it has all tiles, write the result
+};
+
+// The pieces of this CTA, in order; every role walks them by itself.
+struct Walk {
+    int64_t pos, end;        // split: the run left; whole: item and number of items
+    int64_t row, base;       // split, paged: current row and where it begins
+    bool first;
+    __device__ __forceinline__ Walk(const Params& p, int64_t start, int64_t end_, int64_t row_, int64_t base_)
+        : pos(start), end(end_), row(row_), base(base_), first(true) {}
+    __device__ __forceinline__ bool next(const Params& p, Work& w) {
+        if (pos >= end) return false;
+        if (!p.split) {
+            w.row = pos / p.hgs;
+            w.hg = static_cast<int>(pos - w.row * p.hgs);
+            w.keys = row_keys(p, w.row);
+            w.t0 = 0;
+            w.t1 = tiles_of(w.keys);
+            w.slot = -1;
+            pos += gridDim.x;
+            return true;
+        }
+        int64_t in;
+        int nt;
+        if (p.block_table == nullptr) {
+            w.keys = p.max_keys;
+            nt = tiles_of(w.keys);
+            const int64_t item = pos / nt;
+            w.row = item / p.hgs;
+            w.hg = static_cast<int>(item - w.row * p.hgs);
+            in = pos - item * nt;
+        } else {
+            w.keys = row_keys(p, row);
+            nt = tiles_of(w.keys);
+            if (pos - base >= static_cast<int64_t>(nt) * p.hgs) {
+                base += static_cast<int64_t>(nt) * p.hgs;
+                ++row;
+                w.keys = row_keys(p, row);
+                nt = tiles_of(w.keys);
+            }
+            w.row = row;
+            w.hg = static_cast<int>((pos - base) / nt);
+            in = pos - base - static_cast<int64_t>(w.hg) * nt;
+        }
+        w.t0 = static_cast<int>(in);
+        const int64_t left = end - pos;
+        w.t1 = nt - in <= left ? nt : static_cast<int>(in + left);
+        w.slot = (w.t0 == 0 && w.t1 == nt) ? -1 : 2 * static_cast<int>(blockIdx.x) + (first ? 0 : 1);
+        first = false;
+        pos += w.t1 - w.t0;
+        return true;
+    }
+};
+
+// Slot of key j of a row; num_slots (a row of zeros) where it is masked.
+__device__ __forceinline__ int key_slot(const Params& p, int64_t row, int keys, int j) {
+    if (j >= keys) return static_cast<int>(p.num_slots);
+    int64_t s;
+    if (p.block_table == nullptr) {
+        s = __ldg(p.slots + row * p.slots_stride + j);
+        if (s < 0) return static_cast<int>(p.num_slots);
+    } else {
+        const int blk = __ldg(p.block_table + row * p.mbps + j / p.block_size);
+        s = blk < 0 ? p.num_slots : static_cast<int64_t>(blk) * p.block_size + j % p.block_size;
+    }
+    if (s >= p.num_slots) {
+        set_status(p.status, IDX_ERR_DEVICE_CHECK);
+        return static_cast<int>(p.num_slots);
+    }
+    return static_cast<int>(s);
+}
+
+template <int N>
+__global__ void __launch_bounds__(kAttThreads, 1)
+    attend_kernel(const __grid_constant__ CUtensorMap pool_map, const __grid_constant__ CUtensorMap ql_map,
+                  const __grid_constant__ CUtensorMap qp_map, const Params p) {
+    constexpr Plan kPlan = plan_of(N);
+    constexpr int kPairs = kPlan.pairs;
+    constexpr int kSPitch = N < 32 ? 32 : N;   // TMEM columns of a score buffer
+    constexpr int kSCol = 4 * N;               // first column behind the accumulators
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* bar = reinterpret_cast<uint64_t*>(smem + kPlan.bar_off);
+    uint64_t* pair_full = bar;
+    uint64_t* pair_empty = bar + kPairs;
+    uint64_t* pe_full = bar + 2 * kPairs;        // [2]
+    uint64_t* pe_empty = pe_full + 2;            // [2]
+    uint64_t* s_full = pe_full + 4;              // [2]
+    uint64_t* p_full = pe_full + 6;
+    uint64_t* pv_done = pe_full + 7;
+    uint64_t* q_full = pe_full + 8;
+    uint64_t* q_empty = pe_full + 9;
+    uint64_t* o_empty = pe_full + 10;
+    uint64_t* drain = pe_full + 11;
+    int64_t* sh_run = reinterpret_cast<int64_t*>(pe_full + 12);   // start, end, row, base
+    uint32_t* sh_tmem = reinterpret_cast<uint32_t*>(pe_full + 16);
+    int* sh_abort = reinterpret_cast<int*>(sh_tmem + 1);
+    uint32_t* masks = reinterpret_cast<uint32_t*>(smem + kPlan.mask_off);   // [4][2]
+    float* stat = reinterpret_cast<float*>(smem + kPlan.stat_off);          // [5][N]
+    const int warp = warp_id(), lane = lane_id();
+
+    if (warp == 0 && elect_one()) {
+        for (int i = 0; i < kPairs; ++i) {
+            mbar_init(pair_full + i, 1);
+            mbar_init(pair_empty + i, 1);
+        }
+        for (int i = 0; i < 6; ++i) mbar_init(pe_full + i, 1);
+        mbar_init(p_full, kSoftThreads);
+        mbar_init(pv_done, 1);
+        mbar_init(q_full, 1);
+        mbar_init(q_empty, 1);
+        mbar_init(o_empty, kSoftThreads);
+        mbar_init(drain, 1);
+        *sh_abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(sh_tmem, 512);
+        tmem_relinquish();
+    }
+    if (warp == 2 && elect_one()) {
+        tma_prefetch_desc(&pool_map);
+        tma_prefetch_desc(&ql_map);
+        tma_prefetch_desc(&qp_map);
+    }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (warp == 3) {
+        int64_t start, end, row = 0, base = 0;
+        if (!p.split) {
+            start = blockIdx.x;
+            end = p.rows * p.hgs;
+        } else {
+            int64_t tt;
+            if (p.block_table == nullptr) {
+                tt = p.rows * p.hgs * tiles_of(p.max_keys);
+            } else {
+                int64_t none;
+                find_row(p, -1, none, tt);
+            }
+            start = run_start(blockIdx.x, gridDim.x, tt);
+            end = run_start(blockIdx.x + 1, gridDim.x, tt);
+            if (p.block_table != nullptr && start < end) find_row(p, start, row, base);
+        }
+        if (lane == 0) {
+            sh_run[0] = start;
+            sh_run[1] = end;
+            sh_run[2] = row;
+            sh_run[3] = base;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *sh_tmem;
+    volatile int* abort_flag = sh_abort;
+    Walk walk(p, sh_run[0], sh_run[1], sh_run[2], sh_run[3]);
+    Work w;
+
+    if (warp == 0) {
+        // ---- gather: lanes 0-15 take four keys each ----
+        uint32_t it = 0, pc = 0;      // tiles and chunk pairs issued
+        bool ok = true;
+        while (ok && walk.next(p, w)) {
+            if (p.block_table != nullptr && w.keys == 0 && lane == 0 && __ldg(p.seq_lens + w.row) != 0)
+                set_status(p.status, IDX_ERR_DEVICE_CHECK);
+            int4 s = make_int4(0, 0, 0, 0);
+            auto load = [&](int t) {
+                if (lane < 16) {
+                    const int j = t * kKeys + 4 * lane;
+                    s.x = key_slot(p, w.row, w.keys, j);
+                    s.y = key_slot(p, w.row, w.keys, j + 1);
+                    s.z = key_slot(p, w.row, w.keys, j + 2);
+                    s.w = key_slot(p, w.row, w.keys, j + 3);
+                }
+            };
+            load(w.t0);
+            for (int t = w.t0; t < w.t1 && ok; ++t, ++it) {
+                const int none = static_cast<int>(p.num_slots);
+                const uint32_t mine = lane < 16 ? (s.x != none) | (s.y != none) << 1 | (s.z != none) << 2 | (s.w != none) << 3 : 0;
+                uint32_t lo = lane < 8 ? mine << (4 * lane) : 0u, hi = lane >= 8 && lane < 16 ? mine << (4 * (lane - 8)) : 0u;
+                lo = __reduce_or_sync(~0u, lo);
+                hi = __reduce_or_sync(~0u, hi);
+                const int4 rows = s;
+                if (t + 1 < w.t1) load(t + 1);
+                ok = mbar_wait(pe_empty + (it & 1), ((it >> 1) & 1) ^ 1, p.status, abort_flag);
+                if (!__all_sync(~0u, ok)) { ok = false; break; }
+                uint8_t* pe = smem + kPlan.pe_off + (it & 1) * kChunk;
+                if (lane == 0) {
+                    masks[2 * (it & 3)] = lo;
+                    masks[2 * (it & 3) + 1] = hi;
+                    mbar_arrive_expect_tx(pe_full + (it & 1), kChunk);
+                }
+                __syncwarp();
+                if (lane < 16) tma_gather4(smem_u32(pe) + lane * 512, &pool_map, pe_full + (it & 1), IDX_LATENT_DIM, rows);
+                for (int m = 0; m < 4; ++m, ++pc) {
+                    const uint32_t sl = pc % kPairs;
+                    ok = mbar_wait(pair_empty + sl, ((pc / kPairs) & 1) ^ 1, p.status, abort_flag);
+                    if (!__all_sync(~0u, ok)) { ok = false; break; }
+                    if (lane == 0) mbar_arrive_expect_tx(pair_full + sl, kPair);
+                    __syncwarp();
+                    if (lane < 16) {
+                        const uint32_t dst = smem_u32(smem + kPlan.ring_off) + sl * kPair + lane * 512;
+                        tma_gather4(dst, &pool_map, pair_full + sl, 128 * m, rows);
+                        tma_gather4(dst + kChunk, &pool_map, pair_full + sl, 128 * m + 64, rows);
+                    }
+                }
+            }
+        }
+        if (!ok) {
+            // gave up: wait (bounded) for the copies in flight before leaving
+            for (uint32_t k = pc > kPairs ? pc - kPairs : 0; k < pc; ++k)
+                mbar_wait(pair_full + k % kPairs, (k / kPairs) & 1, p.status, nullptr);
+            for (uint32_t k = it > 2 ? it - 2 : 0; k <= it; ++k)
+                mbar_wait(pe_full + (k & 1), (k >> 1) & 1, p.status, nullptr);
+        }
+    } else if (warp == 1) {
+        // ---- every MMA ----
+        if (elect_one()) {
+            constexpr uint32_t kIdS = idesc_bf16(64, N, false, false);
+            constexpr uint32_t kIdO = idesc_bf16(128, N, true, true);
+            const uint32_t q_addr = smem_u32(smem + kPlan.q_off), ring = smem_u32(smem + kPlan.ring_off);
+            const uint32_t pe_addr = smem_u32(smem + kPlan.pe_off), p_addr = smem_u32(smem + kPlan.p_off);
+            uint32_t it = 0, item = 0;      // tiles whose scores were issued, pieces
+            bool ok = true;
+            auto scores = [&](uint32_t i) -> bool {
+                const uint32_t d = tmem + kSCol + (i & 1) * kSPitch;
+                if (!mbar_wait(pe_full + (i & 1), (i >> 1) & 1, p.status, abort_flag)) return false;
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    mma_bf16(d, sdesc_sw128(pe_addr + (i & 1) * kChunk + 32 * k), sdesc_sw128(q_addr + 8 * N * 128 + 32 * k), kIdS,
+                             k != 0);
+                mma_commit(pe_empty + (i & 1));
+                for (int m = 0; m < 4; ++m) {
+                    const uint32_t pc = 4 * i + m, sl = pc % kPairs;
+                    if (!mbar_wait(pair_full + sl, (pc / kPairs) & 1, p.status, abort_flag)) return false;
+                    tc_fence_after();
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        mma_bf16(d, sdesc_sw128(ring + sl * kPair + (k >> 2) * kChunk + 32 * (k & 3)),
+                                 sdesc_sw128(q_addr + (2 * m + (k >> 2)) * N * 128 + 32 * (k & 3)), kIdS, 1u);
+                }
+                mma_commit(s_full + (i & 1));
+                return true;
+            };
+            while (ok && walk.next(p, w)) {
+                ok = mbar_wait(q_full, item & 1, p.status, abort_flag) && scores(it);
+                if (!ok) break;
+                if (w.t1 - w.t0 == 1) mma_commit(q_empty);
+                for (int t = w.t0; t < w.t1; ++t, ++it) {
+                    if (t + 1 < w.t1) {
+                        if (!(ok = scores(it + 1))) break;
+                        if (t + 2 == w.t1) mma_commit(q_empty);
+                    }
+                    if (!(ok = mbar_wait(p_full, it & 1, p.status, abort_flag))) break;
+                    if (t == w.t0 && !(ok = mbar_wait(o_empty, (item & 1) ^ 1, p.status, abort_flag))) break;
+                    tc_fence_after();
+                    for (int m = 0; m < 4; ++m) {
+                        const uint32_t sl = (4 * it + m) % kPairs;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            mma_bf16(tmem + m * N, sdesc_mn_sw128(ring + sl * kPair + 2048 * k, kChunk),
+                                     sdesc_mn_sw128(p_addr + 2048 * k, kChunk), kIdO, (t != w.t0 || k != 0) ? 1u : 0u);
+                        mma_commit(pair_empty + sl);
+                    }
+                    mma_commit(pv_done);
+                }
+                ++item;
+            }
+            // nothing of this CTA may run on when its shared memory and TMEM go
+            mma_commit(drain);
+            mbar_wait(drain, 0, p.status, nullptr);
+        }
+    } else if (warp == 2) {
+        // ---- queries ----
+        if (elect_one()) {
+            uint32_t item = 0;
+            bool ok = true;
+            while (ok && walk.next(p, w)) {
+                ok = mbar_wait(q_empty, (item & 1) ^ 1, p.status, abort_flag);
+                if (!ok) break;
+                mbar_arrive_expect_tx(q_full, 9 * N * 128);
+                const uint32_t q_addr = smem_u32(smem + kPlan.q_off);
+                const int h = w.hg * 64, row = static_cast<int>(w.row);
+                for (int c = 0; c < 8; ++c)
+                    tma_tile_3d(q_addr + c * N * 128, &ql_map, q_full, 64 * c, p.ql_swap ? row : h, p.ql_swap ? h : row);
+                tma_tile_3d(q_addr + 8 * N * 128, &qp_map, q_full, 0, p.qp_swap ? row : h, p.qp_swap ? h : row);
+                ++item;
+            }
+            if (item) mbar_wait(q_full, (item - 1) & 1, p.status, nullptr);
+        }
+    } else if (warp >= 4) {
+        // ---- softmax and epilogue ----
+        const int sw = warp - 4;
+        const int tid = threadIdx.x - 128;
+        const uint32_t lanes = static_cast<uint32_t>(32 * sw) << 16;
+        const int quad = lane & 3, kr = lane >> 2;      // column pair and key row within the warp's 16
+        constexpr int kR = N / 8;                       // column groups of 8 heads
+        uint32_t it = 0;
+        bool ok = true;
+        while (ok && walk.next(p, w)) {
+            // head 8 r + 2 quad + e: maximum and this thread's share of the sum
+            float mx[kR][2], sum[kR][2];
+#pragma unroll
+            for (int r = 0; r < kR; ++r) {
+                mx[r][0] = mx[r][1] = kNone;
+                sum[r][0] = sum[r][1] = 0.0f;
+            }
+            for (int t = w.t0; t < w.t1; ++t, ++it) {
+                ok = ok && mbar_wait(s_full + (it & 1), (it >> 1) & 1, p.status, abort_flag);
+                tc_fence_after();
+                uint32_t raw[kR < 4 ? 1 : kR / 4][16];
+#pragma unroll
+                for (int g = 0; g < (kR < 4 ? 1 : kR / 4); ++g)
+                    tmem_ld_16x256b_x4(tmem + lanes + kSCol + (it & 1) * kSPitch + 32 * g, raw[g]);
+                const uint32_t mask = masks[2 * (it & 3) + (sw >> 1)] >> (16 * (sw & 1));
+                const bool va = (mask >> kr) & 1, vb = (mask >> (kr + 8)) & 1;
+#pragma unroll
+                for (int g = 0; g < (kR < 4 ? 1 : kR / 4); ++g) tmem_wait_ld16(raw[g]);
+                // y[r][e]: key kr, y[r][2 + e]: key kr + 8; log2 of the weight
+                float y[kR][4];
+                bool grow = !ok;
+#pragma unroll
+                for (int r = 0; r < kR; ++r)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float s = __uint_as_float(raw[r / 4][4 * (r % 4) + e]);
+                        y[r][e] = (e < 2 ? va : vb) ? fmaf(s, p.scale_log2, -mx[r][e & 1]) : -INFINITY;
+                        grow |= y[r][e] > kGrow;
+                    }
+                if (named_any<1, kSoftThreads>(grow)) {
+                    // a wait that ran out in any thread ends the loop in all
+                    if (named_any<1, kSoftThreads>(!ok)) { ok = false; break; }
+                    // new maxima: over this warp's 16 keys, then over the four warps
+#pragma unroll
+                    for (int r = 0; r < kR; ++r)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float s0 = __uint_as_float(raw[r / 4][4 * (r % 4) + e]);
+                            const float s1 = __uint_as_float(raw[r / 4][4 * (r % 4) + 2 + e]);
+                            float v = fmaxf(va ? s0 * p.scale_log2 : kNone, vb ? s1 * p.scale_log2 : kNone);
+                            v = fmaxf(v, __shfl_xor_sync(~0u, v, 4));
+                            v = fmaxf(v, __shfl_xor_sync(~0u, v, 8));
+                            v = fmaxf(v, __shfl_xor_sync(~0u, v, 16));
+                            if (kr == 0) stat[sw * N + 8 * r + 2 * quad + e] = v;
+                        }
+                    named_sync<1, kSoftThreads>();
+#pragma unroll
+                    for (int r = 0; r < kR; ++r)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int h = 8 * r + 2 * quad + e;
+                            float v = fmaxf(fmaxf(stat[h], stat[N + h]), fmaxf(stat[2 * N + h], stat[3 * N + h]));
+                            v = fmaxf(v, mx[r][e]);
+                            const float f = exp2_fast(mx[r][e] - v);
+                            mx[r][e] = v;
+                            sum[r][e] *= f;
+                            if (sw == 0 && kr == 0) stat[4 * N + h] = f;
+                            const float s0 = __uint_as_float(raw[r / 4][4 * (r % 4) + e]);
+                            const float s1 = __uint_as_float(raw[r / 4][4 * (r % 4) + 2 + e]);
+                            y[r][e] = va ? fmaf(s0, p.scale_log2, -v) : -INFINITY;
+                            y[r][2 + e] = vb ? fmaf(s1, p.scale_log2, -v) : -INFINITY;
+                        }
+                    named_sync<1, kSoftThreads>();
+                    if (t != w.t0) {
+                        // the accumulator's columns (heads) times their factors
+                        ok = mbar_wait(pv_done, (it - 1) & 1, p.status, abort_flag);
+                        tc_fence_after();
+                        for (int c = 0; c < 4 * N; c += 16) {
+                            uint32_t v[16];
+                            tmem_ld16_nowait(tmem + lanes + c, v);
+                            tmem_wait_ld16(v);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j)
+                                v[j] = __float_as_uint(__uint_as_float(v[j]) * stat[4 * N + ((c + j) & (N - 1))]);
+                            tmem_st16(tmem + lanes + c, v);
+                        }
+                        tmem_wait_st();
+                    }
+                }
+                uint32_t pk[kR][2];
+#pragma unroll
+                for (int r = 0; r < kR; ++r) {
+                    float e[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) e[k] = exp2_fast(y[r][k]);
+                    sum[r][0] += e[0] + e[2];
+                    sum[r][1] += e[1] + e[3];
+                    pk[r][0] = bf16x2(e[0], e[1]);
+                    pk[r][1] = bf16x2(e[2], e[3]);
+                }
+                // weights: row = key, 64 heads of it contiguous
+                if (it > 0) ok = mbar_wait(pv_done, (it - 1) & 1, p.status, abort_flag) && ok;
+                const int ka = 16 * sw + kr;
+                uint8_t* pa = smem + kPlan.p_off + ka * 128 + 4 * quad;
+#pragma unroll
+                for (int r = 0; r < kR; ++r) {
+                    *reinterpret_cast<uint32_t*>(pa + ((r ^ (ka & 7)) << 4)) = pk[r][0];
+                    *reinterpret_cast<uint32_t*>(pa + 1024 + ((r ^ (ka & 7)) << 4)) = pk[r][1];
+                }
+                fence_proxy_async_smem();
+                tc_fence_before();
+                mbar_arrive(p_full);
+            }
+            if (!ok) break;
+            // sums over the warp's keys, then over the four warps
+            ok = mbar_wait(pv_done, (it - 1) & 1, p.status, abort_flag) && ok;
+            tc_fence_after();
+#pragma unroll
+            for (int r = 0; r < kR; ++r)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float v = sum[r][e];
+                    v += __shfl_xor_sync(~0u, v, 4);
+                    v += __shfl_xor_sync(~0u, v, 8);
+                    v += __shfl_xor_sync(~0u, v, 16);
+                    if (kr == 0) stat[sw * N + 8 * r + 2 * quad + e] = v;
+                    if (sw == 0 && kr == 0) stat[4 * N + 8 * r + 2 * quad + e] = mx[r][e];
+                }
+            if (named_any<1, kSoftThreads>(!ok)) { ok = false; break; }
+            const int h0 = w.hg * 64;
+            if (tid < N) {
+                const float l = stat[tid] + stat[N + tid] + stat[2 * N + tid] + stat[3 * N + tid];
+                const float m = stat[4 * N + tid];
+                if (w.slot >= 0)
+                    p.part_ml[static_cast<int64_t>(w.slot) * N + tid] = make_float2(m, l);
+                else if (p.lse != nullptr && h0 + tid < p.heads)
+                    p.lse[w.row * p.heads + h0 + tid] =
+                        l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+                // factor of the head's result (partial sums stay as they are)
+                stat[4 * N + tid] = w.slot >= 0 ? 1.0f : l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
+            }
+            named_sync<1, kSoftThreads>();
+            // lane = latent dimension, column = head
+            for (int c = 0; c < 4 * N; c += 16) {
+                uint32_t v[16];
+                tmem_ld16_nowait(tmem + lanes + c, v);
+                tmem_wait_ld16(v);
+                const int m = c / N, hc = c & (N - 1), d = 128 * m + 32 * sw + lane;
+                if (w.slot >= 0) {
+                    float* dst = p.part_o + (static_cast<int64_t>(w.slot) * N + hc) * IDX_LATENT_DIM + d;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) dst[j * IDX_LATENT_DIM] = __uint_as_float(v[j]);
+                } else {
+                    // neighbouring lanes swap so that each stores two dimensions of one head
+                    const bool odd = lane & 1;
+                    __nv_bfloat16* dst = p.out + (w.row * p.heads + h0 + hc + odd) * IDX_LATENT_DIM + (d & ~1);
+#pragma unroll
+                    for (int j = 0; j < 16; j += 2) {
+                        const float a = __uint_as_float(v[j]) * stat[4 * N + hc + j];
+                        const float b = __uint_as_float(v[j + 1]) * stat[4 * N + hc + j + 1];
+                        const float o = __shfl_xor_sync(~0u, odd ? a : b, 1);
+                        if (h0 + hc + j + odd < p.heads)
+                            *reinterpret_cast<uint32_t*>(dst + j * IDX_LATENT_DIM) = odd ? bf16x2(o, b) : bf16x2(a, o);
+                    }
+                }
+            }
+            tc_fence_before();
+            mbar_arrive(o_empty);
+            named_sync<1, kSoftThreads>();   // the statistics' memory is reused
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+// Joins the partial sums of the rows that were cut: one CTA a (row, head),
+// four warps over the pieces, lanes over the latent dimensions, then the warps'
+// sums in order.
+__global__ void __launch_bounds__(128) join_kernel(const Params p, int N, int ctas) {
+    __shared__ float acc[4][IDX_LATENT_DIM];
+    __shared__ float ls[4];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int64_t row = blockIdx.x;
-    const int h = blockIdx.y, tid = threadIdx.x;
-    const uint16_t* pool = static_cast<const uint16_t*>(a.pool);
-    for (int i = tid; i < IDX_LATENT_RECORD; i += kTile)
-        q[i] = i < IDX_LATENT_DIM ? bf(static_cast<const uint16_t*>(a.ql)[row * a.ql_row + h * a.ql_head + i])
-                                  : bf(static_cast<const uint16_t*>(a.qp)[row * a.qp_row + h * a.qp_head + i - IDX_LATENT_DIM]);
-    int n = a.max_keys;
-    if (a.block_table != nullptr) {
-        n = a.seq_lens[row];
-        if (n < 0 || n > a.max_keys || n > static_cast<int64_t>(a.mbps) * a.block_size) {
-            set_status(a.status, IDX_ERR_DEVICE_CHECK);
-            n = 0;
+    const int head = blockIdx.y, hg = head / 64, h = head % 64;
+    const int warp = warp_id(), lane = lane_id();
+    int64_t a, tt;
+    const int nt = tiles_of(row_keys(p, row));
+    if (p.block_table == nullptr) {
+        tt = p.rows * p.hgs * nt;
+        a = row * p.hgs * nt;
+    } else {
+        int64_t before = 0, all = 0;
+        for (int64_t r = lane; r < p.rows; r += 32) {
+            const int64_t t = static_cast<int64_t>(tiles_of(row_keys(p, r))) * p.hgs;
+            all += t;
+            if (r < row) before += t;
+        }
+        for (int d = 16; d > 0; d >>= 1) {
+            all += __shfl_xor_sync(~0u, all, d);
+            before += __shfl_xor_sync(~0u, before, d);
+        }
+        tt = all;
+        a = before;
+    }
+    a += static_cast<int64_t>(hg) * nt;
+    const int64_t b = a + nt;
+    // first and last CTA with a tile of [a, b)
+    int64_t c0 = a * ctas / tt, c1;
+    while (run_start(c0 + 1, ctas, tt) <= a) ++c0;
+    c1 = c0;
+    while (run_start(c1 + 1, ctas, tt) < b) ++c1;
+    if (c0 == c1) return;
+    auto has = [&](int64_t c) { return run_start(c, ctas, tt) < run_start(c + 1, ctas, tt); };
+    auto slot_of = [&](int64_t c) { return 2 * c + (c == c0 && run_start(c, ctas, tt) < a ? 1 : 0); };
+    float m = kNone;
+    for (int64_t c = c0 + lane; c <= c1; c += 32) {
+        if (!has(c)) continue;
+        const float2 ml = p.part_ml[slot_of(c) * N + h];
+        if (ml.y != 0.0f) m = fmaxf(m, ml.x);
+    }
+    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
+    float4 o[4] = {};
+    float l = 0.0f;
+    for (int64_t c = c0 + warp; c <= c1; c += 4) {
+        if (!has(c)) continue;
+        const int64_t s = slot_of(c) * N + h;
+        const float2 ml = p.part_ml[s];
+        if (ml.y == 0.0f) continue;
+        const float f = exp2_fast(ml.x - m);
+        l += ml.y * f;
+        const float4* src = reinterpret_cast<const float4*>(p.part_o + s * IDX_LATENT_DIM);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float4 v = __ldg(src + 32 * k + lane);
+            o[k].x += v.x * f; o[k].y += v.y * f; o[k].z += v.z * f; o[k].w += v.w * f;
         }
     }
-    float m = -INFINITY, l = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int j0 = 0; j0 < n; j0 += kTile) {
-        __syncthreads();
-        const int64_t slot = j0 + tid < n ? key_slot(a, row, j0 + tid) : -1;
-        sl[tid] = slot;
-        float s = -INFINITY;
-        if (slot >= 0) {
-            const uint16_t* r = pool + slot * IDX_LATENT_RECORD;
-            s = 0.0f;
-            for (int i = 0; i < IDX_LATENT_RECORD; ++i) s = fmaf(q[i], bf(r[i]), s);
-            s *= a.scale;
-        }
-        float w = s;
-        for (int k = 16; k > 0; k >>= 1) w = fmaxf(w, __shfl_xor_sync(~0u, w, k));
-        if ((tid & 31) == 0) red[tid >> 5] = w;
-        __syncthreads();
-        const float mn = fmaxf(m, fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])));
-        if (mn == -INFINITY) continue;
-        const float c = expf(m - mn);
-        m = mn;
-        pr[tid] = slot >= 0 ? expf(s - mn) : 0.0f;
-        __syncthreads();
-        l *= c;
-        for (int i = 0; i < 4; ++i) o[i] *= c;
-        for (int k = 0; k < kTile; ++k) {
-            l += pr[k];
-            if (sl[k] < 0) continue;
-            const uint16_t* r = pool + sl[k] * IDX_LATENT_RECORD;
-            for (int i = 0; i < 4; ++i) o[i] = fmaf(pr[k], bf(r[tid + i * kTile]), o[i]);
-        }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) reinterpret_cast<float4*>(acc[warp])[32 * k + lane] = o[k];
+    if (lane == 0) ls[warp] = l;
+    __syncthreads();
+    const float total = ls[0] + ls[1] + ls[2] + ls[3];
+    const float inv = total == 0.0f ? 0.0f : __fdiv_rn(1.0f, total);
+    const int d = 4 * threadIdx.x;
+    float v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = (acc[0][d + k] + acc[1][d + k] + acc[2][d + k] + acc[3][d + k]) * inv;
+    *reinterpret_cast<uint2*>(p.out + (row * p.heads + head) * IDX_LATENT_DIM + d) =
+        make_uint2(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]));
+    if (threadIdx.x == 0 && p.lse != nullptr)
+        p.lse[row * p.heads + head] = total == 0.0f ? -INFINITY : (m + log2f(total)) * 0.69314718055994531f;
+}
+
+// Heads of one score product.
+int width_of(int heads) { return heads <= 16 ? 16 : heads <= 32 ? 32 : 64; }
+
+// Whether the rows are cut, and the number of CTAs.
+struct Shape {
+    int N, hgs, split, ctas;
+};
+Shape shape_of(int64_t rows, int heads, int64_t max_keys) {
+    Shape s{};
+    s.N = width_of(heads);
+    s.hgs = (heads + 63) / 64;
+    const int64_t g = kMaxCtas;
+    const int64_t items = rows * s.hgs, nt = max_keys > 0 ? (max_keys + kKeys - 1) / kKeys : 1;
+    // Whole rows: ceil(items / g) rounds of nt tiles.  Cut: items nt / g tiles,
+    // plus storing and joining partial sums, which costs about as much as
+    // kCutTiles tiles.
+    constexpr int64_t kCutTiles = 6;
+    const int64_t whole = (items + g - 1) / g * nt, cut = (items * nt + g - 1) / g + kCutTiles;
+    s.split = cut < whole ? 1 : 0;
+    const int64_t n = s.split ? items * nt : items;
+    s.ctas = static_cast<int>(n < g ? n : g);
+    return s;
+}
+
+// Query map: [values, heads, rows] with the smaller stride first.
+bool query_map(CUtensorMap* map, EncodeTiledFn enc, const void* q, int dim, int64_t row_stride, int64_t head_stride,
+               int64_t rows, int heads, int N, int* swap) {
+    if (heads == 1) head_stride = dim;             // strides nobody steps over
+    if (rows == 1) row_stride = head_stride * heads;
+    *swap = head_stride > row_stride;
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(dim), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(rows)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(head_stride) * 2, static_cast<cuuint64_t>(row_stride) * 2};
+    cuuint32_t box[3] = {64, static_cast<cuuint32_t>(N), 1}, one[3] = {1, 1, 1};
+    if (*swap) {
+        std::swap(dims[1], dims[2]);
+        std::swap(strides[0], strides[1]);
+        std::swap(box[1], box[2]);
     }
-    const float inv = m == -INFINITY ? 0.0f : 1.0f / l;
-    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + (row * a.heads + h) * IDX_LATENT_DIM;
-    for (int i = 0; i < 4; ++i) out[tid + i * kTile] = __float2bfloat16_rn(o[i] * inv);
-    if (a.lse != nullptr && tid == 0) a.lse[row * a.heads + h] = m == -INFINITY ? -INFINITY : m + logf(l);
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, box, one,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int N>
+cudaError_t launch_n(const Params& p, const CUtensorMap& pool, const CUtensorMap& ql, const CUtensorMap& qp, int ctas,
+                     cudaStream_t st) {
+    static std::atomic<unsigned long long> done{0};
+    cudaError_t e = set_smem_once(attend_kernel<N>, plan_of(N).total, done);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
+    cfg.blockDim = dim3(kAttThreads, 1, 1);
+    cfg.dynamicSmemBytes = plan_of(N).total;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    kt_mark(st);
+    e = cudaLaunchKernelEx(&cfg, attend_kernel<N>, pool, ql, qp, p);
+    kt_mark(st);
+    if (e != cudaSuccess || !p.split) return e;
+    cfg.gridDim = dim3(static_cast<unsigned>(p.rows), static_cast<unsigned>(p.heads), 1);
+    cfg.blockDim = dim3(128, 1, 1);
+    cfg.dynamicSmemBytes = 0;
+    kt_mark(st);
+    e = cudaLaunchKernelEx(&cfg, join_kernel, p, N, ctas);
+    kt_mark(st);
+    return e;
 }
 
 }  // namespace
 
-size_t attend_ws_bytes(int64_t, int, int64_t) { return 256; }
+size_t attend_ws_bytes(int64_t rows, int heads, int64_t max_keys) {
+    const Shape s = shape_of(rows, heads, max_keys);
+    if (!s.split) return 256;
+    return 256 + align_up(static_cast<size_t>(2) * s.ctas * s.N * (IDX_LATENT_DIM + 2) * 4, 256);
+}
 
-cudaError_t launch_attend(const AttendArgs& a, int sms, cudaStream_t st) {
-    (void)sms;
-    attend_kernel<<<dim3(static_cast<unsigned>(a.rows), a.heads, 1), kTile, 0, st>>>(a);
-    return cudaGetLastError();
+cudaError_t launch_attend(const AttendArgs& a, cudaStream_t st) {
+    EncodeTiledFn enc = encode_tiled_fn();
+    if (!enc) return cudaErrorNotSupported;
+    const Shape s = shape_of(a.rows, a.heads, a.max_keys);
+    Params p{};
+    p.slots = a.slots; p.slots_stride = a.slots_stride;
+    p.block_table = a.block_table; p.seq_lens = a.seq_lens; p.mbps = a.mbps; p.block_size = a.block_size;
+    p.rows = a.rows; p.num_slots = a.num_slots; p.heads = a.heads; p.hgs = s.hgs; p.max_keys = a.max_keys;
+    p.split = s.split;
+    p.scale_log2 = a.scale * 1.4426950408889634f;
+    p.out = static_cast<__nv_bfloat16*>(a.out); p.lse = a.lse; p.status = a.status;
+    p.part_o = static_cast<float*>(a.ws);
+    p.part_ml = reinterpret_cast<float2*>(p.part_o + static_cast<size_t>(2) * s.ctas * s.N * IDX_LATENT_DIM);
+    CUtensorMap pool, ql, qp;
+    cuuint64_t dims[2] = {IDX_LATENT_RECORD, static_cast<cuuint64_t>(a.num_slots)};
+    cuuint64_t strides[1] = {IDX_LATENT_RECORD * 2};
+    cuuint32_t box[2] = {64, 1}, one[2] = {1, 1};
+    if (enc(&pool, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(a.pool), dims, strides, box, one,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS ||
+        !query_map(&ql, enc, a.ql, IDX_LATENT_DIM, a.ql_row, a.ql_head, a.rows, a.heads, s.N, &p.ql_swap) ||
+        !query_map(&qp, enc, a.qp, IDX_LATENT_PE_DIM, a.qp_row, a.qp_head, a.rows, a.heads, s.N, &p.qp_swap))
+        return cudaErrorInvalidValue;
+    if (s.N == 16) return launch_n<16>(p, pool, ql, qp, s.ctas, st);
+    if (s.N == 32) return launch_n<32>(p, pool, ql, qp, s.ctas, st);
+    return launch_n<64>(p, pool, ql, qp, s.ctas, st);
 }
 
 }  // namespace dsaidx
