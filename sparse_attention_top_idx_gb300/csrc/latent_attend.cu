@@ -13,12 +13,14 @@
 // the scores, MN-major for the values.
 //
 // One persistent CTA an SM, warp-specialised:
-//   warp 0     gathers records, four rows a TMA instruction, into a ring of
-//              16 KB chunk pairs (128 latent dimensions of 64 keys) and one of
-//              position chunks; a masked key is a row outside the map: zeros
-//   warp 1     one lane issues every MMA; the scores of tile i + 1 run while
+//   warp 0     one lane issues every MMA; the scores of tile i + 1 run while
 //              tile i is in softmax
-//   warp 2     loads a row's queries
+//   warp 1     loads a row's queries
+//   warps 2-3  gather records, even and odd tiles, each into its own stage of
+//              four chunk pairs (128 latent dimensions of 64 keys) and a
+//              position chunk, with 16-byte asynchronous copies; masked keys
+//              are filled with zeros.  (TMA's row gather took 42 ns for four
+//              128-byte rows, 6.1 us a tile.)
 //   warps 4-7  softmax and epilogue
 // A chunk pair is freed by the value product that reads it last, so the next
 // tile's loads start while this tile's products run.
@@ -55,22 +57,22 @@ constexpr int kMaxCtas = 152;              // one an SM; CTAs never wait on one 
 constexpr float kNone = -3.0e38f;          // maximum of a head without a key so far
 constexpr float kGrow = 8.0f;              // log2 by which a score may pass the maximum
 
-// Shared memory: queries, weights, the pair ring, the position ring, then
-// masks, statistics and barriers.
+// Shared memory: queries, weights, two stages of chunk pairs, two position
+// chunks, then masks, statistics and barriers.
+constexpr int kPairs = 8;
 struct Plan {
-    int pairs, q_off, p_off, ring_off, pe_off, stat_off, mask_off, bar_off, total;
+    int q_off, p_off, ring_off, pe_off, stat_off, mask_off, bar_off, total;
 };
 __host__ __device__ constexpr Plan plan_of(int N) {
     Plan p{};
-    p.pairs = N == 64 ? 8 : N == 32 ? 10 : 11;
     int o = 0;
     p.q_off = o;    o += 9 * N * 128;
     p.p_off = o;    o += kChunk;
-    p.ring_off = o; o += p.pairs * kPair;
+    p.ring_off = o; o += kPairs * kPair;
     p.pe_off = o;   o += 2 * kChunk;
     p.stat_off = o; o += 5 * N * 4;        // four warps' values and one for all
     p.mask_off = o; o += 4 * 8;
-    p.bar_off = o;  o += (2 * p.pairs + 16) * 8 + 32;
+    p.bar_off = o;  o += (2 * kPairs + 16) * 8 + 32;
     p.total = o + 1024;
     return p;
 }
@@ -86,6 +88,7 @@ struct Params {
     int block_size, mbps, heads, hgs, max_keys;
     int split;                 // tiles of all rows in equal runs (else whole rows)
     int ql_swap, qp_swap;      // the map's middle dimension is the row
+    const uint8_t* pool;
     float scale_log2;
     __nv_bfloat16* out;
     float* lse;
@@ -192,7 +195,7 @@ struct Walk {
     }
 };
 
-// Slot of key j of a row; num_slots (a row of zeros) where it is masked.
+// Slot of key j of a row; num_slots where it is masked.
 __device__ __forceinline__ int key_slot(const Params& p, int64_t row, int keys, int j) {
     if (j >= keys) return static_cast<int>(p.num_slots);
     int64_t s;
@@ -212,10 +215,9 @@ __device__ __forceinline__ int key_slot(const Params& p, int64_t row, int keys, 
 
 template <int N>
 __global__ void __launch_bounds__(kAttThreads, 1)
-    attend_kernel(const __grid_constant__ CUtensorMap pool_map, const __grid_constant__ CUtensorMap ql_map,
-                  const __grid_constant__ CUtensorMap qp_map, const Params p) {
+    attend_kernel(const __grid_constant__ CUtensorMap ql_map, const __grid_constant__ CUtensorMap qp_map,
+                  const Params p) {
     constexpr Plan kPlan = plan_of(N);
-    constexpr int kPairs = kPlan.pairs;
     constexpr int kSPitch = N < 32 ? 32 : N;   // TMEM columns of a score buffer
     constexpr int kSCol = 4 * N;               // first column behind the accumulators
     extern __shared__ uint8_t smem_raw[];
@@ -241,10 +243,10 @@ __global__ void __launch_bounds__(kAttThreads, 1)
 
     if (warp == 0 && elect_one()) {
         for (int i = 0; i < kPairs; ++i) {
-            mbar_init(pair_full + i, 1);
+            mbar_init(pair_full + i, 32);
             mbar_init(pair_empty + i, 1);
         }
-        for (int i = 0; i < 6; ++i) mbar_init(pe_full + i, 1);
+        for (int i = 0; i < 6; ++i) mbar_init(pe_full + i, i < 2 ? 32 : 1);
         mbar_init(p_full, kSoftThreads);
         mbar_init(pv_done, 1);
         mbar_init(q_full, 1);
@@ -259,13 +261,12 @@ __global__ void __launch_bounds__(kAttThreads, 1)
         tmem_relinquish();
     }
     if (warp == 2 && elect_one()) {
-        tma_prefetch_desc(&pool_map);
         tma_prefetch_desc(&ql_map);
         tma_prefetch_desc(&qp_map);
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (warp == 3) {
+    if (warp == 2) {
         int64_t start, end, row = 0, base = 0;
         if (!p.split) {
             start = blockIdx.x;
@@ -297,64 +298,80 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     Walk walk(p, sh_run[0], sh_run[1], sh_run[2], sh_run[3]);
     Work w;
 
-    if (warp == 0) {
-        // ---- gather: lanes 0-15 take four keys each ----
-        uint32_t it = 0, pc = 0;      // tiles and chunk pairs issued
+    if (warp == 2 || warp == 3) {
+        // ---- gather: this warp's tiles into its stage ----
+        // A copy instruction moves 128 bytes of four keys: lane / 8 is the key
+        // among them, lane % 8 the 16-byte piece.
+        const uint32_t st = warp - 2;
+        const int sub = lane >> 3, piece = lane & 7;
+        const uint32_t in_row = sub * 128 + ((piece ^ sub) << 4);   // keys 4 k + sub, k even; odd: bit 2 of the row flips
+        const uint32_t pairs = smem_u32(smem + kPlan.ring_off) + st * 4 * kPair, pe = smem_u32(smem + kPlan.pe_off) + st * kChunk;
+        const int none = static_cast<int>(p.num_slots);
+        uint32_t it = 0, mine = 0;      // tiles passed, tiles loaded
         bool ok = true;
         while (ok && walk.next(p, w)) {
-            if (p.block_table != nullptr && w.keys == 0 && lane == 0 && __ldg(p.seq_lens + w.row) != 0)
+            if (p.block_table != nullptr && w.keys == 0 && lane == 0 && st == 0 && __ldg(p.seq_lens + w.row) != 0)
                 set_status(p.status, IDX_ERR_DEVICE_CHECK);
-            int4 s = make_int4(0, 0, 0, 0);
-            auto load = [&](int t) {
-                if (lane < 16) {
-                    const int j = t * kKeys + 4 * lane;
-                    s.x = key_slot(p, w.row, w.keys, j);
-                    s.y = key_slot(p, w.row, w.keys, j + 1);
-                    s.z = key_slot(p, w.row, w.keys, j + 2);
-                    s.w = key_slot(p, w.row, w.keys, j + 3);
-                }
-            };
-            load(w.t0);
-            for (int t = w.t0; t < w.t1 && ok; ++t, ++it) {
-                const int none = static_cast<int>(p.num_slots);
-                const uint32_t mine = lane < 16 ? (s.x != none) | (s.y != none) << 1 | (s.z != none) << 2 | (s.w != none) << 3 : 0;
-                uint32_t lo = lane < 8 ? mine << (4 * lane) : 0u, hi = lane >= 8 && lane < 16 ? mine << (4 * (lane - 8)) : 0u;
-                lo = __reduce_or_sync(~0u, lo);
-                hi = __reduce_or_sync(~0u, hi);
-                const int4 rows = s;
-                if (t + 1 < w.t1) load(t + 1);
-                ok = mbar_wait(pe_empty + (it & 1), ((it >> 1) & 1) ^ 1, p.status, abort_flag);
-                if (!__all_sync(~0u, ok)) { ok = false; break; }
-                uint8_t* pe = smem + kPlan.pe_off + (it & 1) * kChunk;
-                if (lane == 0) {
-                    masks[2 * (it & 3)] = lo;
-                    masks[2 * (it & 3) + 1] = hi;
-                    mbar_arrive_expect_tx(pe_full + (it & 1), kChunk);
-                }
-                __syncwarp();
-                if (lane < 16) tma_gather4(smem_u32(pe) + lane * 512, &pool_map, pe_full + (it & 1), IDX_LATENT_DIM, rows);
-                for (int m = 0; m < 4; ++m, ++pc) {
-                    const uint32_t sl = pc % kPairs;
-                    ok = mbar_wait(pair_empty + sl, ((pc / kPairs) & 1) ^ 1, p.status, abort_flag);
-                    if (!__all_sync(~0u, ok)) { ok = false; break; }
-                    if (lane == 0) mbar_arrive_expect_tx(pair_full + sl, kPair);
-                    __syncwarp();
-                    if (lane < 16) {
-                        const uint32_t dst = smem_u32(smem + kPlan.ring_off) + sl * kPair + lane * 512;
-                        tma_gather4(dst, &pool_map, pair_full + sl, 128 * m, rows);
-                        tma_gather4(dst + kChunk, &pool_map, pair_full + sl, 128 * m + 64, rows);
-                    }
-                }
+            int t = w.t0 + ((it ^ st) & 1);
+            int sa = none, sb = none;       // slots of keys lane and lane + 32
+            if (t < w.t1) {
+                sa = key_slot(p, w.row, w.keys, t * kKeys + lane);
+                sb = key_slot(p, w.row, w.keys, t * kKeys + 32 + lane);
             }
+            for (; t < w.t1; t += 2, ++mine) {
+                const uint32_t lo = __ballot_sync(~0u, sa != none), hi = __ballot_sync(~0u, sb != none);
+                const uint8_t* src[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    const int s = __shfl_sync(~0u, k < 8 ? sa : sb, (4 * k + sub) & 31);
+                    src[k] = s == none ? nullptr : p.pool + static_cast<int64_t>(s) * (IDX_LATENT_RECORD * 2) + 16 * piece;
+                }
+                if (t + 2 < w.t1) {
+                    sa = key_slot(p, w.row, w.keys, (t + 2) * kKeys + lane);
+                    sb = key_slot(p, w.row, w.keys, (t + 2) * kKeys + 32 + lane);
+                }
+                const uint32_t ti = it + (t - w.t0);
+                auto chunk = [&](uint32_t dst, int c) {
+#pragma unroll
+                    for (int k = 0; k < 16; ++k)
+                        copy16(dst + 512 * k + ((k & 1) ? in_row ^ 64u : in_row), src[k] ? src[k] + 128 * c : p.pool, src[k] ? 16 : 0);
+                };
+                ok = mbar_wait(pe_empty + st, (mine & 1) ^ 1, p.status, abort_flag);
+                if (!(ok = __all_sync(~0u, ok))) break;
+                if (lane == 0) {
+                    masks[2 * (ti & 3)] = lo;
+                    masks[2 * (ti & 3) + 1] = hi;
+                }
+                chunk(pe, 8);
+                copy_commit();
+                for (int m = 0; m < 4; ++m) {
+                    ok = mbar_wait(pair_empty + 4 * st + m, (mine & 1) ^ 1, p.status, abort_flag);
+                    if (!(ok = __all_sync(~0u, ok))) break;
+                    chunk(pairs + m * kPair, 2 * m);
+                    chunk(pairs + m * kPair + kChunk, 2 * m + 1);
+                    copy_commit();
+                }
+                if (!ok) break;
+                copy_wait<4>();
+                fence_proxy_async_smem();
+                mbar_arrive(pe_full + st);
+                copy_wait<3>();
+                fence_proxy_async_smem();
+                mbar_arrive(pair_full + 4 * st);
+                copy_wait<2>();
+                fence_proxy_async_smem();
+                mbar_arrive(pair_full + 4 * st + 1);
+                copy_wait<1>();
+                fence_proxy_async_smem();
+                mbar_arrive(pair_full + 4 * st + 2);
+                copy_wait<0>();
+                fence_proxy_async_smem();
+                mbar_arrive(pair_full + 4 * st + 3);
+            }
+            it += w.t1 - w.t0;
         }
-        if (!ok) {
-            // gave up: wait (bounded) for the copies in flight before leaving
-            for (uint32_t k = pc > kPairs ? pc - kPairs : 0; k < pc; ++k)
-                mbar_wait(pair_full + k % kPairs, (k / kPairs) & 1, p.status, nullptr);
-            for (uint32_t k = it > 2 ? it - 2 : 0; k <= it; ++k)
-                mbar_wait(pe_full + (k & 1), (k >> 1) & 1, p.status, nullptr);
-        }
-    } else if (warp == 1) {
+        copy_wait<0>();
+    } else if (warp == 0) {
         // ---- every MMA ----
         if (elect_one()) {
             constexpr uint32_t kIdS = idesc_bf16(64, N, false, false);
@@ -373,8 +390,8 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                              k != 0);
                 mma_commit(pe_empty + (i & 1));
                 for (int m = 0; m < 4; ++m) {
-                    const uint32_t pc = 4 * i + m, sl = pc % kPairs;
-                    if (!mbar_wait(pair_full + sl, (pc / kPairs) & 1, p.status, abort_flag)) return false;
+                    const uint32_t sl = 4 * (i & 1) + m;
+                    if (!mbar_wait(pair_full + sl, (i >> 1) & 1, p.status, abort_flag)) return false;
                     tc_fence_after();
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
@@ -397,7 +414,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                     if (t == w.t0 && !(ok = mbar_wait(o_empty, (item & 1) ^ 1, p.status, abort_flag))) break;
                     tc_fence_after();
                     for (int m = 0; m < 4; ++m) {
-                        const uint32_t sl = (4 * it + m) % kPairs;
+                        const uint32_t sl = 4 * (it & 1) + m;
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
                             mma_bf16(tmem + m * N, sdesc_mn_sw128(ring + sl * kPair + 2048 * k, kChunk),
@@ -412,7 +429,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
             mma_commit(drain);
             mbar_wait(drain, 0, p.status, nullptr);
         }
-    } else if (warp == 2) {
+    } else if (warp == 1) {
         // ---- queries ----
         if (elect_one()) {
             uint32_t item = 0;
@@ -730,8 +747,7 @@ bool query_map(CUtensorMap* map, EncodeTiledFn enc, const void* q, int dim, int6
 }
 
 template <int N>
-cudaError_t launch_n(const Params& p, const CUtensorMap& pool, const CUtensorMap& ql, const CUtensorMap& qp, int ctas,
-                     cudaStream_t st) {
+cudaError_t launch_n(const Params& p, const CUtensorMap& ql, const CUtensorMap& qp, int ctas, cudaStream_t st) {
     static std::atomic<unsigned long long> done{0};
     cudaError_t e = set_smem_once(attend_kernel<N>, plan_of(N).total, done);
     if (e != cudaSuccess) return e;
@@ -746,7 +762,7 @@ cudaError_t launch_n(const Params& p, const CUtensorMap& pool, const CUtensorMap
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     kt_mark(st);
-    e = cudaLaunchKernelEx(&cfg, attend_kernel<N>, pool, ql, qp, p);
+    e = cudaLaunchKernelEx(&cfg, attend_kernel<N>, ql, qp, p);
     kt_mark(st);
     if (e != cudaSuccess || !p.split) return e;
     cfg.gridDim = dim3(static_cast<unsigned>(p.rows), static_cast<unsigned>(p.heads), 1);
@@ -773,25 +789,20 @@ cudaError_t launch_attend(const AttendArgs& a, cudaStream_t st) {
     Params p{};
     p.slots = a.slots; p.slots_stride = a.slots_stride;
     p.block_table = a.block_table; p.seq_lens = a.seq_lens; p.mbps = a.mbps; p.block_size = a.block_size;
+    p.pool = static_cast<const uint8_t*>(a.pool);
     p.rows = a.rows; p.num_slots = a.num_slots; p.heads = a.heads; p.hgs = s.hgs; p.max_keys = a.max_keys;
     p.split = s.split;
     p.scale_log2 = a.scale * 1.4426950408889634f;
     p.out = static_cast<__nv_bfloat16*>(a.out); p.lse = a.lse; p.status = a.status;
     p.part_o = static_cast<float*>(a.ws);
     p.part_ml = reinterpret_cast<float2*>(p.part_o + static_cast<size_t>(2) * s.ctas * s.N * IDX_LATENT_DIM);
-    CUtensorMap pool, ql, qp;
-    cuuint64_t dims[2] = {IDX_LATENT_RECORD, static_cast<cuuint64_t>(a.num_slots)};
-    cuuint64_t strides[1] = {IDX_LATENT_RECORD * 2};
-    cuuint32_t box[2] = {64, 1}, one[2] = {1, 1};
-    if (enc(&pool, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(a.pool), dims, strides, box, one,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS ||
-        !query_map(&ql, enc, a.ql, IDX_LATENT_DIM, a.ql_row, a.ql_head, a.rows, a.heads, s.N, &p.ql_swap) ||
+    CUtensorMap ql, qp;
+    if (!query_map(&ql, enc, a.ql, IDX_LATENT_DIM, a.ql_row, a.ql_head, a.rows, a.heads, s.N, &p.ql_swap) ||
         !query_map(&qp, enc, a.qp, IDX_LATENT_PE_DIM, a.qp_row, a.qp_head, a.rows, a.heads, s.N, &p.qp_swap))
         return cudaErrorInvalidValue;
-    if (s.N == 16) return launch_n<16>(p, pool, ql, qp, s.ctas, st);
-    if (s.N == 32) return launch_n<32>(p, pool, ql, qp, s.ctas, st);
-    return launch_n<64>(p, pool, ql, qp, s.ctas, st);
+    if (s.N == 16) return launch_n<16>(p, ql, qp, s.ctas, st);
+    if (s.N == 32) return launch_n<32>(p, ql, qp, s.ctas, st);
+    return launch_n<64>(p, ql, qp, s.ctas, st);
 }
 
 }  // namespace dsaidx

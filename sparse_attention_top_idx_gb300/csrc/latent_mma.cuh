@@ -1,6 +1,6 @@
 // latent_mma.cuh -- what the attention kernels add to common.cuh: shared-memory
 // descriptors and instruction descriptors for operands stored with either
-// index contiguous, the row gather of TMA, TMEM stores and small helpers.
+// index contiguous, 16-byte copies, TMEM stores and small helpers.
 //
 // One tile format serves every operand: "chunks" of R rows of 128 bytes (64
 // bf16) with the 128-byte swizzle, 16-byte piece c of row r at c ^ (r & 7).  A
@@ -42,15 +42,17 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 
-// Four rows of a 2-D map (x: element in the row) to four consecutive 128-byte
-// rows of shared memory; a row index outside the map gives zeros.
-__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int x, int4 rows) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(rows.x), "r"(rows.y), "r"(rows.z), "r"(rows.w)
-        : "memory");
+// Asynchronous 16-byte copy to shared memory; zeros where bytes is 0 (src is
+// not read then).
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+
 __device__ __forceinline__ void tma_tile_3d(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
     asm volatile(
         "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
