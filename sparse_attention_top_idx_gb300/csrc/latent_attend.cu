@@ -16,12 +16,13 @@
 //   warp 0     one lane issues every MMA; the scores of tile i + 1 run while
 //              tile i is in softmax
 //   warp 1     loads a row's queries
-//   warps 2-3  gather records, even and odd tiles, each into its own stage of
-//              four chunk pairs (128 latent dimensions of 64 keys) and a
-//              position chunk, with 16-byte asynchronous copies; masked keys
-//              are filled with zeros.  (TMA's row gather took 42 ns for four
-//              128-byte rows, 6.1 us a tile.)
 //   warps 4-7  softmax and epilogue
+//   warps 8-11 gather records: two warps the even tiles, two the odd ones,
+//              each tile into its own stage of four chunk pairs (128 latent
+//              dimensions of 64 keys) and a position chunk, with 16-byte
+//              asynchronous copies; masked keys are filled with zeros.  (TMA's
+//              row gather took 42 ns for four 128-byte rows, 6.1 us a tile;
+//              one warp a stage 2.2 us, bound by its issue rate.)
 // A chunk pair is freed by the value product that reads it last, so the next
 // tile's loads start while this tile's products run.
 //
@@ -51,7 +52,7 @@ namespace {
 constexpr int kKeys = 64;                  // keys a tile
 constexpr int kChunk = kKeys * 128;        // bytes of a chunk: 64 keys x 64 values
 constexpr int kPair = 2 * kChunk;
-constexpr int kAttThreads = 256;
+constexpr int kAttThreads = 384;
 constexpr int kSoftThreads = 128;
 constexpr int kMaxCtas = 152;              // one an SM; CTAs never wait on one another
 constexpr float kNone = -3.0e38f;          // maximum of a head without a key so far
@@ -243,10 +244,10 @@ __global__ void __launch_bounds__(kAttThreads, 1)
 
     if (warp == 0 && elect_one()) {
         for (int i = 0; i < kPairs; ++i) {
-            mbar_init(pair_full + i, 32);
+            mbar_init(pair_full + i, 64);
             mbar_init(pair_empty + i, 1);
         }
-        for (int i = 0; i < 6; ++i) mbar_init(pe_full + i, i < 2 ? 32 : 1);
+        for (int i = 0; i < 6; ++i) mbar_init(pe_full + i, i < 2 ? 64 : 1);
         mbar_init(p_full, kSoftThreads);
         mbar_init(pv_done, 1);
         mbar_init(q_full, 1);
@@ -298,50 +299,48 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     Walk walk(p, sh_run[0], sh_run[1], sh_run[2], sh_run[3]);
     Work w;
 
-    if (warp == 2 || warp == 3) {
-        // ---- gather: this warp's tiles into its stage ----
+    if (warp >= 8) {
+        // ---- gather: 32 keys of every other tile, into its stage ----
         // A copy instruction moves 128 bytes of four keys: lane / 8 is the key
         // among them, lane % 8 the 16-byte piece.
-        const uint32_t st = warp - 2;
+        const uint32_t st = (warp - 8) >> 1, half = warp & 1;
         const int sub = lane >> 3, piece = lane & 7;
-        const uint32_t in_row = sub * 128 + ((piece ^ sub) << 4);   // keys 4 k + sub, k even; odd: bit 2 of the row flips
+        const uint32_t in_row = half * 4096 + sub * 128 + ((piece ^ sub) << 4);   // of keys 4 k + sub, k even; k odd: ^ 64
         const uint32_t pairs = smem_u32(smem + kPlan.ring_off) + st * 4 * kPair, pe = smem_u32(smem + kPlan.pe_off) + st * kChunk;
         const int none = static_cast<int>(p.num_slots);
         uint32_t it = 0, mine = 0;      // tiles passed, tiles loaded
         bool ok = true;
         while (ok && walk.next(p, w)) {
-            if (p.block_table != nullptr && w.keys == 0 && lane == 0 && st == 0 && __ldg(p.seq_lens + w.row) != 0)
+            if (p.block_table != nullptr && w.keys == 0 && lane == 0 && __ldg(p.seq_lens + w.row) != 0)
                 set_status(p.status, IDX_ERR_DEVICE_CHECK);
             int t = w.t0 + ((it ^ st) & 1);
-            int sa = none, sb = none;       // slots of keys lane and lane + 32
-            if (t < w.t1) {
-                sa = key_slot(p, w.row, w.keys, t * kKeys + lane);
-                sb = key_slot(p, w.row, w.keys, t * kKeys + 32 + lane);
-            }
+            const int j = 32 * half + lane;
+            int slot = t < w.t1 ? key_slot(p, w.row, w.keys, t * kKeys + j) : none;
             for (; t < w.t1; t += 2, ++mine) {
-                const uint32_t lo = __ballot_sync(~0u, sa != none), hi = __ballot_sync(~0u, sb != none);
-                const uint8_t* src[16];
+                const uint32_t valid = __ballot_sync(~0u, slot != none);
+                const uint8_t* src[8];
 #pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                    const int s = __shfl_sync(~0u, k < 8 ? sa : sb, (4 * k + sub) & 31);
-                    src[k] = s == none ? nullptr : p.pool + static_cast<int64_t>(s) * (IDX_LATENT_RECORD * 2) + 16 * piece;
+                for (int k = 0; k < 8; ++k) {
+                    const int s = __shfl_sync(~0u, slot, 4 * k + sub);
+                    src[k] = p.pool + static_cast<int64_t>(s == none ? 0 : s) * (IDX_LATENT_RECORD * 2) + 16 * piece;
                 }
-                if (t + 2 < w.t1) {
-                    sa = key_slot(p, w.row, w.keys, (t + 2) * kKeys + lane);
-                    sb = key_slot(p, w.row, w.keys, (t + 2) * kKeys + 32 + lane);
-                }
+                if (t + 2 < w.t1) slot = key_slot(p, w.row, w.keys, (t + 2) * kKeys + j);
                 const uint32_t ti = it + (t - w.t0);
                 auto chunk = [&](uint32_t dst, int c) {
+                    const uint32_t even = dst + in_row, odd = dst + (in_row ^ 64u);
+                    if (valid == ~0u) {
 #pragma unroll
-                    for (int k = 0; k < 16; ++k)
-                        copy16(dst + 512 * k + ((k & 1) ? in_row ^ 64u : in_row), src[k] ? src[k] + 128 * c : p.pool, src[k] ? 16 : 0);
+                        for (int k = 0; k < 8; ++k) copy16(((k & 1) ? odd : even) + 512 * k, src[k] + 128 * c);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            copy16_or_zero(((k & 1) ? odd : even) + 512 * k, src[k] + 128 * c,
+                                           (valid >> (4 * k + sub)) & 1 ? 16 : 0);
+                    }
                 };
                 ok = mbar_wait(pe_empty + st, (mine & 1) ^ 1, p.status, abort_flag);
                 if (!(ok = __all_sync(~0u, ok))) break;
-                if (lane == 0) {
-                    masks[2 * (ti & 3)] = lo;
-                    masks[2 * (ti & 3) + 1] = hi;
-                }
+                if (lane == 0) masks[2 * (ti & 3) + half] = valid;
                 chunk(pe, 8);
                 copy_commit();
                 for (int m = 0; m < 4; ++m) {
@@ -447,7 +446,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
             }
             if (item) mbar_wait(q_full, (item - 1) & 1, p.status, nullptr);
         }
-    } else if (warp >= 4) {
+    } else if (warp >= 4 && warp < 8) {
         // ---- softmax and epilogue ----
         const int sw = warp - 4;
         const int tid = threadIdx.x - 128;

@@ -42,9 +42,12 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 
-// Asynchronous 16-byte copy to shared memory; zeros where bytes is 0 (src is
-// not read then).
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t bytes) {
+// Asynchronous 16-byte copy to shared memory; the second form writes zeros
+// where bytes is 0 (src is not read then).
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy16_or_zero(uint32_t dst, const void* src, uint32_t bytes) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
