@@ -13,16 +13,17 @@
 // the scores, MN-major for the values.
 //
 // One persistent CTA an SM, warp-specialised:
-//   warp 0     one lane issues every MMA; the scores of tile i + 1 run while
-//              tile i is in softmax
+//   warp 0     one lane issues every MMA.  The scores of tile i + 1 run while
+//              tile i is in softmax; while their records have not landed, the
+//              value product of tile i is issued as soon as its weights are
+//              there, which frees its records early
 //   warp 1     loads a row's queries
 //   warps 4-7  softmax and epilogue
-//   warps 8-11 gather records: two warps the even tiles, two the odd ones,
-//              each tile into its own stage of four chunk pairs (128 latent
-//              dimensions of 64 keys) and a position chunk, with 16-byte
-//              asynchronous copies; masked keys are filled with zeros.  (TMA's
-//              row gather took 42 ns for four 128-byte rows, 6.1 us a tile;
-//              one warp a stage 2.2 us, bound by its issue rate.)
+//   warps 8-11 gather records, 16 keys of every tile each, with 16-byte
+//              asynchronous copies into a ring of chunk pairs (128 latent
+//              dimensions of 64 keys) and one of position chunks; masked keys
+//              are filled with zeros.  (TMA's row gather took 42 ns for four
+//              128-byte rows, 6.1 us a tile.)
 // A chunk pair is freed by the value product that reads it last, so the next
 // tile's loads start while this tile's products run.
 //
@@ -54,26 +55,27 @@ constexpr int kChunk = kKeys * 128;        // bytes of a chunk: 64 keys x 64 val
 constexpr int kPair = 2 * kChunk;
 constexpr int kAttThreads = 384;
 constexpr int kSoftThreads = 128;
+constexpr int kGatherThreads = 128;
 constexpr int kMaxCtas = 152;              // one an SM; CTAs never wait on one another
 constexpr float kNone = -3.0e38f;          // maximum of a head without a key so far
 constexpr float kGrow = 8.0f;              // log2 by which a score may pass the maximum
 
-// Shared memory: queries, weights, two stages of chunk pairs, two position
-// chunks, then masks, statistics and barriers.
-constexpr int kPairs = 8;
+// Shared memory: queries, weights, the pair ring, two position chunks, then
+// masks, statistics and barriers.
 struct Plan {
-    int q_off, p_off, ring_off, pe_off, stat_off, mask_off, bar_off, total;
+    int pairs, q_off, p_off, ring_off, pe_off, stat_off, mask_off, bar_off, total;
 };
 __host__ __device__ constexpr Plan plan_of(int N) {
     Plan p{};
+    p.pairs = N == 64 ? 8 : N == 32 ? 10 : 11;   // a tile takes four
     int o = 0;
     p.q_off = o;    o += 9 * N * 128;
     p.p_off = o;    o += kChunk;
-    p.ring_off = o; o += kPairs * kPair;
+    p.ring_off = o; o += p.pairs * kPair;
     p.pe_off = o;   o += 2 * kChunk;
     p.stat_off = o; o += 5 * N * 4;        // four warps' values and one for all
     p.mask_off = o; o += 4 * 8;
-    p.bar_off = o;  o += (2 * kPairs + 16) * 8 + 32;
+    p.bar_off = o;  o += (2 * p.pairs + 16) * 8 + 32;
     p.total = o + 1024;
     return p;
 }
@@ -219,6 +221,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     attend_kernel(const __grid_constant__ CUtensorMap ql_map, const __grid_constant__ CUtensorMap qp_map,
                   const Params p) {
     constexpr Plan kPlan = plan_of(N);
+    constexpr int kPairs = kPlan.pairs;
     constexpr int kSPitch = N < 32 ? 32 : N;   // TMEM columns of a score buffer
     constexpr int kSCol = 4 * N;               // first column behind the accumulators
     extern __shared__ uint8_t smem_raw[];
@@ -238,16 +241,16 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     int64_t* sh_run = reinterpret_cast<int64_t*>(pe_full + 12);   // start, end, row, base
     uint32_t* sh_tmem = reinterpret_cast<uint32_t*>(pe_full + 16);
     int* sh_abort = reinterpret_cast<int*>(sh_tmem + 1);
-    uint32_t* masks = reinterpret_cast<uint32_t*>(smem + kPlan.mask_off);   // [4][2]
+    uint16_t* masks = reinterpret_cast<uint16_t*>(smem + kPlan.mask_off);   // [4 tiles][4]: 16 keys each
     float* stat = reinterpret_cast<float*>(smem + kPlan.stat_off);          // [5][N]
     const int warp = warp_id(), lane = lane_id();
 
     if (warp == 0 && elect_one()) {
         for (int i = 0; i < kPairs; ++i) {
-            mbar_init(pair_full + i, 64);
+            mbar_init(pair_full + i, kGatherThreads);
             mbar_init(pair_empty + i, 1);
         }
-        for (int i = 0; i < 6; ++i) mbar_init(pe_full + i, i < 2 ? 64 : 1);
+        for (int i = 0; i < 6; ++i) mbar_init(pe_full + i, i < 2 ? kGatherThreads + 4 : 1);
         mbar_init(p_full, kSoftThreads);
         mbar_init(pv_done, 1);
         mbar_init(q_full, 1);
@@ -300,76 +303,61 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     Work w;
 
     if (warp >= 8) {
-        // ---- gather: 32 keys of every other tile, into its stage ----
+        // ---- gather: 16 keys of every tile ----
         // A copy instruction moves 128 bytes of four keys: lane / 8 is the key
         // among them, lane % 8 the 16-byte piece.
-        const uint32_t st = (warp - 8) >> 1, half = warp & 1;
-        const int sub = lane >> 3, piece = lane & 7;
-        const uint32_t in_row = half * 4096 + sub * 128 + ((piece ^ sub) << 4);   // of keys 4 k + sub, k even; k odd: ^ 64
-        const uint32_t pairs = smem_u32(smem + kPlan.ring_off) + st * 4 * kPair, pe = smem_u32(smem + kPlan.pe_off) + st * kChunk;
-        const int none = static_cast<int>(p.num_slots);
-        uint32_t it = 0, mine = 0;      // tiles passed, tiles loaded
+        const int wq = warp - 8, sub = lane >> 3, piece = lane & 7;
+        const uint32_t even = wq * 2048 + sub * 128 + ((piece ^ sub) << 4), odd = even ^ 64u;   // keys 4 k + sub by k
+        const uint32_t ring = smem_u32(smem + kPlan.ring_off), pe = smem_u32(smem + kPlan.pe_off);
+        const int none = static_cast<int>(p.num_slots), j = 16 * wq + (lane & 15);
+        uint32_t it = 0, sl = 0, ph = 1;      // tiles, ring slot and the parity that frees it
         bool ok = true;
         while (ok && walk.next(p, w)) {
             if (p.block_table != nullptr && w.keys == 0 && lane == 0 && __ldg(p.seq_lens + w.row) != 0)
                 set_status(p.status, IDX_ERR_DEVICE_CHECK);
-            int t = w.t0 + ((it ^ st) & 1);
-            const int j = 32 * half + lane;
-            int slot = t < w.t1 ? key_slot(p, w.row, w.keys, t * kKeys + j) : none;
-            for (; t < w.t1; t += 2, ++mine) {
-                const uint32_t valid = __ballot_sync(~0u, slot != none);
-                const uint8_t* src[8];
+            int slot = key_slot(p, w.row, w.keys, w.t0 * kKeys + j);
+            for (int t = w.t0; t < w.t1; ++t, ++it) {
+                const uint32_t valid = __ballot_sync(~0u, slot != none) & 0xFFFFu;
+                const uint8_t* src[4];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
+                for (int k = 0; k < 4; ++k) {
                     const int s = __shfl_sync(~0u, slot, 4 * k + sub);
                     src[k] = p.pool + static_cast<int64_t>(s == none ? 0 : s) * (IDX_LATENT_RECORD * 2) + 16 * piece;
                 }
-                if (t + 2 < w.t1) slot = key_slot(p, w.row, w.keys, (t + 2) * kKeys + j);
-                const uint32_t ti = it + (t - w.t0);
+                if (t + 1 < w.t1) slot = key_slot(p, w.row, w.keys, (t + 1) * kKeys + j);
                 auto chunk = [&](uint32_t dst, int c) {
-                    const uint32_t even = dst + in_row, odd = dst + (in_row ^ 64u);
-                    if (valid == ~0u) {
+                    if (valid == 0xFFFFu) {
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) copy16(((k & 1) ? odd : even) + 512 * k, src[k] + 128 * c);
+                        for (int k = 0; k < 4; ++k) copy16(dst + ((k & 1) ? odd : even) + 512 * k, src[k] + 128 * c);
                     } else {
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            copy16_or_zero(((k & 1) ? odd : even) + 512 * k, src[k] + 128 * c,
+                        for (int k = 0; k < 4; ++k)
+                            copy16_or_zero(dst + ((k & 1) ? odd : even) + 512 * k, src[k] + 128 * c,
                                            (valid >> (4 * k + sub)) & 1 ? 16 : 0);
                     }
                 };
-                ok = mbar_wait(pe_empty + st, (mine & 1) ^ 1, p.status, abort_flag);
+                ok = mbar_wait(pe_empty + (it & 1), ((it >> 1) & 1) ^ 1, p.status, abort_flag);
                 if (!(ok = __all_sync(~0u, ok))) break;
-                if (lane == 0) masks[2 * (ti & 3) + half] = valid;
-                chunk(pe, 8);
-                copy_commit();
+                chunk(pe + (it & 1) * kChunk, 8);
+                copy_arrive(pe_full + (it & 1));
+                if (lane == 0) {
+                    masks[4 * (it & 3) + wq] = static_cast<uint16_t>(valid);
+                    mbar_arrive(pe_full + (it & 1));
+                }
+#pragma unroll 1
                 for (int m = 0; m < 4; ++m) {
-                    ok = mbar_wait(pair_empty + 4 * st + m, (mine & 1) ^ 1, p.status, abort_flag);
+                    ok = mbar_wait(pair_empty + sl, ph, p.status, abort_flag);
                     if (!(ok = __all_sync(~0u, ok))) break;
-                    chunk(pairs + m * kPair, 2 * m);
-                    chunk(pairs + m * kPair + kChunk, 2 * m + 1);
-                    copy_commit();
+                    const uint32_t dst = ring + sl * kPair;
+                    chunk(dst, 2 * m);
+                    chunk(dst + kChunk, 2 * m + 1);
+                    copy_arrive(pair_full + sl);
+                    if (++sl == kPairs) sl = 0, ph ^= 1;
                 }
                 if (!ok) break;
-                copy_wait<4>();
-                fence_proxy_async_smem();
-                mbar_arrive(pe_full + st);
-                copy_wait<3>();
-                fence_proxy_async_smem();
-                mbar_arrive(pair_full + 4 * st);
-                copy_wait<2>();
-                fence_proxy_async_smem();
-                mbar_arrive(pair_full + 4 * st + 1);
-                copy_wait<1>();
-                fence_proxy_async_smem();
-                mbar_arrive(pair_full + 4 * st + 2);
-                copy_wait<0>();
-                fence_proxy_async_smem();
-                mbar_arrive(pair_full + 4 * st + 3);
             }
-            it += w.t1 - w.t0;
         }
-        copy_wait<0>();
+        copy_wait_all();
     } else if (warp == 0) {
         // ---- every MMA ----
         if (elect_one()) {
@@ -377,53 +365,83 @@ __global__ void __launch_bounds__(kAttThreads, 1)
             constexpr uint32_t kIdO = idesc_bf16(128, N, true, true);
             const uint32_t q_addr = smem_u32(smem + kPlan.q_off), ring = smem_u32(smem + kPlan.ring_off);
             const uint32_t pe_addr = smem_u32(smem + kPlan.pe_off), p_addr = smem_u32(smem + kPlan.p_off);
-            uint32_t it = 0, item = 0;      // tiles whose scores were issued, pieces
-            bool ok = true;
-            auto scores = [&](uint32_t i) -> bool {
-                const uint32_t d = tmem + kSCol + (i & 1) * kSPitch;
-                if (!mbar_wait(pe_full + (i & 1), (i >> 1) & 1, p.status, abort_flag)) return false;
+            uint32_t it = 0, item = 0;                    // tile and piece of the score products
+            uint32_t s_sl = 0, s_ph = 0, v_sl = 0;        // ring position of the score and the value products
+            bool ok = true, pending = false, v_first = false;   // the value product of tile v_it is still to be issued
+            uint32_t v_it = 0, v_item = 0;
+            auto values = [&]() {
                 tc_fence_after();
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    mma_bf16(d, sdesc_sw128(pe_addr + (i & 1) * kChunk + 32 * k), sdesc_sw128(q_addr + 8 * N * 128 + 32 * k), kIdS,
-                             k != 0);
-                mma_commit(pe_empty + (i & 1));
+#pragma unroll 1
                 for (int m = 0; m < 4; ++m) {
-                    const uint32_t sl = 4 * (i & 1) + m;
-                    if (!mbar_wait(pair_full + sl, (i >> 1) & 1, p.status, abort_flag)) return false;
-                    tc_fence_after();
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        mma_bf16(d, sdesc_sw128(ring + sl * kPair + (k >> 2) * kChunk + 32 * (k & 3)),
-                                 sdesc_sw128(q_addr + (2 * m + (k >> 2)) * N * 128 + 32 * (k & 3)), kIdS, 1u);
+                    for (int k = 0; k < 4; ++k)
+                        mma_bf16(tmem + m * N, sdesc_mn_sw128(ring + v_sl * kPair + 2048 * k, kChunk),
+                                 sdesc_mn_sw128(p_addr + 2048 * k, kChunk), kIdO, (!v_first || k != 0) ? 1u : 0u);
+                    mma_commit(pair_empty + v_sl);
+                    if (++v_sl == kPairs) v_sl = 0;
                 }
-                mma_commit(s_full + (i & 1));
+                mma_commit(pv_done);
+                pending = false;
+            };
+            // the weights are there, and the accumulators of the piece before were read
+            auto finish_values = [&]() -> bool {
+                if (!pending) return true;
+                if (!mbar_wait(p_full, v_it & 1, p.status, abort_flag)) return false;
+                if (v_first && !mbar_wait(o_empty, (v_item & 1) ^ 1, p.status, abort_flag)) return false;
+                values();
                 return true;
             };
+            // wait for operands of a score product; value products pass it
+            auto wait_operand = [&](uint64_t* b, uint32_t parity) -> bool {
+                unsigned long long since = 0;
+                for (uint32_t n = 1; pending && !mbar_test(b, parity); ++n) {
+                    if (mbar_test(p_full, v_it & 1) && (!v_first || mbar_test(o_empty, (v_item & 1) ^ 1))) values();
+                    if ((n & 1023u) == 0) {
+                        if (*abort_flag) return false;
+                        const unsigned long long now = global_timer_ns();
+                        if (since == 0) since = now;
+                        if (now - since > kWaitLimitNs) break;   // the wait below ends it
+                    }
+                }
+                return mbar_wait(b, parity, p.status, abort_flag);
+            };
             while (ok && walk.next(p, w)) {
-                ok = mbar_wait(q_full, item & 1, p.status, abort_flag) && scores(it);
-                if (!ok) break;
-                if (w.t1 - w.t0 == 1) mma_commit(q_empty);
+                if (!(ok = wait_operand(q_full, item & 1))) break;
                 for (int t = w.t0; t < w.t1; ++t, ++it) {
-                    if (t + 1 < w.t1) {
-                        if (!(ok = scores(it + 1))) break;
-                        if (t + 2 == w.t1) mma_commit(q_empty);
-                    }
-                    if (!(ok = mbar_wait(p_full, it & 1, p.status, abort_flag))) break;
-                    if (t == w.t0 && !(ok = mbar_wait(o_empty, (item & 1) ^ 1, p.status, abort_flag))) break;
+                    const uint32_t d = tmem + kSCol + (it & 1) * kSPitch;
+                    if (!(ok = wait_operand(pe_full + (it & 1), (it >> 1) & 1))) break;
+                    // the records were copied by other threads: order their
+                    // writes before the tensor core's reads
+                    fence_proxy_async_smem();
                     tc_fence_after();
-                    for (int m = 0; m < 4; ++m) {
-                        const uint32_t sl = 4 * (it & 1) + m;
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            mma_bf16(tmem + m * N, sdesc_mn_sw128(ring + sl * kPair + 2048 * k, kChunk),
-                                     sdesc_mn_sw128(p_addr + 2048 * k, kChunk), kIdO, (t != w.t0 || k != 0) ? 1u : 0u);
-                        mma_commit(pair_empty + sl);
+                    for (int k = 0; k < 4; ++k)
+                        mma_bf16(d, sdesc_sw128(pe_addr + (it & 1) * kChunk + 32 * k),
+                                 sdesc_sw128(q_addr + 8 * N * 128 + 32 * k), kIdS, k != 0);
+                    mma_commit(pe_empty + (it & 1));
+#pragma unroll 1
+                    for (int m = 0; m < 4; ++m) {
+                        if (!(ok = wait_operand(pair_full + s_sl, s_ph))) break;
+                        fence_proxy_async_smem();
+                        tc_fence_after();
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            mma_bf16(d, sdesc_sw128(ring + s_sl * kPair + (k >> 2) * kChunk + 32 * (k & 3)),
+                                     sdesc_sw128(q_addr + (2 * m + (k >> 2)) * N * 128 + 32 * (k & 3)), kIdS, 1u);
+                        if (++s_sl == kPairs) s_sl = 0, s_ph ^= 1;
                     }
-                    mma_commit(pv_done);
+                    if (!ok) break;
+                    mma_commit(s_full + (it & 1));
+                    if (t + 1 == w.t1) mma_commit(q_empty);
+                    if (!(ok = finish_values())) break;
+                    pending = true;
+                    v_first = t == w.t0;
+                    v_it = it;
+                    v_item = item;
                 }
                 ++item;
             }
+            if (ok) finish_values();
             // nothing of this CTA may run on when its shared memory and TMEM go
             mma_commit(drain);
             mbar_wait(drain, 0, p.status, nullptr);
@@ -470,7 +488,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
 #pragma unroll
                 for (int g = 0; g < (kR < 4 ? 1 : kR / 4); ++g)
                     tmem_ld_16x256b_x4(tmem + lanes + kSCol + (it & 1) * kSPitch + 32 * g, raw[g]);
-                const uint32_t mask = masks[2 * (it & 3) + (sw >> 1)] >> (16 * (sw & 1));
+                const uint32_t mask = masks[4 * (it & 3) + sw];
                 const bool va = (mask >> kr) & 1, vb = (mask >> (kr + 8)) & 1;
 #pragma unroll
                 for (int g = 0; g < (kR < 4 ? 1 : kR / 4); ++g) tmem_wait_ld16(raw[g]);
