@@ -606,27 +606,41 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                 stat[4 * N + tid] = w.slot >= 0 ? 1.0f : l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
             }
             named_sync<1, kSoftThreads>();
-            // lane = latent dimension, column = head
-            for (int c = 0; c < 4 * N; c += 16) {
-                uint32_t v[16];
-                tmem_ld16_nowait(tmem + lanes + c, v);
-                tmem_wait_ld16(v);
-                const int m = c / N, hc = c & (N - 1), d = 128 * m + 32 * sw + lane;
-                if (w.slot >= 0) {
-                    float* dst = p.part_o + (static_cast<int64_t>(w.slot) * N + hc) * IDX_LATENT_DIM + d;
+            // lane = latent dimension, column = head: 16 heads at a time, the
+            // four groups of 128 dimensions in flight together
+#pragma unroll 1
+            for (int hc = 0; hc < N; hc += 16) {
+                uint32_t v[4][16];
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) dst[j * IDX_LATENT_DIM] = __uint_as_float(v[j]);
-                } else {
-                    // neighbouring lanes swap so that each stores two dimensions of one head
-                    const bool odd = lane & 1;
-                    __nv_bfloat16* dst = p.out + (w.row * p.heads + h0 + hc + odd) * IDX_LATENT_DIM + (d & ~1);
+                for (int m = 0; m < 4; ++m) tmem_ld16_nowait(tmem + lanes + m * N + hc, v[m]);
+                const int d0 = 32 * sw + lane;
+                if (w.slot >= 0) {
+                    float* dst = p.part_o + (static_cast<int64_t>(w.slot) * N + hc) * IDX_LATENT_DIM + d0;
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) {
+                        tmem_wait_ld16(v[m]);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) dst[j * IDX_LATENT_DIM + 128 * m] = __uint_as_float(v[m][j]);
+                    }
+                    continue;
+                }
+                float f[16];
+#pragma unroll
+                for (int j = 0; j < 16; j += 4)
+                    *reinterpret_cast<float4*>(f + j) = *reinterpret_cast<const float4*>(stat + 4 * N + hc + j);
+                // neighbouring lanes swap so that each stores two dimensions of one head
+                const bool odd = lane & 1;
+                const int left = p.heads - h0 - hc - odd;      // heads from this lane's first one on
+                __nv_bfloat16* dst = p.out + (w.row * p.heads + h0 + hc + odd) * IDX_LATENT_DIM + (d0 & ~1);
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    tmem_wait_ld16(v[m]);
 #pragma unroll
                     for (int j = 0; j < 16; j += 2) {
-                        const float a = __uint_as_float(v[j]) * stat[4 * N + hc + j];
-                        const float b = __uint_as_float(v[j + 1]) * stat[4 * N + hc + j + 1];
+                        const float a = __uint_as_float(v[m][j]) * f[j], b = __uint_as_float(v[m][j + 1]) * f[j + 1];
                         const float o = __shfl_xor_sync(~0u, odd ? a : b, 1);
-                        if (h0 + hc + j + odd < p.heads)
-                            *reinterpret_cast<uint32_t*>(dst + j * IDX_LATENT_DIM) = odd ? bf16x2(o, b) : bf16x2(a, o);
+                        const uint32_t two = odd ? bf16x2(o, b) : bf16x2(a, o);
+                        if (j < left) *reinterpret_cast<uint32_t*>(dst + j * IDX_LATENT_DIM + 128 * m) = two;
                     }
                 }
             }
