@@ -40,10 +40,10 @@
 #include <cuda_bf16.h>
 
 #include <cmath>
-#include <utility>
 
 #include "internal.h"
 #include "latent.h"
+#include "latent_map.h"
 #include "latent_mma.cuh"
 
 namespace dsaidx {
@@ -758,25 +758,6 @@ Shape shape_of(int64_t rows, int heads, int64_t max_keys) {
     return s;
 }
 
-// Query map: [values, heads, rows] with the smaller stride first.
-bool query_map(CUtensorMap* map, EncodeTiledFn enc, const void* q, int dim, int64_t row_stride, int64_t head_stride,
-               int64_t rows, int heads, int N, int* swap) {
-    if (heads == 1) head_stride = dim;             // strides nobody steps over
-    if (rows == 1) row_stride = head_stride * heads;
-    *swap = head_stride > row_stride;
-    cuuint64_t dims[3] = {static_cast<cuuint64_t>(dim), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(rows)};
-    cuuint64_t strides[2] = {static_cast<cuuint64_t>(head_stride) * 2, static_cast<cuuint64_t>(row_stride) * 2};
-    cuuint32_t box[3] = {64, static_cast<cuuint32_t>(N), 1}, one[3] = {1, 1, 1};
-    if (*swap) {
-        std::swap(dims[1], dims[2]);
-        std::swap(strides[0], strides[1]);
-        std::swap(box[1], box[2]);
-    }
-    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, box, one,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int N>
 cudaError_t launch_n(const Params& p, const CUtensorMap& ql, const CUtensorMap& qp, int ctas, cudaStream_t st) {
     static std::atomic<unsigned long long> done{0};
@@ -828,8 +809,8 @@ cudaError_t launch_attend(const AttendArgs& a, cudaStream_t st) {
     p.part_o = static_cast<float*>(a.ws);
     p.part_ml = reinterpret_cast<float2*>(p.part_o + static_cast<size_t>(2) * s.ctas * s.N * IDX_LATENT_DIM);
     CUtensorMap ql, qp;
-    if (!query_map(&ql, enc, a.ql, IDX_LATENT_DIM, a.ql_row, a.ql_head, a.rows, a.heads, s.N, &p.ql_swap) ||
-        !query_map(&qp, enc, a.qp, IDX_LATENT_PE_DIM, a.qp_row, a.qp_head, a.rows, a.heads, s.N, &p.qp_swap))
+    if (!head_map(&ql, enc, a.ql, IDX_LATENT_DIM, a.ql_row, a.ql_head, a.rows, a.heads, s.N, 1, &p.ql_swap) ||
+        !head_map(&qp, enc, a.qp, IDX_LATENT_PE_DIM, a.qp_row, a.qp_head, a.rows, a.heads, s.N, 1, &p.qp_swap))
         return cudaErrorInvalidValue;
     if (s.N == 16) return launch_n<16>(p, ql, qp, s.ctas, st);
     if (s.N == 32) return launch_n<32>(p, ql, qp, s.ctas, st);
