@@ -15,11 +15,16 @@ bool mult8(int64_t s) { return s % 8 == 0; }
 
 constexpr int64_t kInt31 = int64_t(1) << 31;
 
-// Number of SMs of the current device.
+// Number of SMs of the current device, asked for once a device.
 bool sm_count(int* sms) {
+    static std::atomic<int> known[64];
     int dev = 0;
-    return cudaGetDevice(&dev) == cudaSuccess &&
-           cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    const bool kept = dev >= 0 && dev < 64;
+    if (kept && (*sms = known[dev].load(std::memory_order_relaxed)) > 0) return true;
+    if (cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return false;
+    if (kept) known[dev].store(*sms, std::memory_order_relaxed);
+    return true;
 }
 
 bool pool_ok(const idx_latent_pool* p) {

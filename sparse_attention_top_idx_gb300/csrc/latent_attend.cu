@@ -14,9 +14,9 @@
 //
 // One persistent CTA an SM, warp-specialised:
 //   warp 0     one lane issues every MMA.  The scores of tile i + 1 run while
-//              tile i is in softmax; while their records have not landed, the
-//              value product of tile i is issued as soon as its weights are
-//              there, which frees its records early
+//              tile i is in softmax; between their steps the value product of
+//              tile i is issued as soon as its weights are there, which frees
+//              its records early
 //   warp 1     loads a row's queries
 //   warps 4-7  softmax and epilogue
 //   warps 8-11 gather records, 16 keys of every tile each, with 16-byte
@@ -394,8 +394,9 @@ __global__ void __launch_bounds__(kAttThreads, 1)
             // wait for operands of a score product; value products pass it
             auto wait_operand = [&](uint64_t* b, uint32_t parity) -> bool {
                 unsigned long long since = 0;
-                for (uint32_t n = 1; pending && !mbar_test(b, parity); ++n) {
+                for (uint32_t n = 1; pending; ++n) {
                     if (mbar_test(p_full, v_it & 1) && (!v_first || mbar_test(o_empty, (v_item & 1) ^ 1))) values();
+                    if (mbar_test(b, parity)) return true;
                     if ((n & 1023u) == 0) {
                         if (*abort_flag) return false;
                         const unsigned long long now = global_timer_ns();

@@ -1,13 +1,14 @@
 // rope.cu -- idx_rope: rotary positions on part of every head.
 //
-// Bound by memory: each element is read and written once.  A CTA takes a run
-// of (token, head) rows, computes the cosines and sines of the tokens it spans
-// once into shared memory (one integer multiply and one sincospi a pair,
-// shared by all heads of a token) and turns the rows with up to 16-byte
-// accesses, kRows rows in flight a thread.  Block shape: x covers the work
-// items of one row (a vector of kVec elements; with pairs half a head apart,
-// a vector and its partner together, so that a turn in place has one owner),
-// y the rows, so only the token of a row takes a division.
+// Bound by memory: each element is read and written once, so everything else
+// is kept off the path.  Block shape: x covers the work items of one head (a
+// vector of up to 16 bytes; with pairs half a head apart a vector and its
+// partner together, so that a turn in place has one owner), y the heads of one
+// token, or of several where there are few heads.  A thread keeps its item
+// and token, so the cosines and sines it needs sit in registers for all its
+// heads and its addresses advance by one stride; the CTA computes each pair's
+// once (one integer multiply and one sincospi), while the first heads' values
+// are on their way.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -19,9 +20,9 @@ namespace dsaidx {
 
 namespace {
 
-constexpr int kRopeThreads = 256;
-constexpr int kRopeRows = 4;              // rows in flight a thread
-constexpr int kRopeTableBytes = 40960;    // cosines and sines of the tokens a CTA spans
+// 128 threads: 8192 x 64 heads x 128, half of each turned in halves, 56 us
+// (4.8 TB/s); 256 threads 58 us.  4000 x 64 x 192 interleaved 36 us against 40.
+constexpr int kRopeThreads = 128;
 
 template <class T> __device__ __forceinline__ float to_f32(T v) { return static_cast<float>(v); }
 template <class T> __device__ __forceinline__ T from_f32(float v);
@@ -39,68 +40,79 @@ struct RopeParams {
     void* y;
     const int64_t* pos;
     const uint64_t* steps;
-    int64_t xt, xh, yt, yh, rows;
-    int heads, head_dim, rot, offset, rows_per_cta, items;
-    int rot_items;      // of the items: rotated ones first, then copies
-    int step, dist;     // split pairs: elements from item to item, from a to b
+    int64_t xt, xh, yt, yh, tokens;
+    int heads, head_dim, rot, offset, items;
+    int rot_items;         // of the items: rotated ones first, then copies
+    int step, dist;        // split pairs: elements from item to item, from a to b
+    int tok_cta, hy;       // tokens a CTA, heads of a token next to each other in y
+    int heads_cta;         // heads a CTA (blockIdx.y)
     float amplitude;
-    float sign;         // -1: the transposed map
+    float sign;            // -1: the transposed map
 };
 
 // kSplit: a pair's two values lie in two vectors (halves; or interleaved pairs
 // that no two-element access may touch); else next to each other in one.
 template <class T, int kVec, bool kSplit>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) {
-    extern __shared__ float2 cs[];   // [tokens spanned][rot / 2]
+    extern __shared__ float2 cs[];   // [tok_cta][rot / 2]
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int np = p.rot >> 1;
-    const int64_t row0 = static_cast<int64_t>(blockIdx.x) * p.rows_per_cta;
-    const int rows = static_cast<int>(p.rows - row0 < p.rows_per_cta ? p.rows - row0 : p.rows_per_cta);
-    const int64_t t0 = row0 / p.heads;
-    const int h0 = static_cast<int>(row0 - t0 * p.heads);
-    const int toks = (h0 + rows - 1) / p.heads + 1;
-    const int tid = threadIdx.y * blockDim.x + threadIdx.x, nthr = blockDim.x * blockDim.y;
-    for (int i = tid; i < toks * np; i += nthr) {
-        const int t = i / np, k = i - t * np;
-        float2 v = rope_cs(p.pos[t0 + t], p.steps[k], p.amplitude);
-        v.y *= p.sign;
-        cs[i] = v;
-    }
-    __syncthreads();
     using V = Vec<T, kVec>;
-    for (int item = threadIdx.x; item < p.items; item += blockDim.x) {
-        const bool turned = item < p.rot_items;
-        // element of the head this item starts at, and its first pair
-        int e, pair = 0;
+    constexpr int kPairs = kSplit ? kVec : kVec / 2;
+    // heads in flight a thread; two vectors of a split pair are enough (two
+    // heads of them: 68 us in the case above, for want of registers)
+    constexpr int kRopeHeads = kSplit ? 1 : 2;
+    const int np = p.rot >> 1;
+    const int64_t tok0 = static_cast<int64_t>(blockIdx.x) * p.tok_cta;
+    const int toks = static_cast<int>(p.tokens - tok0 < p.tok_cta ? p.tokens - tok0 : p.tok_cta);
+    const int tl = threadIdx.y / p.hy;
+    const int h0 = blockIdx.y * p.heads_cta + threadIdx.y - tl * p.hy;
+    const int h1 = tl < toks ? min(p.heads, (static_cast<int>(blockIdx.y) + 1) * p.heads_cta) : 0;
+    const T* x = static_cast<const T*>(p.x) + (tok0 + tl) * p.xt;
+    T* y = static_cast<T*>(p.y) + (tok0 + tl) * p.yt;
+    V a[kRopeHeads], b[kRopeHeads];
+    bool turned = false;
+    int e = 0;                       // element of the head the item starts at
+    auto load = [&](int item, int h) {
+        turned = item < p.rot_items;
         if (turned) {
             e = p.offset + item * (kSplit ? p.step : kVec);
-            pair = kSplit ? item * kVec : item * kVec / 2;
         } else {
             e = (item - p.rot_items) * kVec;
             if (e >= p.offset) e += p.rot;
         }
-        for (int r0 = threadIdx.y; r0 < rows; r0 += kRopeRows * blockDim.y) {
-            V a[kRopeRows], b[kRopeRows];
-            int t[kRopeRows], h[kRopeRows];
 #pragma unroll
-            for (int u = 0; u < kRopeRows; ++u) {
-                const int r = r0 + u * blockDim.y;
-                if (r >= rows) continue;
-                t[u] = (h0 + r) / p.heads;
-                h[u] = h0 + r - t[u] * p.heads;
-                const T* src = static_cast<const T*>(p.x) + (t0 + t[u]) * p.xt + h[u] * p.xh + e;
-                a[u] = *reinterpret_cast<const V*>(src);
-                if constexpr (kSplit)
-                    if (turned) b[u] = *reinterpret_cast<const V*>(src + p.dist);
-            }
+        for (int u = 0; u < kRopeHeads; ++u) {
+            if (h + u * p.hy >= h1) continue;
+            const T* src = x + (h + u * p.hy) * p.xh + e;
+            a[u] = *reinterpret_cast<const V*>(src);
+            if constexpr (kSplit)
+                if (turned) b[u] = *reinterpret_cast<const V*>(src + p.dist);
+        }
+    };
+    // the first values are on their way while the table is made
+    int item = threadIdx.x;
+    load(item, h0);
+    for (int i = threadIdx.y * blockDim.x + threadIdx.x; i < toks * np; i += blockDim.x * blockDim.y) {
+        const int tk = i / np, k = i - tk * np;
+        float2 v = rope_cs(p.pos[tok0 + tk], p.steps[k], p.amplitude);
+        v.y *= p.sign;
+        cs[i] = v;
+    }
+    __syncthreads();
+    while (true) {
+        float2 c[kPairs];
+        if (turned) {
 #pragma unroll
-            for (int u = 0; u < kRopeRows; ++u) {
-                const int r = r0 + u * blockDim.y;
-                if (r >= rows) continue;
-                T* dst = static_cast<T*>(p.y) + (t0 + t[u]) * p.yt + h[u] * p.yh + e;
+            for (int j = 0; j < kPairs; ++j) c[j] = cs[tl * np + item * kPairs + j];
+        }
+        for (int h = h0; h < h1; h += kRopeHeads * p.hy) {
+            if (h != h0) load(item, h);
+#pragma unroll
+            for (int u = 0; u < kRopeHeads; ++u) {
+                if (h + u * p.hy >= h1) continue;
+                T* dst = y + (h + u * p.hy) * p.yh + e;
                 if (turned) {
-                    const float2* c = cs + t[u] * np + pair;
                     if constexpr (kSplit) {
 #pragma unroll
                         for (int j = 0; j < kVec; ++j) {
@@ -121,6 +133,9 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
                 *reinterpret_cast<V*>(dst) = a[u];
             }
         }
+        item += blockDim.x;
+        if (item >= p.items) break;
+        load(item, h0);
     }
 }
 
@@ -130,21 +145,22 @@ cudaError_t launch_rope_t(RopeParams p, bool half, bool inplace, int sms, cudaSt
     p.dist = half ? p.rot / 2 : 1;
     p.rot_items = kSplit ? p.rot / 2 / kVec : p.rot / kVec;
     p.items = p.rot_items + (inplace ? 0 : (p.head_dim - p.rot) / kVec);
-    const int bx = p.items < kRopeThreads ? p.items : kRopeThreads, by = kRopeThreads / bx;
-    // kRopeRows rows a thread where that leaves two CTAs an SM, else one; the
-    // table of the tokens spanned (rows / heads + 2 at most) has to fit
-    int64_t rpc = static_cast<int64_t>(kRopeRows) * by;
-    if ((p.rows + rpc - 1) / rpc < 2 * sms) rpc = by;
-    const int fit = kRopeTableBytes / (p.rot / 2 * 8);   // >= 10 tokens
-    if (rpc / p.heads + 2 > fit) rpc = static_cast<int64_t>(fit - 2) * p.heads;
-    p.rows_per_cta = static_cast<int>(rpc);
-    const int64_t toks = rpc / p.heads + 2;
-    const int64_t grid = (p.rows + rpc - 1) / rpc;
-    if (grid >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
+    const int bx = p.items < kRopeThreads ? p.items : kRopeThreads, most = kRopeThreads / bx;
+    // y: the heads of a token in equal rounds, or several tokens' heads
+    const int rounds = (p.heads + most - 1) / most;
+    p.hy = (p.heads + rounds - 1) / rounds;
+    p.tok_cta = most / p.hy;
+    if (p.tok_cta > p.tokens) p.tok_cta = static_cast<int>(p.tokens);
+    // few tokens: their heads go to several CTAs, down to one round each
+    const int64_t groups = (p.tokens + p.tok_cta - 1) / p.tok_cta;
+    int64_t splits = (2 * sms + groups - 1) / groups;
+    if (splits > rounds) splits = rounds;
+    p.heads_cta = static_cast<int>((rounds + splits - 1) / splits) * p.hy;
+    if (groups >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
-    cfg.blockDim = dim3(static_cast<unsigned>(bx), static_cast<unsigned>(by), 1);
-    cfg.dynamicSmemBytes = static_cast<size_t>(toks) * (p.rot / 2) * 8;
+    cfg.gridDim = dim3(static_cast<unsigned>(groups), static_cast<unsigned>((p.heads + p.heads_cta - 1) / p.heads_cta), 1);
+    cfg.blockDim = dim3(static_cast<unsigned>(bx), static_cast<unsigned>(p.hy * p.tok_cta), 1);
+    cfg.dynamicSmemBytes = static_cast<size_t>(p.tok_cta) * (p.rot / 2) * sizeof(float2);   // at most 16 KB
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -186,7 +202,7 @@ cudaError_t launch_rope(const RopeArgs& a, int sms, cudaStream_t st) {
     RopeParams p{};
     p.x = a.x; p.y = a.y; p.pos = a.positions; p.steps = a.steps;
     p.xt = a.xt; p.xh = a.xh; p.yt = a.yt; p.yh = a.yh;
-    p.rows = a.tokens * a.heads;
+    p.tokens = a.tokens;
     p.heads = a.heads; p.head_dim = a.head_dim; p.rot = a.rot; p.offset = a.offset;
     p.amplitude = a.amplitude;
     p.sign = (a.flags & IDX_ROPE_TRANSPOSE) ? -1.0f : 1.0f;

@@ -17,7 +17,7 @@ from typing import Optional
 import torch
 
 from . import dsaidx
-from .dsaidx import _check, _need, _ptr, _stream
+from .dsaidx import IdxError
 
 HEADER = os.path.join(os.path.dirname(dsaidx.HEADER), "dsaidx_latent.h")
 
@@ -73,16 +73,51 @@ def header_functions():
     return sorted(set(re.findall(r"\b(idx_[a-z_]+)\s*\(", src)))
 
 
-def _strided(t: torch.Tensor, dtype, name: str, shape):
-    """A CUDA tensor of that type and shape whose last dimension is contiguous."""
+# The calls below take a few microseconds on the GPU, so the checks are written
+# for speed: one pass over what has to hold, the message only where it fails.
+def _refuse(t, dtype, name: str, shape, dense: bool):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError("%s must be a CUDA tensor" % name)
     if t.dtype != dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if tuple(t.shape) != tuple(shape):
+    if shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-    if t.numel() and shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError("%s must be contiguous in its last dimension" % name)
+    raise ValueError("%s must be contiguous%s" % (name, "" if dense else " in its last dimension"))
+
+
+def _dense(t: torch.Tensor, dtype, name: str, shape=None) -> int:
+    """Address of a contiguous CUDA tensor of that type (and shape)."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and (shape is None or t.shape == shape)
+            and t.is_contiguous()):
+        _refuse(t, dtype, name, shape, True)
+    return t.data_ptr()
+
+
+def _strided(t: torch.Tensor, dtype, name: str, shape):
+    """Address and strides of a CUDA tensor of that type and shape whose last dimension is contiguous."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and t.shape == shape):
+        _refuse(t, dtype, name, shape, False)
+    st = t.stride()
+    if st[-1] != 1 and shape[-1] > 1 and t.numel():
+        _refuse(t, dtype, name, shape, False)
+    return t.data_ptr(), st
+
+
+def _maybe(t, dtype, name: str, shape=None):
+    """_dense of an optional tensor: None where there is none."""
+    return None if t is None else _dense(t, dtype, name, shape)
+
+
+def _check(code: int, what: str):
+    if code:
+        raise IdxError(code, what)
+
+
+def _stream(stream) -> int:
+    """The stream's handle; the current one's without building a Stream object (2.9 us a call)."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream
 
 
 class RopePlan:
@@ -93,6 +128,10 @@ class RopePlan:
         self.amplitude = amplitude
         self.rot_dim = 2 * steps.numel()
 
+    def on_device(self) -> int:
+        """Address of the steps; they have to be in device memory."""
+        return _dense(self.steps, torch.int64, "plan.steps")
+
 
 def rope_steps(rot_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
                original_max_pos: float = 4096, beta_fast: float = 32.0, beta_slow: float = 1.0):
@@ -102,7 +141,7 @@ def rope_steps(rot_dim: int, base: float = 10000.0, scaling: str = "none", facto
     steps = torch.zeros(max(rot_dim // 2, 1), dtype=torch.int64)
     amp = ctypes.c_float(0.0)
     _check(load().idx_rope_steps(rot_dim, base, _SCALING[scaling], factor, original_max_pos, beta_fast, beta_slow,
-                                 _ptr(steps), ctypes.byref(amp)), "idx_rope_steps")
+                                 steps.data_ptr(), ctypes.byref(amp)), "idx_rope_steps")
     return steps, float(amp.value)
 
 
@@ -126,15 +165,13 @@ def rope(x: torch.Tensor, positions: torch.Tensor, plan: RopePlan, layout: int =
         raise TypeError("x must be [tokens, heads, head_dim] of bfloat16, float16 or float32")
     if layout not in (INTERLEAVED, HALF):
         raise ValueError("layout must be INTERLEAVED or HALF")
-    T, H, D = x.shape
+    T, H, D = shape = x.shape
     out = x if out is None else out
-    _strided(x, x.dtype, "x", (T, H, D))
-    _strided(out, x.dtype, "out", (T, H, D))
-    _need(positions, torch.int64, "positions", (T,))
-    _need(plan.steps, torch.int64, "plan.steps")
-    _check(load().idx_rope(_ptr(x), x.stride(0), x.stride(1), _ptr(out), out.stride(0), out.stride(1),
-                           _DTYPE[x.dtype], T, H, D, _ptr(positions), _ptr(plan.steps), plan.rot_dim, offset,
-                           plan.amplitude, layout | (_TRANSPOSE if transpose else 0), _stream(stream)), "idx_rope")
+    xp, xs = _strided(x, x.dtype, "x", shape)
+    yp, ys = _strided(out, x.dtype, "out", shape)
+    _check(load().idx_rope(xp, xs[0], xs[1], yp, ys[0], ys[1], _DTYPE[x.dtype], T, H, D,
+                           _dense(positions, torch.int64, "positions", (T,)), plan.on_device(), plan.rot_dim, offset,
+                           plan.amplitude, layout | _TRANSPOSE if transpose else layout, _stream(stream)), "idx_rope")
     return out
 
 
@@ -143,20 +180,17 @@ class LatentCache:
     [num_blocks, block_size, 576], each record [latent 512 | turned key 64]."""
 
     def __init__(self, pool: torch.Tensor):
-        _need(pool, torch.bfloat16, "pool")
+        _dense(pool, torch.bfloat16, "pool")
         if pool.dim() != 3 or pool.shape[2] != RECORD:
             raise ValueError("pool must be [num_blocks, block_size, %d]" % RECORD)
         self.pool = pool
         self.num_blocks, self.block_size = int(pool.shape[0]), int(pool.shape[1])
         self._desc = _Pool(pool.data_ptr(), self.num_blocks, self.block_size)
+        self.desc = ctypes.byref(self._desc)   # what the calls take
 
     @staticmethod
     def allocate(num_blocks: int, block_size: int, device="cuda"):
         return LatentCache(torch.zeros(num_blocks, block_size, RECORD, dtype=torch.bfloat16, device=device))
-
-    @property
-    def desc(self):
-        return ctypes.byref(self._desc)
 
 
 def latent_append(cache: LatentCache, latent: torch.Tensor, k_pe: torch.Tensor, positions: Optional[torch.Tensor],
@@ -166,23 +200,20 @@ def latent_append(cache: LatentCache, latent: torch.Tensor, k_pe: torch.Tensor, 
     [n, 64], rows may be strided) to their slots, k_pe turned by positions
     [n] int64 on the way (copied where plan is None)."""
     n = latent.shape[0]
-    _strided(latent, torch.bfloat16, "latent", (n, LATENT_DIM))
-    _strided(k_pe, torch.bfloat16, "k_pe", (n, PE_DIM))
-    _need(slot_mapping, torch.int64, "slot_mapping", (n,))
+    lp, ls = _strided(latent, torch.bfloat16, "latent", (n, LATENT_DIM))
+    kp, ks = _strided(k_pe, torch.bfloat16, "k_pe", (n, PE_DIM))
     if layout not in (INTERLEAVED, HALF):
         raise ValueError("layout must be INTERLEAVED or HALF")
+    pos = steps = None
+    amplitude = 1.0
     if plan is not None:
         if plan.rot_dim != PE_DIM:
             raise ValueError("plan must turn %d elements" % PE_DIM)
-        _need(positions, torch.int64, "positions", (n,))
-        _need(plan.steps, torch.int64, "plan.steps")
-    if status is not None:
-        _need(status, torch.int32, "status")
-    _check(load().idx_latent_append(cache.desc, _ptr(latent), latent.stride(0), _ptr(k_pe), k_pe.stride(0),
-                                    _ptr(positions if plan is not None else None), _ptr(slot_mapping), n,
-                                    _ptr(plan.steps if plan is not None else None),
-                                    plan.amplitude if plan is not None else 1.0, layout, _ptr(status),
-                                    _stream(stream)), "idx_latent_append")
+        pos, steps, amplitude = _dense(positions, torch.int64, "positions", (n,)), plan.on_device(), plan.amplitude
+    _check(load().idx_latent_append(cache.desc, lp, ls[0], kp, ks[0], pos,
+                                    _dense(slot_mapping, torch.int64, "slot_mapping", (n,)), n, steps, amplitude,
+                                    layout, _maybe(status, torch.int32, "status"), _stream(stream)),
+           "idx_latent_append")
 
 
 def workspace_bytes(rows: int, heads: int, max_keys: int) -> int:
@@ -190,17 +221,16 @@ def workspace_bytes(rows: int, heads: int, max_keys: int) -> int:
     return int(load().idx_latent_workspace_bytes(rows, heads, max_keys))
 
 
-def _absorbed_tensors(q_latent, q_pe, out, lse, workspace):
+def _absorbed(q_latent, q_pe, out, lse, workspace):
+    """Checks what the two absorbed calls share: rows, heads and their common arguments."""
     if q_latent.dim() != 3:
         raise ValueError("q_latent must be [rows, heads, %d]" % LATENT_DIM)
-    T, H = q_latent.shape[0], q_latent.shape[1]
-    _strided(q_latent, torch.bfloat16, "q_latent", (T, H, LATENT_DIM))
-    _strided(q_pe, torch.bfloat16, "q_pe", (T, H, PE_DIM))
-    _need(out, torch.bfloat16, "out", (T, H, LATENT_DIM))
-    if lse is not None:
-        _need(lse, torch.float32, "lse", (T, H))
-    _need(workspace, torch.uint8, "workspace")
-    return T, H
+    T, H, _ = q_latent.shape
+    lp, ls = _strided(q_latent, torch.bfloat16, "q_latent", (T, H, LATENT_DIM))
+    kp, ks = _strided(q_pe, torch.bfloat16, "q_pe", (T, H, PE_DIM))
+    return (T, H, (lp, ls[0], ls[1], kp, ks[0], ks[1]),
+            (_dense(out, torch.bfloat16, "out", (T, H, LATENT_DIM)), _maybe(lse, torch.float32, "lse", (T, H)),
+             _dense(workspace, torch.uint8, "workspace"), workspace.numel()))
 
 
 def latent_attend_slots(cache: LatentCache, q_latent: torch.Tensor, q_pe: torch.Tensor, slots: torch.Tensor,
@@ -210,14 +240,13 @@ def latent_attend_slots(cache: LatentCache, q_latent: torch.Tensor, q_pe: torch.
     q_pe [rows, heads, 64]) attend over the records at its slots [rows, topk]
     int64 (the out_slot of the score calls; negative entries are skipped).
     out [rows, heads, 512] bf16, lse [rows, heads] fp32."""
-    T, H = _absorbed_tensors(q_latent, q_pe, out, lse, workspace)
+    T, H, query, result = _absorbed(q_latent, q_pe, out, lse, workspace)
     if slots.dim() != 2:
         raise ValueError("slots must be [rows, topk]")
-    _strided(slots, torch.int64, "slots", (T, slots.shape[1]))
-    _check(load().idx_latent_attend_slots(cache.desc, _ptr(q_latent), q_latent.stride(0), q_latent.stride(1),
-                                          _ptr(q_pe), q_pe.stride(0), q_pe.stride(1), _ptr(slots), slots.stride(0), T,
-                                          H, slots.shape[1], scale, _ptr(out), _ptr(lse), _ptr(workspace),
-                                          workspace.numel(), _stream(stream)), "idx_latent_attend_slots")
+    topk = slots.shape[1]
+    sp, ss = _strided(slots, torch.int64, "slots", (T, topk))
+    _check(load().idx_latent_attend_slots(cache.desc, *query, sp, ss[0], T, H, topk, scale, *result, _stream(stream)),
+           "idx_latent_attend_slots")
 
 
 def latent_attend_paged(cache: LatentCache, q_latent: torch.Tensor, q_pe: torch.Tensor, block_table: torch.Tensor,
@@ -225,16 +254,12 @@ def latent_attend_paged(cache: LatentCache, q_latent: torch.Tensor, q_pe: torch.
                         workspace: torch.Tensor, lse: Optional[torch.Tensor] = None, stream=None):
     """idx_latent_attend_paged: one query a sequence over all its records
     (block_table [batch, max_blocks_per_seq], seq_lens [batch] int32)."""
-    T, H = _absorbed_tensors(q_latent, q_pe, out, lse, workspace)
-    _need(block_table, torch.int32, "block_table")
-    _need(seq_lens, torch.int32, "seq_lens", (T,))
+    T, H, query, result = _absorbed(q_latent, q_pe, out, lse, workspace)
     if block_table.dim() != 2 or block_table.shape[0] != T:
         raise ValueError("block_table must be [batch, max_blocks_per_seq]")
-    _check(load().idx_latent_attend_paged(cache.desc, _ptr(q_latent), q_latent.stride(0), q_latent.stride(1),
-                                          _ptr(q_pe), q_pe.stride(0), q_pe.stride(1), _ptr(block_table),
-                                          block_table.shape[1], _ptr(seq_lens), T, max_seq_len, H, scale, _ptr(out),
-                                          _ptr(lse), _ptr(workspace), workspace.numel(), _stream(stream)),
-           "idx_latent_attend_paged")
+    _check(load().idx_latent_attend_paged(cache.desc, *query, _dense(block_table, torch.int32, "block_table"),
+                                          block_table.shape[1], _dense(seq_lens, torch.int32, "seq_lens", (T,)), T,
+                                          max_seq_len, H, scale, *result, _stream(stream)), "idx_latent_attend_paged")
 
 
 def latent_attend_expanded(q: torch.Tensor, k_nope: torch.Tensor, k_pe: torch.Tensor, v: torch.Tensor,
@@ -247,21 +272,15 @@ def latent_attend_expanded(q: torch.Tensor, k_nope: torch.Tensor, k_pe: torch.Te
     if q.dim() != 3 or k_nope.dim() != 3:
         raise ValueError("q and k_nope must be [tokens, heads, dim]")
     T, H, S = q.shape[0], q.shape[1], k_nope.shape[0]
-    _strided(q, torch.bfloat16, "q", (T, H, NOPE_DIM + PE_DIM))
-    _strided(k_nope, torch.bfloat16, "k_nope", (S, H, NOPE_DIM))
-    _strided(k_pe, torch.bfloat16, "k_pe", (S, PE_DIM))
-    _strided(v, torch.bfloat16, "v", (S, H, V_DIM))
-    _need(cu_seqlens_q, torch.int32, "cu_seqlens_q")
-    B = cu_seqlens_q.numel() - 1
-    _need(cu_seqlens_q, torch.int32, "cu_seqlens_q", (B + 1,))
-    _need(cu_seqlens_k, torch.int32, "cu_seqlens_k", (B + 1,))
-    _need(out, torch.bfloat16, "out", (T, H, V_DIM))
-    if lse is not None:
-        _need(lse, torch.float32, "lse", (T, H))
-    if status is not None:
-        _need(status, torch.int32, "status")
-    _check(load().idx_latent_attend_expanded(_ptr(q), q.stride(0), q.stride(1), _ptr(k_nope), k_nope.stride(0),
-                                             k_nope.stride(1), _ptr(k_pe), k_pe.stride(0), _ptr(v), v.stride(0),
-                                             v.stride(1), _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), B, T, S, H, scale,
-                                             _ptr(out), _ptr(lse), _ptr(status), _stream(stream)),
+    bf16, B = torch.bfloat16, cu_seqlens_q.numel() - 1
+    qp, qs = _strided(q, bf16, "q", (T, H, NOPE_DIM + PE_DIM))
+    np_, ns = _strided(k_nope, bf16, "k_nope", (S, H, NOPE_DIM))
+    pp, ps = _strided(k_pe, bf16, "k_pe", (S, PE_DIM))
+    vp, vs = _strided(v, bf16, "v", (S, H, V_DIM))
+    _check(load().idx_latent_attend_expanded(qp, qs[0], qs[1], np_, ns[0], ns[1], pp, ps[0], vp, vs[0], vs[1],
+                                             _dense(cu_seqlens_q, torch.int32, "cu_seqlens_q", (B + 1,)),
+                                             _dense(cu_seqlens_k, torch.int32, "cu_seqlens_k", (B + 1,)), B, T, S, H,
+                                             scale, _dense(out, bf16, "out", (T, H, V_DIM)),
+                                             _maybe(lse, torch.float32, "lse", (T, H)),
+                                             _maybe(status, torch.int32, "status"), _stream(stream)),
            "idx_latent_attend_expanded")
