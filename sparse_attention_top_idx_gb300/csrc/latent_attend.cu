@@ -13,11 +13,12 @@
 // the scores, MN-major for the values.
 //
 // One persistent CTA an SM, warp-specialised:
-//   warp 0     one lane issues every MMA.  The scores of tile i + 1 run while
-//              tile i is in softmax; between their steps the value product of
-//              tile i is issued as soon as its weights are there, which frees
-//              its records early
+//   warp 0     one lane issues the score products, up to two tiles ahead of
+//              the softmax
 //   warp 1     loads a row's queries
+//   warp 2     one lane issues the value products.  (One lane for both was the
+//              kernel's bound: its polling and 56 issues took 3400 cycles a
+//              tile.)
 //   warps 4-7  softmax and epilogue
 //   warps 8-11 gather records, 16 keys of every tile each, with 16-byte
 //              asynchronous copies into a ring of chunk pairs (128 latent
@@ -75,7 +76,7 @@ __host__ __device__ constexpr Plan plan_of(int N) {
     p.pe_off = o;   o += 2 * kChunk;
     p.stat_off = o; o += 5 * N * 4;        // four warps' values and one for all
     p.mask_off = o; o += 4 * 8;
-    p.bar_off = o;  o += (2 * p.pairs + 16) * 8 + 32;
+    p.bar_off = o;  o += (2 * p.pairs + 20) * 8;
     p.total = o + 1024;
     return p;
 }
@@ -198,20 +199,26 @@ struct Walk {
     }
 };
 
-// Slot of key j of a row; num_slots where it is masked.
-__device__ __forceinline__ int key_slot(const Params& p, int64_t row, int keys, int j) {
-    if (j >= keys) return static_cast<int>(p.num_slots);
-    int64_t s;
+// What names key j of a row: its entry of the slot list or of the block table.
+// Read a tile ahead; key_slot, which looks at it, comes when it has arrived.
+__device__ __forceinline__ int64_t key_entry(const Params& p, int64_t row, int keys, int j) {
+    if (j >= keys) return -1;
+    return p.block_table == nullptr ? __ldg(p.slots + row * p.slots_stride + j)
+                                    : static_cast<int64_t>(__ldg(p.block_table + row * p.mbps + j / p.block_size));
+}
+// Slot of key j; num_slots where it is masked.
+__device__ __forceinline__ int key_slot(const Params& p, int keys, int j, int64_t entry) {
+    const int none = static_cast<int>(p.num_slots);
+    if (j >= keys) return none;
+    int64_t s = entry;
     if (p.block_table == nullptr) {
-        s = __ldg(p.slots + row * p.slots_stride + j);
-        if (s < 0) return static_cast<int>(p.num_slots);
+        if (s < 0) return none;
     } else {
-        const int blk = __ldg(p.block_table + row * p.mbps + j / p.block_size);
-        s = blk < 0 ? p.num_slots : static_cast<int64_t>(blk) * p.block_size + j % p.block_size;
+        s = entry < 0 ? p.num_slots : entry * p.block_size + j % p.block_size;
     }
     if (s >= p.num_slots) {
         set_status(p.status, IDX_ERR_DEVICE_CHECK);
-        return static_cast<int>(p.num_slots);
+        return none;
     }
     return static_cast<int>(s);
 }
@@ -237,9 +244,10 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     uint64_t* q_full = pe_full + 8;
     uint64_t* q_empty = pe_full + 9;
     uint64_t* o_empty = pe_full + 10;
-    uint64_t* drain = pe_full + 11;
-    int64_t* sh_run = reinterpret_cast<int64_t*>(pe_full + 12);   // start, end, row, base
-    uint32_t* sh_tmem = reinterpret_cast<uint32_t*>(pe_full + 16);
+    uint64_t* drain = pe_full + 11;              // [2]
+    uint64_t* s_empty = pe_full + 13;            // [2]
+    int64_t* sh_run = reinterpret_cast<int64_t*>(pe_full + 15);   // start, end, row, base
+    uint32_t* sh_tmem = reinterpret_cast<uint32_t*>(pe_full + 19);
     int* sh_abort = reinterpret_cast<int*>(sh_tmem + 1);
     uint16_t* masks = reinterpret_cast<uint16_t*>(smem + kPlan.mask_off);   // [4 tiles][4]: 16 keys each
     float* stat = reinterpret_cast<float*>(smem + kPlan.stat_off);          // [5][N]
@@ -257,6 +265,9 @@ __global__ void __launch_bounds__(kAttThreads, 1)
         mbar_init(q_empty, 1);
         mbar_init(o_empty, kSoftThreads);
         mbar_init(drain, 1);
+        mbar_init(drain + 1, 1);
+        mbar_init(s_empty, kSoftThreads);
+        mbar_init(s_empty + 1, kSoftThreads);
         *sh_abort = 0;
         fence_mbar_init();
     }
@@ -315,8 +326,9 @@ __global__ void __launch_bounds__(kAttThreads, 1)
         while (ok && walk.next(p, w)) {
             if (p.block_table != nullptr && w.keys == 0 && lane == 0 && __ldg(p.seq_lens + w.row) != 0)
                 set_status(p.status, IDX_ERR_DEVICE_CHECK);
-            int slot = key_slot(p, w.row, w.keys, w.t0 * kKeys + j);
+            int64_t entry = key_entry(p, w.row, w.keys, w.t0 * kKeys + j);
             for (int t = w.t0; t < w.t1; ++t, ++it) {
+                const int slot = key_slot(p, w.keys, t * kKeys + j, entry);
                 const uint32_t valid = __ballot_sync(~0u, slot != none) & 0xFFFFu;
                 const uint8_t* src[4];
 #pragma unroll
@@ -324,7 +336,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                     const int s = __shfl_sync(~0u, slot, 4 * k + sub);
                     src[k] = p.pool + static_cast<int64_t>(s == none ? 0 : s) * (IDX_LATENT_RECORD * 2) + 16 * piece;
                 }
-                if (t + 1 < w.t1) slot = key_slot(p, w.row, w.keys, (t + 1) * kKeys + j);
+                if (t + 1 < w.t1) entry = key_entry(p, w.row, w.keys, (t + 1) * kKeys + j);
                 auto chunk = [&](uint32_t dst, int c) {
                     if (valid == 0xFFFFu) {
 #pragma unroll
@@ -359,58 +371,20 @@ __global__ void __launch_bounds__(kAttThreads, 1)
         }
         copy_wait_all();
     } else if (warp == 0) {
-        // ---- every MMA ----
+        // ---- score products ----
         if (elect_one()) {
             constexpr uint32_t kIdS = idesc_bf16(64, N, false, false);
-            constexpr uint32_t kIdO = idesc_bf16(128, N, true, true);
             const uint32_t q_addr = smem_u32(smem + kPlan.q_off), ring = smem_u32(smem + kPlan.ring_off);
-            const uint32_t pe_addr = smem_u32(smem + kPlan.pe_off), p_addr = smem_u32(smem + kPlan.p_off);
-            uint32_t it = 0, item = 0;                    // tile and piece of the score products
-            uint32_t s_sl = 0, s_ph = 0, v_sl = 0;        // ring position of the score and the value products
-            bool ok = true, pending = false, v_first = false;   // the value product of tile v_it is still to be issued
-            uint32_t v_it = 0, v_item = 0;
-            auto values = [&]() {
-                tc_fence_after();
-#pragma unroll 1
-                for (int m = 0; m < 4; ++m) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma_bf16(tmem + m * N, sdesc_mn_sw128(ring + v_sl * kPair + 2048 * k, kChunk),
-                                 sdesc_mn_sw128(p_addr + 2048 * k, kChunk), kIdO, (!v_first || k != 0) ? 1u : 0u);
-                    mma_commit(pair_empty + v_sl);
-                    if (++v_sl == kPairs) v_sl = 0;
-                }
-                mma_commit(pv_done);
-                pending = false;
-            };
-            // the weights are there, and the accumulators of the piece before were read
-            auto finish_values = [&]() -> bool {
-                if (!pending) return true;
-                if (!mbar_wait(p_full, v_it & 1, p.status, abort_flag)) return false;
-                if (v_first && !mbar_wait(o_empty, (v_item & 1) ^ 1, p.status, abort_flag)) return false;
-                values();
-                return true;
-            };
-            // wait for operands of a score product; value products pass it
-            auto wait_operand = [&](uint64_t* b, uint32_t parity) -> bool {
-                unsigned long long since = 0;
-                for (uint32_t n = 1; pending; ++n) {
-                    if (mbar_test(p_full, v_it & 1) && (!v_first || mbar_test(o_empty, (v_item & 1) ^ 1))) values();
-                    if (mbar_test(b, parity)) return true;
-                    if ((n & 1023u) == 0) {
-                        if (*abort_flag) return false;
-                        const unsigned long long now = global_timer_ns();
-                        if (since == 0) since = now;
-                        if (now - since > kWaitLimitNs) break;   // the wait below ends it
-                    }
-                }
-                return mbar_wait(b, parity, p.status, abort_flag);
-            };
+            const uint32_t pe_addr = smem_u32(smem + kPlan.pe_off);
+            uint32_t it = 0, item = 0, sl = 0, ph = 0;
+            bool ok = true;
             while (ok && walk.next(p, w)) {
-                if (!(ok = wait_operand(q_full, item & 1))) break;
+                if (!(ok = mbar_wait(q_full, item & 1, p.status, abort_flag))) break;
                 for (int t = w.t0; t < w.t1; ++t, ++it) {
                     const uint32_t d = tmem + kSCol + (it & 1) * kSPitch;
-                    if (!(ok = wait_operand(pe_full + (it & 1), (it >> 1) & 1))) break;
+                    // the softmax has read the scores before last
+                    if (!(ok = mbar_wait(s_empty + (it & 1), ((it >> 1) & 1) ^ 1, p.status, abort_flag))) break;
+                    if (!(ok = mbar_wait(pe_full + (it & 1), (it >> 1) & 1, p.status, abort_flag))) break;
                     // the records were copied by other threads: order their
                     // writes before the tensor core's reads
                     fence_proxy_async_smem();
@@ -422,30 +396,55 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                     mma_commit(pe_empty + (it & 1));
 #pragma unroll 1
                     for (int m = 0; m < 4; ++m) {
-                        if (!(ok = wait_operand(pair_full + s_sl, s_ph))) break;
+                        if (!(ok = mbar_wait(pair_full + sl, ph, p.status, abort_flag))) break;
                         fence_proxy_async_smem();
                         tc_fence_after();
 #pragma unroll
                         for (int k = 0; k < 8; ++k)
-                            mma_bf16(d, sdesc_sw128(ring + s_sl * kPair + (k >> 2) * kChunk + 32 * (k & 3)),
+                            mma_bf16(d, sdesc_sw128(ring + sl * kPair + (k >> 2) * kChunk + 32 * (k & 3)),
                                      sdesc_sw128(q_addr + (2 * m + (k >> 2)) * N * 128 + 32 * (k & 3)), kIdS, 1u);
-                        if (++s_sl == kPairs) s_sl = 0, s_ph ^= 1;
+                        if (++sl == kPairs) sl = 0, ph ^= 1;
                     }
                     if (!ok) break;
                     mma_commit(s_full + (it & 1));
                     if (t + 1 == w.t1) mma_commit(q_empty);
-                    if (!(ok = finish_values())) break;
-                    pending = true;
-                    v_first = t == w.t0;
-                    v_it = it;
-                    v_item = item;
                 }
                 ++item;
             }
-            if (ok) finish_values();
             // nothing of this CTA may run on when its shared memory and TMEM go
             mma_commit(drain);
             mbar_wait(drain, 0, p.status, nullptr);
+        }
+    } else if (warp == 2) {
+        // ---- value products ----
+        if (elect_one()) {
+            constexpr uint32_t kIdO = idesc_bf16(128, N, true, true);
+            const uint32_t ring = smem_u32(smem + kPlan.ring_off), p_addr = smem_u32(smem + kPlan.p_off);
+            uint32_t it = 0, item = 0, sl = 0;
+            bool ok = true;
+            while (ok && walk.next(p, w)) {
+                for (int t = w.t0; t < w.t1; ++t, ++it) {
+                    // the weights are there, which the records were before them
+                    if (!(ok = mbar_wait(p_full, it & 1, p.status, abort_flag))) break;
+                    // the accumulators of the piece before were read
+                    if (t == w.t0 && !(ok = mbar_wait(o_empty, (item & 1) ^ 1, p.status, abort_flag))) break;
+                    fence_proxy_async_smem();
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int m = 0; m < 4; ++m) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            mma_bf16(tmem + m * N, sdesc_mn_sw128(ring + sl * kPair + 2048 * k, kChunk),
+                                     sdesc_mn_sw128(p_addr + 2048 * k, kChunk), kIdO, (t != w.t0 || k != 0) ? 1u : 0u);
+                        mma_commit(pair_empty + sl);
+                        if (++sl == kPairs) sl = 0;
+                    }
+                    mma_commit(pv_done);
+                }
+                ++item;
+            }
+            mma_commit(drain + 1);
+            mbar_wait(drain + 1, 0, p.status, nullptr);
         }
     } else if (warp == 1) {
         // ---- queries ----
@@ -493,6 +492,8 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                 const bool va = (mask >> kr) & 1, vb = (mask >> (kr + 8)) & 1;
 #pragma unroll
                 for (int g = 0; g < (kR < 4 ? 1 : kR / 4); ++g) tmem_wait_ld16(raw[g]);
+                tc_fence_before();
+                mbar_arrive(s_empty + (it & 1));
                 // y[r][e]: key kr, y[r][2 + e]: key kr + 8; log2 of the weight
                 float y[kR][4];
                 bool grow = !ok;
