@@ -58,6 +58,7 @@ constexpr int kAttThreads = 384;
 constexpr int kSoftThreads = 128;
 constexpr int kGatherThreads = 128;
 constexpr int kMaxCtas = 152;              // one an SM; CTAs never wait on one another
+constexpr int kMinRun = 2;                 // tiles a CTA, at least, where rows are cut
 constexpr float kNone = -3.0e38f;          // maximum of a head without a key so far
 constexpr float kGrow = 8.0f;              // log2 by which a score may pass the maximum
 
@@ -657,17 +658,23 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
-// Joins the partial sums of the rows that were cut: one CTA a (row, head),
-// four warps over the pieces, lanes over the latent dimensions, then the warps'
-// sums in order.
-__global__ void __launch_bounds__(128) join_kernel(const Params p, int N, int ctas) {
-    __shared__ float acc[4][IDX_LATENT_DIM];
-    __shared__ float ls[4];
+// Joins the partial sums of the rows that were cut: one CTA a (row, head).
+// Thread i finds piece i's factor, then eight warps take the pieces in turn,
+// four of them in flight, lanes over the latent dimensions; the warps' sums are
+// added in order.
+constexpr int kJoinThreads = 256;
+static_assert(kMaxCtas <= kJoinThreads, "a thread a piece");
+
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const Params p, int N, int ctas) {
+    constexpr int kWarps = kJoinThreads / 32;
+    __shared__ float acc[kWarps][IDX_LATENT_DIM];
+    __shared__ float fac[kJoinThreads], red[2][kWarps];
+    __shared__ int from[kJoinThreads];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int64_t row = blockIdx.x;
     const int head = blockIdx.y, hg = head / 64, h = head % 64;
-    const int warp = warp_id(), lane = lane_id();
+    const int warp = warp_id(), lane = lane_id(), tid = threadIdx.x;
     int64_t a, tt;
     const int nt = tiles_of(row_keys(p, row));
     if (p.block_table == nullptr) {
@@ -692,47 +699,75 @@ __global__ void __launch_bounds__(128) join_kernel(const Params p, int N, int ct
     // first and last CTA with a tile of [a, b)
     int64_t c0 = a * ctas / tt, c1;
     while (run_start(c0 + 1, ctas, tt) <= a) ++c0;
-    c1 = c0;
+    c1 = (b - 1) * ctas / tt;
     while (run_start(c1 + 1, ctas, tt) < b) ++c1;
-    if (c0 == c1) return;
-    auto has = [&](int64_t c) { return run_start(c, ctas, tt) < run_start(c + 1, ctas, tt); };
-    auto slot_of = [&](int64_t c) { return 2 * c + (c == c0 && run_start(c, ctas, tt) < a ? 1 : 0); };
+    if (c0 == c1) return;      // it wrote the result
+    const int pieces = static_cast<int>(c1 - c0) + 1;
+    // a run may be empty; the row is the second piece of its first CTA unless
+    // it begins with that CTA's run
     float m = kNone;
-    for (int64_t c = c0 + lane; c <= c1; c += 32) {
-        if (!has(c)) continue;
-        const float2 ml = p.part_ml[slot_of(c) * N + h];
-        if (ml.y != 0.0f) m = fmaxf(m, ml.x);
+    float2 ml = make_float2(kNone, 0.0f);
+    if (tid < pieces) {
+        const int64_t c = c0 + tid, start = run_start(c, ctas, tt);
+        if (start < run_start(c + 1, ctas, tt)) {
+            from[tid] = static_cast<int>(2 * c + (start < a ? 1 : 0));
+            ml = p.part_ml[static_cast<int64_t>(from[tid]) * N + h];
+            if (ml.y != 0.0f) m = ml.x;
+        }
     }
     for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
-    float4 o[4] = {};
-    float l = 0.0f;
-    for (int64_t c = c0 + warp; c <= c1; c += 4) {
-        if (!has(c)) continue;
-        const int64_t s = slot_of(c) * N + h;
-        const float2 ml = p.part_ml[s];
-        if (ml.y == 0.0f) continue;
-        const float f = exp2_fast(ml.x - m);
-        l += ml.y * f;
-        const float4* src = reinterpret_cast<const float4*>(p.part_o + s * IDX_LATENT_DIM);
+    if (lane == 0) red[0][warp] = m;
+    __syncthreads();
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float4 v = __ldg(src + 32 * k + lane);
-            o[k].x += v.x * f; o[k].y += v.y * f; o[k].z += v.z * f; o[k].w += v.w * f;
+    for (int k = 0; k < kWarps; ++k) m = fmaxf(m, red[0][k]);
+    const float mine = ml.y != 0.0f ? exp2_fast(ml.x - m) : 0.0f;
+    fac[tid] = mine;
+    float l = mine != 0.0f ? ml.y * mine : 0.0f;
+    for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(~0u, l, d);
+    if (lane == 0) red[1][warp] = l;
+    __syncthreads();
+    float4 o[4] = {};
+    for (int k0 = warp; k0 < pieces; k0 += 4 * kWarps) {
+        float4 v[4][4];
+        float f[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int k = k0 + u * kWarps;
+            f[u] = k < pieces ? fac[k] : 0.0f;
+            if (f[u] == 0.0f) continue;
+            const float4* src =
+                reinterpret_cast<const float4*>(p.part_o + (static_cast<int64_t>(from[k]) * N + h) * IDX_LATENT_DIM);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[u][q] = __ldg(src + 32 * q + lane);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            if (f[u] == 0.0f) continue;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                o[q].x += v[u][q].x * f[u];
+                o[q].y += v[u][q].y * f[u];
+                o[q].z += v[u][q].z * f[u];
+                o[q].w += v[u][q].w * f[u];
+            }
         }
     }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) reinterpret_cast<float4*>(acc[warp])[32 * k + lane] = o[k];
-    if (lane == 0) ls[warp] = l;
+    for (int q = 0; q < 4; ++q) reinterpret_cast<float4*>(acc[warp])[32 * q + lane] = o[q];
     __syncthreads();
-    const float total = ls[0] + ls[1] + ls[2] + ls[3];
-    const float inv = total == 0.0f ? 0.0f : __fdiv_rn(1.0f, total);
-    const int d = 4 * threadIdx.x;
-    float v[4];
+    float total = 0.0f;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = (acc[0][d + k] + acc[1][d + k] + acc[2][d + k] + acc[3][d + k]) * inv;
-    *reinterpret_cast<uint2*>(p.out + (row * p.heads + head) * IDX_LATENT_DIM + d) =
-        make_uint2(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]));
-    if (threadIdx.x == 0 && p.lse != nullptr)
+    for (int k = 0; k < kWarps; ++k) total += red[1][k];
+    const float inv = total == 0.0f ? 0.0f : __fdiv_rn(1.0f, total);
+    const int d = 2 * tid;
+    float2 v = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k) {
+        v.x += acc[k][d];
+        v.y += acc[k][d + 1];
+    }
+    *reinterpret_cast<uint32_t*>(p.out + (row * p.heads + head) * IDX_LATENT_DIM + d) = bf16x2(v.x * inv, v.y * inv);
+    if (tid == 0 && p.lse != nullptr)
         p.lse[row * p.heads + head] = total == 0.0f ? -INFINITY : (m + log2f(total)) * 0.69314718055994531f;
 }
 
@@ -750,12 +785,14 @@ Shape shape_of(int64_t rows, int heads, int64_t max_keys) {
     const int64_t g = kMaxCtas;
     const int64_t items = rows * s.hgs, nt = max_keys > 0 ? (max_keys + kKeys - 1) / kKeys : 1;
     // Whole rows: ceil(items / g) rounds of nt tiles.  Cut: items nt / g tiles,
-    // plus storing and joining partial sums, which costs about as much as
-    // kCutTiles tiles.
-    constexpr int64_t kCutTiles = 6;
-    const int64_t whole = (items + g - 1) / g * nt, cut = (items * nt + g - 1) / g + kCutTiles;
+    // plus storing and joining partial sums, which costs about as much as 9
+    // tiles (12 of 64 heads).  Measured: 200 rows of 16 tiles, 16 heads, cut
+    // 43.5 us, whole 45.8; 64 heads 81.8 and 59.9; 64 heads, 64 rows of 8 tiles
+    // 35.9 and 19.7, of 32 tiles 51.6 and 54.0.
+    const int64_t join = s.N == 64 ? 12 : 9;
+    const int64_t whole = (items + g - 1) / g * nt, cut = (items * nt + g - 1) / g + join;
     s.split = cut < whole ? 1 : 0;
-    const int64_t n = s.split ? items * nt : items;
+    const int64_t n = s.split ? (items * nt + kMinRun - 1) / kMinRun : items;
     s.ctas = static_cast<int>(n < g ? n : g);
     return s;
 }
@@ -780,7 +817,7 @@ cudaError_t launch_n(const Params& p, const CUtensorMap& ql, const CUtensorMap& 
     kt_mark(st);
     if (e != cudaSuccess || !p.split) return e;
     cfg.gridDim = dim3(static_cast<unsigned>(p.rows), static_cast<unsigned>(p.heads), 1);
-    cfg.blockDim = dim3(128, 1, 1);
+    cfg.blockDim = dim3(kJoinThreads, 1, 1);
     cfg.dynamicSmemBytes = 0;
     kt_mark(st);
     e = cudaLaunchKernelEx(&cfg, join_kernel, p, N, ctas);
