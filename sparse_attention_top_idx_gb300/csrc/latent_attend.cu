@@ -658,23 +658,21 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
-// Joins the partial sums of the rows that were cut: one CTA a (row, head).
-// Thread i finds piece i's factor, then eight warps take the pieces in turn,
-// four of them in flight, lanes over the latent dimensions; the warps' sums are
-// added in order.
-constexpr int kJoinThreads = 256;
-static_assert(kMaxCtas <= kJoinThreads, "a thread a piece");
+// Joins the partial sums of the rows that were cut.  kW warps take the pieces
+// of a (row, head) in turn, four of them in flight, lanes over the latent
+// dimensions; the warps' sums are added in order.  A CTA has eight warps.
+constexpr int kJoinWarps = 8;
 
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const Params p, int N, int ctas) {
-    constexpr int kWarps = kJoinThreads / 32;
-    __shared__ float acc[kWarps][IDX_LATENT_DIM];
-    __shared__ float fac[kJoinThreads], red[2][kWarps];
-    __shared__ int from[kJoinThreads];
+template <int kW>
+__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const Params p, int N, int ctas) {
+    __shared__ float acc[kW > 1 ? kJoinWarps : 1][IDX_LATENT_DIM];
+    __shared__ float sums[kJoinWarps];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int64_t row = blockIdx.x;
-    const int head = blockIdx.y, hg = head / 64, h = head % 64;
-    const int warp = warp_id(), lane = lane_id(), tid = threadIdx.x;
+    const int warp = warp_id(), lane = lane_id(), wh = warp % kW;
+    const int head = blockIdx.y * (kJoinWarps / kW) + warp / kW, hg = head / 64, h = head % 64;
+    const bool live = head < p.heads;
     int64_t a, tt;
     const int nt = tiles_of(row_keys(p, row));
     if (p.block_table == nullptr) {
@@ -701,74 +699,77 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Params p, int 
     while (run_start(c0 + 1, ctas, tt) <= a) ++c0;
     c1 = (b - 1) * ctas / tt;
     while (run_start(c1 + 1, ctas, tt) < b) ++c1;
-    if (c0 == c1) return;      // it wrote the result
-    const int pieces = static_cast<int>(c1 - c0) + 1;
-    // a run may be empty; the row is the second piece of its first CTA unless
-    // it begins with that CTA's run
-    float m = kNone;
-    float2 ml = make_float2(kNone, 0.0f);
-    if (tid < pieces) {
-        const int64_t c = c0 + tid, start = run_start(c, ctas, tt);
-        if (start < run_start(c + 1, ctas, tt)) {
-            from[tid] = static_cast<int>(2 * c + (start < a ? 1 : 0));
-            ml = p.part_ml[static_cast<int64_t>(from[tid]) * N + h];
-            if (ml.y != 0.0f) m = ml.x;
-        }
-    }
-    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
-    if (lane == 0) red[0][warp] = m;
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < kWarps; ++k) m = fmaxf(m, red[0][k]);
-    const float mine = ml.y != 0.0f ? exp2_fast(ml.x - m) : 0.0f;
-    fac[tid] = mine;
-    float l = mine != 0.0f ? ml.y * mine : 0.0f;
-    for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(~0u, l, d);
-    if (lane == 0) red[1][warp] = l;
-    __syncthreads();
+    // (one CTA: it wrote the result.)  A run may be empty; the row is the second
+    // piece of its first CTA unless it begins with that CTA's run.
+    const bool cut = live && c0 != c1;
+    auto piece = [&](int64_t c) -> int64_t {
+        const int64_t start = run_start(c, ctas, tt);
+        return start < run_start(c + 1, ctas, tt) ? (2 * c + (start < a ? 1 : 0)) * N + h : -1;
+    };
+    float m = kNone, l = 0.0f;
     float4 o[4] = {};
-    for (int k0 = warp; k0 < pieces; k0 += 4 * kWarps) {
-        float4 v[4][4];
-        float f[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int k = k0 + u * kWarps;
-            f[u] = k < pieces ? fac[k] : 0.0f;
-            if (f[u] == 0.0f) continue;
-            const float4* src =
-                reinterpret_cast<const float4*>(p.part_o + (static_cast<int64_t>(from[k]) * N + h) * IDX_LATENT_DIM);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) v[u][q] = __ldg(src + 32 * q + lane);
+    if (cut) {
+        for (int64_t c = c0 + lane; c <= c1; c += 32) {
+            const int64_t s = piece(c);
+            const float2 ml = s >= 0 ? p.part_ml[s] : make_float2(kNone, 0.0f);
+            if (ml.y != 0.0f) m = fmaxf(m, ml.x);
         }
+        for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
+        for (int64_t cb = c0 + wh; cb <= c1; cb += 4 * kW) {
+            float4 v[4][4];
+            float2 ml[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            if (f[u] == 0.0f) continue;
+            for (int u = 0; u < 4; ++u) {
+                const int64_t c = cb + u * kW, s = c <= c1 ? piece(c) : -1;
+                ml[u] = make_float2(kNone, 0.0f);
+                if (s < 0) continue;
+                ml[u] = p.part_ml[s];
+                const float4* src = reinterpret_cast<const float4*>(p.part_o + s * IDX_LATENT_DIM);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                o[q].x += v[u][q].x * f[u];
-                o[q].y += v[u][q].y * f[u];
-                o[q].z += v[u][q].z * f[u];
-                o[q].w += v[u][q].w * f[u];
+                for (int q = 0; q < 4; ++q) v[u][q] = __ldg(src + 32 * q + lane);
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                if (ml[u].y == 0.0f) continue;
+                const float f = exp2_fast(ml[u].x - m);
+                l += ml[u].y * f;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    o[q].x += v[u][q].x * f;
+                    o[q].y += v[u][q].y * f;
+                    o[q].z += v[u][q].z * f;
+                    o[q].w += v[u][q].w * f;
+                }
             }
         }
     }
+    if constexpr (kW > 1) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) reinterpret_cast<float4*>(acc[warp])[32 * q + lane] = o[q];
-    __syncthreads();
-    float total = 0.0f;
+        for (int q = 0; q < 4; ++q) reinterpret_cast<float4*>(acc[warp])[32 * q + lane] = o[q];
+        if (lane == 0) sums[warp] = l;
+        __syncthreads();
+        if (wh != 0) return;
 #pragma unroll
-    for (int k = 0; k < kWarps; ++k) total += red[1][k];
-    const float inv = total == 0.0f ? 0.0f : __fdiv_rn(1.0f, total);
-    const int d = 2 * tid;
-    float2 v = make_float2(0.0f, 0.0f);
+        for (int k = 1; k < kW; ++k) {
+            l += sums[warp + k];
 #pragma unroll
-    for (int k = 0; k < kWarps; ++k) {
-        v.x += acc[k][d];
-        v.y += acc[k][d + 1];
+            for (int q = 0; q < 4; ++q) {
+                const float4 v = reinterpret_cast<const float4*>(acc[warp + k])[32 * q + lane];
+                o[q].x += v.x;
+                o[q].y += v.y;
+                o[q].z += v.z;
+                o[q].w += v.w;
+            }
+        }
     }
-    *reinterpret_cast<uint32_t*>(p.out + (row * p.heads + head) * IDX_LATENT_DIM + d) = bf16x2(v.x * inv, v.y * inv);
-    if (tid == 0 && p.lse != nullptr)
-        p.lse[row * p.heads + head] = total == 0.0f ? -INFINITY : (m + log2f(total)) * 0.69314718055994531f;
+    if (!cut) return;
+    const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
+    uint2* out = reinterpret_cast<uint2*>(p.out + (row * p.heads + head) * IDX_LATENT_DIM);
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        out[32 * q + lane] = make_uint2(bf16x2(o[q].x * inv, o[q].y * inv), bf16x2(o[q].z * inv, o[q].w * inv));
+    if (lane == 0 && p.lse != nullptr)
+        p.lse[row * p.heads + head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
 }
 
 // Heads of one score product.
@@ -816,11 +817,17 @@ cudaError_t launch_n(const Params& p, const CUtensorMap& ql, const CUtensorMap& 
     e = cudaLaunchKernelEx(&cfg, attend_kernel<N>, ql, qp, p);
     kt_mark(st);
     if (e != cudaSuccess || !p.split) return e;
-    cfg.gridDim = dim3(static_cast<unsigned>(p.rows), static_cast<unsigned>(p.heads), 1);
-    cfg.blockDim = dim3(kJoinThreads, 1, 1);
+    // warps a (row, head): eight where rows have many pieces, else as many as
+    // there is parallelism for.  Measured: 9 rows to 75 pieces, 16 heads, whole
+    // call 403 us with one warp, 369 with eight; 32 rows of 3.4 pieces, 128
+    // heads, 46 us with one, 57 with four, 74 with eight; 32 rows of 4.8
+    // pieces, 16 heads, 58.6, 55.1 and 58.0 us.
+    const int warps = ctas > 6 * p.rows * p.hgs ? 8 : p.rows * p.heads <= 1024 ? 4 : 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(p.rows), static_cast<unsigned>((p.heads * warps + kJoinWarps - 1) / kJoinWarps), 1);
+    cfg.blockDim = dim3(32 * kJoinWarps, 1, 1);
     cfg.dynamicSmemBytes = 0;
     kt_mark(st);
-    e = cudaLaunchKernelEx(&cfg, join_kernel, p, N, ctas);
+    e = cudaLaunchKernelEx(&cfg, warps == 8 ? join_kernel<8> : warps == 4 ? join_kernel<4> : join_kernel<1>, p, N, ctas);
     kt_mark(st);
     return e;
 }
