@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(kExpThreads, 1)
                 mma_commit(pv_done + t);
                 return true;
             };
-            bool ok = (n0 == 0 || scores(0, 0)) && (n1 == 0 || scores(1, 0));
+            bool ok = mbar_wait(q_full, 0, p.status, abort_flag) && (n0 == 0 || scores(0, 0)) && (n1 == 0 || scores(1, 0));
             for (int i = 0; i < n && ok; ++i) {
                 if (i < n0) ok = values(0, i);
                 if (ok && i + 1 < n0) ok = scores(0, i + 1);

@@ -535,3 +535,32 @@ def test_expanded_status_and_stream():
     out, lse = expanded_call(q, k, pe, v, cuq, bad, expect=5)
     check_expanded(out[:50], lse[:50], q[:50], k[:50], pe[:50], v[:50], [50], [50])
     assert bool(out[50:].isnan().all())
+
+
+def test_expanded_repeats_bit_for_bit():
+    """Many CTAs at once, cold and warm: nothing may depend on when a copy lands."""
+    g = gen(35)
+    q, k, pe, v, cuq, cuk = expanded_inputs(g, [1500, 300], [9000, 300], 16)
+    first = expanded_call(q, k, pe, v, cuq, cuk)
+    assert bool(first[0].isfinite().all()) and bool(first[1].isfinite().all())
+    flush = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    for i in range(20):
+        if i % 2:
+            flush.zero_()
+        out, lse = expanded_call(q, k, pe, v, cuq, cuk)
+        assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+
+
+def test_attend_repeats_bit_for_bit_cold():
+    g = gen(36)
+    pool = normal(g, 300, 64, REC)
+    ql, qp = queries(g, 400, 128)
+    slots = torch.randint(0, 300 * 64, (400, 512), generator=g, device="cuda")
+    cache = latent.LatentCache(pool)
+    first = slots_call(cache, ql, qp, slots)
+    flush = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    for i in range(20):
+        if i % 2:
+            flush.zero_()
+        out, lse = slots_call(cache, ql, qp, slots)
+        assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
