@@ -1,11 +1,11 @@
 // rope.cu -- idx_rope: rotary positions on part of every head.
 //
 // Bound by memory: each element is read and written once, so everything else
-// is kept off the path.  Block shape: x covers the work items of one head (a
-// vector of up to 16 bytes; with pairs half a head apart a vector and its
-// partner together, so that a turn in place has one owner), y the heads of one
-// token, or of several where there are few heads.  A thread keeps its item
-// and token, so the cosines and sines it needs sit in registers for all its
+// is kept off the path.  A CTA takes the heads of one token, or of several
+// where there are few heads; a thread takes one work item of a head (a vector
+// of up to 16 bytes; with pairs half a head apart a vector and its partner
+// together, so that a turn in place has one owner) and keeps it and its token
+// over all its heads, so the cosines and sines it needs sit in registers for all its
 // heads and its addresses advance by one stride; the CTA computes each pair's
 // once (one integer multiply and one sincospi), while the first heads' values
 // are on their way.
@@ -20,8 +20,9 @@ namespace dsaidx {
 
 namespace {
 
-// 128 threads: 8192 x 64 heads x 128, half of each turned in halves, 56 us
-// (4.8 TB/s); 256 threads 58 us.  4000 x 64 x 192 interleaved 36 us against 40.
+// Most threads of a CTA.  8192 x 64 heads x 128, half of each turned in halves:
+// 52 us (5.1 TB/s) with 96 of 128, 56 with 192 of 256; 4000 x 64 x 192
+// interleaved 36 us against 40.
 constexpr int kRopeThreads = 128;
 
 template <class T> __device__ __forceinline__ float to_f32(T v) { return static_cast<float>(v); }
@@ -44,7 +45,7 @@ struct RopeParams {
     int heads, head_dim, rot, offset, items;
     int rot_items;         // of the items: rotated ones first, then copies
     int step, dist;        // split pairs: elements from item to item, from a to b
-    int tok_cta, hy;       // tokens a CTA, heads of a token next to each other in y
+    int tok_cta, hy;       // tokens a CTA, heads of a token taken at once
     int heads_cta;         // heads a CTA (blockIdx.y)
     float amplitude;
     float sign;            // -1: the transposed map
@@ -60,13 +61,23 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
     using V = Vec<T, kVec>;
     constexpr int kPairs = kSplit ? kVec : kVec / 2;
     // heads in flight a thread; two vectors of a split pair are enough (two
-    // heads of them: 68 us in the case above, for want of registers)
+    // heads of them: 59 us in the case above, for want of registers)
     constexpr int kRopeHeads = kSplit ? 1 : 2;
     const int np = p.rot >> 1;
     const int64_t tok0 = static_cast<int64_t>(blockIdx.x) * p.tok_cta;
     const int toks = static_cast<int>(p.tokens - tok0 < p.tok_cta ? p.tokens - tok0 : p.tok_cta);
-    const int tl = threadIdx.y / p.hy;
-    const int h0 = blockIdx.y * p.heads_cta + threadIdx.y - tl * p.hy;
+    // item and head of this thread: the rotated items of all heads first, so
+    // that few warps hold both kinds
+    int item = threadIdx.x, ty = 0;
+    if (p.items <= kRopeThreads) {
+        const int first = p.rot_items * p.hy * p.tok_cta;
+        const bool copies = item >= first;
+        const int n = copies ? p.items - p.rot_items : p.rot_items, i = copies ? item - first : item;
+        ty = i / n;
+        item = i - ty * n + (copies ? p.rot_items : 0);
+    }
+    const int tl = ty / p.hy;
+    const int h0 = blockIdx.y * p.heads_cta + ty - tl * p.hy;
     const int h1 = tl < toks ? min(p.heads, (static_cast<int>(blockIdx.y) + 1) * p.heads_cta) : 0;
     const T* x = static_cast<const T*>(p.x) + (tok0 + tl) * p.xt;
     T* y = static_cast<T*>(p.y) + (tok0 + tl) * p.yt;
@@ -91,9 +102,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
         }
     };
     // the first values are on their way while the table is made
-    int item = threadIdx.x;
     load(item, h0);
-    for (int i = threadIdx.y * blockDim.x + threadIdx.x; i < toks * np; i += blockDim.x * blockDim.y) {
+    for (int i = threadIdx.x; i < toks * np; i += blockDim.x) {
         const int tk = i / np, k = i - tk * np;
         float2 v = rope_cs(p.pos[tok0 + tk], p.steps[k], p.amplitude);
         v.y *= p.sign;
@@ -133,7 +143,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
                 *reinterpret_cast<V*>(dst) = a[u];
             }
         }
-        item += blockDim.x;
+        item += kRopeThreads;            // a head of more items than threads
         if (item >= p.items) break;
         load(item, h0);
     }
@@ -145,10 +155,15 @@ cudaError_t launch_rope_t(RopeParams p, bool half, bool inplace, int sms, cudaSt
     p.dist = half ? p.rot / 2 : 1;
     p.rot_items = kSplit ? p.rot / 2 / kVec : p.rot / kVec;
     p.items = p.rot_items + (inplace ? 0 : (p.head_dim - p.rot) / kVec);
-    const int bx = p.items < kRopeThreads ? p.items : kRopeThreads, most = kRopeThreads / bx;
-    // y: the heads of a token in equal rounds, or several tokens' heads
-    const int rounds = (p.heads + most - 1) / most;
-    p.hy = (p.heads + rounds - 1) / rounds;
+    const int most = p.items < kRopeThreads ? kRopeThreads / p.items : 1;
+    // the heads of a token in rounds of hy, or several tokens' heads: the largest
+    // hy that leaves the fewest threads idle in the last round, not below two
+    // thirds of the CTA (64 heads of 12 items: 8 rounds of 8 heads 52 us, 7 of
+    // 10 57 us)
+    p.hy = p.heads < most ? p.heads : most;
+    for (int hy = p.hy - 1; hy >= 1 && 3 * hy >= 2 * most; --hy)
+        if ((p.heads + hy - 1) / hy * hy < (p.heads + p.hy - 1) / p.hy * p.hy) p.hy = hy;
+    const int rounds = (p.heads + p.hy - 1) / p.hy;
     p.tok_cta = most / p.hy;
     if (p.tok_cta > p.tokens) p.tok_cta = static_cast<int>(p.tokens);
     // few tokens: their heads go to several CTAs, down to one round each
@@ -159,7 +174,8 @@ cudaError_t launch_rope_t(RopeParams p, bool half, bool inplace, int sms, cudaSt
     if (groups >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(groups), static_cast<unsigned>((p.heads + p.heads_cta - 1) / p.heads_cta), 1);
-    cfg.blockDim = dim3(static_cast<unsigned>(bx), static_cast<unsigned>(p.hy * p.tok_cta), 1);
+    const int threads = p.items < kRopeThreads ? p.items * p.hy * p.tok_cta : kRopeThreads;
+    cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
     cfg.dynamicSmemBytes = static_cast<size_t>(p.tok_cta) * (p.rot / 2) * sizeof(float2);   // at most 16 KB
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
