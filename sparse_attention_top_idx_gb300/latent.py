@@ -127,10 +127,13 @@ class RopePlan:
         self.steps = steps
         self.amplitude = amplitude
         self.rot_dim = 2 * steps.numel()
+        self._address = _dense(steps, torch.int64, "plan.steps") if steps.is_cuda else None
 
     def on_device(self) -> int:
         """Address of the steps; they have to be in device memory."""
-        return _dense(self.steps, torch.int64, "plan.steps")
+        if self._address is None:
+            raise TypeError("plan.steps must be a CUDA tensor")
+        return self._address
 
 
 def rope_steps(rot_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
@@ -161,17 +164,24 @@ def rope(x: torch.Tensor, positions: torch.Tensor, plan: RopePlan, layout: int =
     position [tokens] int64; into out (which gets the other elements too) or
     in place.  transpose=True applies the transposed map: the gradient of the
     turn with respect to x, given the gradient of its result."""
-    if x.dim() != 3 or x.dtype not in _DTYPE:
+    dtype, shape = x.dtype, x.shape
+    code = _DTYPE.get(dtype)
+    if code is None or len(shape) != 3:
         raise TypeError("x must be [tokens, heads, head_dim] of bfloat16, float16 or float32")
-    if layout not in (INTERLEAVED, HALF):
+    if layout != INTERLEAVED and layout != HALF:
         raise ValueError("layout must be INTERLEAVED or HALF")
-    T, H, D = shape = x.shape
-    out = x if out is None else out
-    xp, xs = _strided(x, x.dtype, "x", shape)
-    yp, ys = _strided(out, x.dtype, "out", shape)
-    _check(load().idx_rope(xp, xs[0], xs[1], yp, ys[0], ys[1], _DTYPE[x.dtype], T, H, D,
-                           _dense(positions, torch.int64, "positions", (T,)), plan.on_device(), plan.rot_dim, offset,
-                           plan.amplitude, layout | _TRANSPOSE if transpose else layout, _stream(stream)), "idx_rope")
+    T, H, D = shape
+    xp, xs = _strided(x, dtype, "x", shape)
+    if out is None:
+        out, yp, ys = x, xp, xs
+    else:
+        yp, ys = _strided(out, dtype, "out", shape)
+    err = (_bound or load()).idx_rope(xp, xs[0], xs[1], yp, ys[0], ys[1], code, T, H, D,
+                                      _dense(positions, torch.int64, "positions", (T,)), plan.on_device(),
+                                      plan.rot_dim, offset, plan.amplitude, layout | _TRANSPOSE if transpose else layout,
+                                      _stream(stream))
+    if err:
+        raise IdxError(err, "idx_rope")
     return out
 
 
@@ -202,7 +212,7 @@ def latent_append(cache: LatentCache, latent: torch.Tensor, k_pe: torch.Tensor, 
     n = latent.shape[0]
     lp, ls = _strided(latent, torch.bfloat16, "latent", (n, LATENT_DIM))
     kp, ks = _strided(k_pe, torch.bfloat16, "k_pe", (n, PE_DIM))
-    if layout not in (INTERLEAVED, HALF):
+    if layout != INTERLEAVED and layout != HALF:
         raise ValueError("layout must be INTERLEAVED or HALF")
     pos = steps = None
     amplitude = 1.0
@@ -210,10 +220,12 @@ def latent_append(cache: LatentCache, latent: torch.Tensor, k_pe: torch.Tensor, 
         if plan.rot_dim != PE_DIM:
             raise ValueError("plan must turn %d elements" % PE_DIM)
         pos, steps, amplitude = _dense(positions, torch.int64, "positions", (n,)), plan.on_device(), plan.amplitude
-    _check(load().idx_latent_append(cache.desc, lp, ls[0], kp, ks[0], pos,
-                                    _dense(slot_mapping, torch.int64, "slot_mapping", (n,)), n, steps, amplitude,
-                                    layout, _maybe(status, torch.int32, "status"), _stream(stream)),
-           "idx_latent_append")
+    err = (_bound or load()).idx_latent_append(cache.desc, lp, ls[0], kp, ks[0], pos,
+                                               _dense(slot_mapping, torch.int64, "slot_mapping", (n,)), n, steps,
+                                               amplitude, layout, _maybe(status, torch.int32, "status"),
+                                               _stream(stream))
+    if err:
+        raise IdxError(err, "idx_latent_append")
 
 
 def workspace_bytes(rows: int, heads: int, max_keys: int) -> int:
