@@ -37,7 +37,10 @@
 //
 // Few rows over many keys: the tiles of all rows form one line that is cut
 // into equal runs, one a CTA; a row that is cut leaves partial sums (fp32) in
-// the workspace, which a second kernel joins in the order of the keys.
+// the workspace, which a second kernel joins in the order of the keys.  Few
+// rows over few keys: the CTAs of a cluster share a row's tiles, leave their
+// partial sums in shared memory and join each other's, a share of the heads
+// each, through it.
 #include <cuda_bf16.h>
 
 #include <cmath>
@@ -91,7 +94,7 @@ struct Params {
     const int32_t* seq_lens;
     int64_t rows, num_slots;
     int block_size, mbps, heads, hgs, max_keys;
-    int split;                 // tiles of all rows in equal runs (else whole rows)
+    int split;                 // 0: whole rows; 1: the tiles of all rows in equal runs; 2: a row's tiles over a cluster
     int ql_swap, qp_swap;      // the map's middle dimension is the row
     const uint8_t* pool;
     float scale_log2;
@@ -146,18 +149,28 @@ __device__ __forceinline__ void find_row(const Params& p, int64_t x, int64_t& ro
 struct Work {
     int64_t row;
     int hg, keys, t0, t1;
-    int slot;       // where its partial sums go; -1: it has all tiles, write the result
+    int slot;       // where its partial sums go; -1: it has all tiles, write the result; -2: the cluster joins
 };
 
 // The pieces of this CTA, in order; every role walks them by itself.
 struct Walk {
     int64_t pos, end;        // split: the run left; whole: item and number of items
-    int64_t row, base;       // split, paged: current row and where it begins
+    int64_t row, base;       // split, paged: current row and where it begins; cluster: row and head group
     bool first;
     __device__ __forceinline__ Walk(const Params& p, int64_t start, int64_t end_, int64_t row_, int64_t base_)
         : pos(start), end(end_), row(row_), base(base_), first(true) {}
     __device__ __forceinline__ bool next(const Params& p, Work& w) {
         if (pos >= end) return false;
+        if (p.split == 2) {
+            w.row = row;
+            w.hg = static_cast<int>(base);
+            w.keys = row_keys(p, row);
+            w.t0 = static_cast<int>(pos);
+            w.t1 = static_cast<int>(end);
+            w.slot = -2;
+            pos = end;
+            return true;
+        }
         if (!p.split) {
             w.row = pos / p.hgs;
             w.hg = static_cast<int>(pos - w.row * p.hgs);
@@ -224,7 +237,7 @@ __device__ __forceinline__ int key_slot(const Params& p, int keys, int j, int64_
     return static_cast<int>(s);
 }
 
-template <int N>
+template <int N, int kCl>
 __global__ void __launch_bounds__(kAttThreads, 1)
     attend_kernel(const __grid_constant__ CUtensorMap ql_map, const __grid_constant__ CUtensorMap qp_map,
                   const Params p) {
@@ -284,7 +297,14 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (warp == 2) {
         int64_t start, end, row = 0, base = 0;
-        if (!p.split) {
+        if (kCl > 1) {
+            const int item = blockIdx.x / kCl, rank = blockIdx.x % kCl;
+            row = item / p.hgs;
+            base = item % p.hgs;
+            const int64_t nt = tiles_of(row_keys(p, row));
+            start = rank * nt / kCl;
+            end = (rank + 1) * nt / kCl;
+        } else if (!p.split) {
             start = blockIdx.x;
             end = p.rows * p.hgs;
         } else {
@@ -596,6 +616,28 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                     if (sw == 0 && kr == 0) stat[4 * N + 8 * r + 2 * quad + e] = mx[r][e];
                 }
             if (named_any<1, kSoftThreads>(!ok)) { ok = false; break; }
+            if constexpr (kCl > 1) {
+                // this CTA's share to its own shared memory (the ring's loads
+                // are all consumed): statistics, then the accumulators [head][512]
+                float2 ml = make_float2(0.0f, 0.0f);
+                if (tid < N) ml = make_float2(stat[4 * N + tid], stat[tid] + stat[N + tid] + stat[2 * N + tid] + stat[3 * N + tid]);
+                named_sync<1, kSoftThreads>();
+                if (tid < N) reinterpret_cast<float2*>(stat)[tid] = ml;
+                float* share = reinterpret_cast<float*>(smem + kPlan.ring_off) + 32 * sw + lane;
+#pragma unroll 1
+                for (int hc = 0; hc < N; hc += 16) {
+                    uint32_t v[4][16];
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) tmem_ld16_nowait(tmem + lanes + m * N + hc, v[m]);
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) {
+                        tmem_wait_ld16(v[m]);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) share[(hc + j) * IDX_LATENT_DIM + 128 * m] = __uint_as_float(v[m][j]);
+                    }
+                }
+                break;      // a cluster's CTA has one piece
+            }
             const int h0 = w.hg * 64;
             if (tid < N) {
                 const float l = stat[tid] + stat[N + tid] + stat[2 * N + tid] + stat[3 * N + tid];
@@ -651,11 +693,55 @@ __global__ void __launch_bounds__(kAttThreads, 1)
             mbar_arrive(o_empty);
             named_sync<1, kSoftThreads>();   // the statistics' memory is reused
         }
+        // a share without tiles
+        if (kCl > 1 && it == 0 && tid < N) reinterpret_cast<float2*>(stat)[tid] = make_float2(kNone, 0.0f);
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     if (warp == 1) tmem_dealloc(tmem, 512);
+    if constexpr (kCl > 1) {
+        // ---- join: N / kCl heads a CTA, every thread ----
+        constexpr int kShare = N / kCl;
+        const int rank = static_cast<int>(cluster_rank());
+        cluster_arrive();
+        cluster_wait();
+        const int64_t row = sh_run[2];
+        const int h0 = static_cast<int>(sh_run[3]) * 64;
+        for (int i = threadIdx.x; i < kShare * (IDX_LATENT_DIM / 4); i += kAttThreads) {
+            const int h = rank * kShare + i / (IDX_LATENT_DIM / 4), d = 4 * (i % (IDX_LATENT_DIM / 4));
+            if (h0 + h >= p.heads) continue;
+            float2 ml[kCl];
+            float4 v[kCl];
+            float m = kNone, l = 0.0f;
+#pragma unroll
+            for (int r = 0; r < kCl; ++r) {
+                const uint2 b = dsmem_ld_v2(dsmem_addr(stat + 2 * h, r));
+                ml[r] = make_float2(__uint_as_float(b.x), __uint_as_float(b.y));
+                v[r] = dsmem_ld_f4(dsmem_addr(smem + kPlan.ring_off + (h * IDX_LATENT_DIM + d) * 4, r));
+                if (ml[r].y != 0.0f) m = fmaxf(m, ml[r].x);
+            }
+            float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int r = 0; r < kCl; ++r) {
+                if (ml[r].y == 0.0f) continue;      // nothing there: neither are its sums
+                const float f = exp2_fast(ml[r].x - m);
+                l += ml[r].y * f;
+                o.x += v[r].x * f;
+                o.y += v[r].y * f;
+                o.z += v[r].z * f;
+                o.w += v[r].w * f;
+            }
+            const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
+            const int64_t at = row * p.heads + h0 + h;
+            *reinterpret_cast<uint2*>(p.out + at * IDX_LATENT_DIM + d) =
+                make_uint2(bf16x2(o.x * inv, o.y * inv), bf16x2(o.z * inv, o.w * inv));
+            if (d == 0 && p.lse != nullptr) p.lse[at] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+        }
+        // nobody leaves while another still reads its share
+        cluster_arrive();
+        cluster_wait();
+    }
 }
 
 // Joins the partial sums of the rows that were cut.  kW warps take the pieces
@@ -775,48 +861,72 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const Params p, i
 // Heads of one score product.
 int width_of(int heads) { return heads <= 16 ? 16 : heads <= 32 ? 32 : 64; }
 
-// Whether the rows are cut, and the number of CTAs.
+// How the rows are spread over CTAs.
 struct Shape {
-    int N, hgs, split, ctas;
+    int N, hgs, split, ctas, cluster;
 };
-Shape shape_of(int64_t rows, int heads, int64_t max_keys) {
+Shape shape_of(int64_t rows, int heads, int64_t max_keys, bool paged) {
     Shape s{};
     s.N = width_of(heads);
     s.hgs = (heads + 63) / 64;
+    s.cluster = 1;
     const int64_t g = kMaxCtas;
     const int64_t items = rows * s.hgs, nt = max_keys > 0 ? (max_keys + kKeys - 1) / kKeys : 1;
-    // Whole rows: ceil(items / g) rounds of nt tiles.  Cut: items nt / g tiles,
-    // plus storing and joining partial sums, which costs about as much as 9
-    // tiles (12 of 64 heads).  Measured: 200 rows of 16 tiles, 16 heads, cut
-    // 43.5 us, whole 45.8; 64 heads 81.8 and 59.9; 64 heads, 64 rows of 8 tiles
-    // 35.9 and 19.7, of 32 tiles 51.6 and 54.0.
+    // Tiles one CTA passes, and what joining costs in tiles.  Whole rows:
+    // ceil(items / g) rounds of nt.  Clusters of c, while all fit at once (of
+    // eight: 64 CTAs; 16 rows of 8 tiles took 25.8 us in eights, 13.7 in fours,
+    // 18.5 whole): 1 tile; 64 rows of 32 tiles, 64 heads, 35 us in pairs, 45
+    // cut, 54 whole.  Cut: storing and joining partial sums in memory costs
+    // about 9 tiles (12 of 64 heads); 200 rows of 16 tiles, 16 heads, 39 us cut
+    // and 46 whole, 64 heads 82 and 60.  A paged batch is ragged, which the cut
+    // evens out (32 x 4500 / 10000, 16 heads: 55 us, in fours 66), so long
+    // contexts take no clusters.
     const int64_t join = s.N == 64 ? 12 : 9;
-    const int64_t whole = (items + g - 1) / g * nt, cut = (items * nt + g - 1) / g + join;
-    s.split = cut < whole ? 1 : 0;
-    const int64_t n = s.split ? (items * nt + kMinRun - 1) / kMinRun : items;
-    s.ctas = static_cast<int>(n < g ? n : g);
+    int64_t best = (items + g - 1) / g * nt;
+    s.ctas = static_cast<int>(items < g ? items : g);
+    for (int c = 2; c <= 8; c *= 2) {
+        const int64_t cost = (nt + c - 1) / c + 1;
+        if (items * c <= (c == 8 ? 64 : c == 4 ? 128 : g) && c <= nt && cost < best && !(paged && nt > 16)) {
+            best = cost;
+            s.split = 2;
+            s.cluster = c;
+            s.ctas = static_cast<int>(items) * c;
+        }
+    }
+    const int64_t cut = (items * nt + g - 1) / g + join;
+    if (cut < best) {
+        s.split = 1;
+        s.cluster = 1;
+        const int64_t n = (items * nt + kMinRun - 1) / kMinRun;
+        s.ctas = static_cast<int>(n < g ? n : g);
+    }
     return s;
 }
 
-template <int N>
+template <int N, int kCl>
 cudaError_t launch_n(const Params& p, const CUtensorMap& ql, const CUtensorMap& qp, int ctas, cudaStream_t st) {
     static std::atomic<unsigned long long> done{0};
-    cudaError_t e = set_smem_once(attend_kernel<N>, plan_of(N).total, done);
+    cudaError_t e = set_smem_once(attend_kernel<N, kCl>, plan_of(N).total, done);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
     cfg.blockDim = dim3(kAttThreads, 1, 1);
     cfg.dynamicSmemBytes = plan_of(N).total;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = kCl;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
+    cfg.numAttrs = kCl > 1 ? 2 : 1;
+    kt_mark(st);
+    e = cudaLaunchKernelEx(&cfg, attend_kernel<N, kCl>, ql, qp, p);
+    kt_mark(st);
+    if (e != cudaSuccess || p.split != 1) return e;
     cfg.numAttrs = 1;
-    kt_mark(st);
-    e = cudaLaunchKernelEx(&cfg, attend_kernel<N>, ql, qp, p);
-    kt_mark(st);
-    if (e != cudaSuccess || !p.split) return e;
     // warps a (row, head): eight where rows have many pieces, else as many as
     // there is parallelism for.  Measured: 9 rows to 75 pieces, 16 heads, whole
     // call 403 us with one warp, 369 with eight; 32 rows of 3.4 pieces, 128
@@ -832,18 +942,34 @@ cudaError_t launch_n(const Params& p, const CUtensorMap& ql, const CUtensorMap& 
     return e;
 }
 
+template <int N>
+cudaError_t launch_cl(const Params& p, const CUtensorMap& ql, const CUtensorMap& qp, const Shape& s, cudaStream_t st) {
+    switch (s.cluster) {
+        case 2: return launch_n<N, 2>(p, ql, qp, s.ctas, st);
+        case 4: return launch_n<N, 4>(p, ql, qp, s.ctas, st);
+        case 8: return launch_n<N, 8>(p, ql, qp, s.ctas, st);
+        default: return launch_n<N, 1>(p, ql, qp, s.ctas, st);
+    }
+}
+
 }  // namespace
 
 size_t attend_ws_bytes(int64_t rows, int heads, int64_t max_keys) {
-    const Shape s = shape_of(rows, heads, max_keys);
-    if (!s.split) return 256;
-    return 256 + align_up(static_cast<size_t>(2) * s.ctas * s.N * (IDX_LATENT_DIM + 2) * 4, 256);
+    // the same for both sources of keys
+    size_t most = 256;
+    for (const bool paged : {false, true}) {
+        const Shape s = shape_of(rows, heads, max_keys, paged);
+        if (s.split != 1) continue;
+        const size_t need = 256 + align_up(static_cast<size_t>(2) * s.ctas * s.N * (IDX_LATENT_DIM + 2) * 4, 256);
+        if (need > most) most = need;
+    }
+    return most;
 }
 
 cudaError_t launch_attend(const AttendArgs& a, cudaStream_t st) {
     EncodeTiledFn enc = encode_tiled_fn();
     if (!enc) return cudaErrorNotSupported;
-    const Shape s = shape_of(a.rows, a.heads, a.max_keys);
+    const Shape s = shape_of(a.rows, a.heads, a.max_keys, a.block_table != nullptr);
     Params p{};
     p.slots = a.slots; p.slots_stride = a.slots_stride;
     p.block_table = a.block_table; p.seq_lens = a.seq_lens; p.mbps = a.mbps; p.block_size = a.block_size;
@@ -858,9 +984,9 @@ cudaError_t launch_attend(const AttendArgs& a, cudaStream_t st) {
     if (!head_map(&ql, enc, a.ql, IDX_LATENT_DIM, a.ql_row, a.ql_head, a.rows, a.heads, s.N, 1, &p.ql_swap) ||
         !head_map(&qp, enc, a.qp, IDX_LATENT_PE_DIM, a.qp_row, a.qp_head, a.rows, a.heads, s.N, 1, &p.qp_swap))
         return cudaErrorInvalidValue;
-    if (s.N == 16) return launch_n<16>(p, ql, qp, s.ctas, st);
-    if (s.N == 32) return launch_n<32>(p, ql, qp, s.ctas, st);
-    return launch_n<64>(p, ql, qp, s.ctas, st);
+    if (s.N == 16) return launch_cl<16>(p, ql, qp, s, st);
+    if (s.N == 32) return launch_cl<32>(p, ql, qp, s, st);
+    return launch_cl<64>(p, ql, qp, s, st);
 }
 
 }  // namespace dsaidx

@@ -129,6 +129,16 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
     return ok != 0;
 }
 
+// Four floats of any CTA's shared memory (an address of dsmem_addr).
+__device__ __forceinline__ float4 dsmem_ld_f4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
 // Barrier of kCount threads; the second form also gives the OR of a predicate.
 template <int kId, int kCount>
 __device__ __forceinline__ void named_sync() {

@@ -237,7 +237,9 @@ def want_slots(pool, ql, qp, slots, scale=SCALE):
 
 @pytest.mark.parametrize("T,H,topk,kind", [(1, 1, 1, 0), (1, 128, 64, 0), (3, 16, 63, 1), (2, 64, 65, 0), (5, 20, 1000, 1),
                                            (32, 128, 512, 1), (2, 130, 129, 0), (700, 17, 40, 1), (160, 64, 128, 0),
-                                           (4, 33, 2048, 0), (1, 16, 4096, 0), (620, 100, 192, 0)])
+                                           (4, 33, 2048, 0), (1, 16, 4096, 0), (620, 100, 192, 0), (64, 16, 129, 0),
+                                           (64, 30, 300, 1), (30, 128, 577, 0), (16, 64, 512, 0), (8, 5, 1024, 0),
+                                           (3, 32, 700, 1), (70, 40, 128, 0)])
 def test_attend_slots(T, H, topk, kind):
     g = gen(T * 7 + H)
     pool = normal(g, 40, 64, REC)
@@ -349,7 +351,8 @@ def want_paged(pool, ql, qp, slots):
 
 @pytest.mark.parametrize("lens,bs,H", [([1], 64, 16), ([0, 1, 63, 64, 65], 32, 20), ([4500, 10000, 0, 7], 64, 16),
                                        ([129, 257, 2000], 48, 128), ([30000], 64, 64), ([20000, 3], 1, 8),
-                                       ([33] * 300, 32, 16), ([50, 1000] * 400, 64, 4)])
+                                       ([33] * 300, 32, 16), ([50, 1000] * 400, 64, 4), ([0, 1000, 64, 1], 64, 64),
+                                       ([0, 0, 900], 16, 33), ([129] * 20, 64, 128), ([0], 64, 16)])
 def test_attend_paged(lens, bs, H):
     g = gen(sum(lens) + bs)
     pool, table, sl, slots = paged_inputs(g, lens, bs)
