@@ -73,6 +73,6 @@ struct ExpandedArgs {
     float* lse;
     int32_t* status;
 };
-cudaError_t launch_expanded(const ExpandedArgs& a, cudaStream_t st);
+cudaError_t launch_expanded(const ExpandedArgs& a, int sms, cudaStream_t st);
 
 }  // namespace dsaidx

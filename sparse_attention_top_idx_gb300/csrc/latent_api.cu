@@ -208,10 +208,12 @@ idx_status idx_latent_attend_expanded(const void* q_dev, int64_t q_row_stride, i
     if (heads > 1 && q_head_stride < 1) return IDX_ERR_INVALID_ARG;
     if (total_k > 1 && (kn_row_stride < 1 || kp_row_stride < 1 || v_row_stride < 1)) return IDX_ERR_INVALID_ARG;
     if (((total_q + 255) / 256 + batch) * heads >= kInt31) return IDX_ERR_INVALID_ARG;
+    int sms = 0;
+    if (!sm_count(&sms)) return IDX_ERR_CUDA;
     ExpandedArgs a{q_dev, kn_dev, kp_dev, v_dev, q_row_stride, q_head_stride, kn_row_stride, kn_head_stride,
                    kp_row_stride, v_row_stride, v_head_stride, total_q, total_k, cu_seqlens_q_dev, cu_seqlens_k_dev,
                    batch, heads, scale, out_dev, lse_dev, status_dev};
-    return status_of(launch_expanded(a, static_cast<cudaStream_t>(stream)));
+    return status_of(launch_expanded(a, sms, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -58,20 +58,22 @@ struct Params {
     int64_t total_q, total_k;
     int q_swap, kn_swap, kp_swap, v_swap;
     int kn_one, v_one;           // keys / values shared by the heads: head coordinate 0
+    int fold;                    // a CTA takes the j-th query tile from either end of its sequence
     float scale_log2;
     __nv_bfloat16* out;
     float* lse;
     int32_t* status;
 };
 
-// The 256 queries of a CTA: rows q0 .. q0 + nq of sequence keys k0 .. k0 + nk;
-// query r (0..) sees keys 0 .. see0 + r of them.
+// The queries of a CTA: two tiles of a sequence whose queries are rows
+// q0 .. q0 + nq and whose keys are rows k0 .. k0 + nk.  Tile t begins at its
+// query off[t] (off1 < 0: one tile); query r sees keys 0 .. nk - nq + r.
 struct Item {
-    int q0, nq, k0, nk, see0;
+    int q0, nq, k0, nk, off0, off1;
 };
 
-// Query block `block` counted from the last sequence's last block down (later
-// blocks of a sequence see more keys and start first).  False: there are fewer.
+// Block `block` counted from the last sequence's last block down (later blocks
+// of a sequence see more keys and start first).  False: there are fewer.
 // Executed by a whole warp.
 __device__ bool find_item(const Params& p, int block, Item& it) {
     const int lane = lane_id();
@@ -99,11 +101,14 @@ __device__ bool find_item(const Params& p, int block, Item& it) {
             const int before = __shfl_sync(~0u, v - n, src);
             n = __shfl_sync(~0u, n, src);
             const int qb = n - 1 - (left - before);
-            it.q0 = q0 + 2 * kTile * qb;
-            it.nq = min(2 * kTile, q1 - it.q0);
+            it.q0 = q0;
+            it.nq = q1 - q0;
             it.k0 = k0;
             it.nk = k1 - k0;
-            it.see0 = (k1 - k0) - (q1 - q0) + 2 * kTile * qb;
+            const int tiles = (it.nq + kTile - 1) / kTile;
+            const int t0 = p.fold ? qb : 2 * qb, t1 = p.fold ? tiles - 1 - qb : 2 * qb + 1;
+            it.off0 = t0 * kTile;
+            it.off1 = t1 > t0 && t1 < tiles ? t1 * kTile : -1;
             return true;
         }
         left -= __shfl_sync(~0u, v, 31);
@@ -133,7 +138,7 @@ __global__ void __launch_bounds__(kExpThreads, 1)
     uint64_t* v_tail = full + 25;      // the last tile's values are on their way
     uint32_t* sh_tmem = reinterpret_cast<uint32_t*>(full + 26);
     int* sh_abort = reinterpret_cast<int*>(full + 27);
-    int* sh_item = reinterpret_cast<int*>(full + 28);   // found, then the item (6 ints)
+    int* sh_item = reinterpret_cast<int*>(full + 28);   // found, then the item (6 values)
     const int warp = warp_id(), lane = lane_id();
     const int h = blockIdx.x % p.heads, block = blockIdx.x / p.heads;
 
@@ -166,7 +171,8 @@ __global__ void __launch_bounds__(kExpThreads, 1)
             sh_item[2] = it.nq;
             sh_item[3] = it.k0;
             sh_item[4] = it.nk;
-            sh_item[5] = it.see0;
+            sh_item[5] = it.off0;
+            sh_item[6] = it.off1;
         }
     }
     tc_fence_before();
@@ -175,10 +181,11 @@ __global__ void __launch_bounds__(kExpThreads, 1)
     const uint32_t tmem = *sh_tmem;
     volatile int* abort_flag = sh_abort;
     const bool found = sh_item[0] != 0;
-    const Item w{sh_item[1], sh_item[2], sh_item[3], sh_item[4], sh_item[5]};
+    const Item w{sh_item[1], sh_item[2], sh_item[3], sh_item[4], sh_item[5], sh_item[6]};
     // key tiles of the two query tiles: up to the last query's horizon
-    const int rows0 = min(w.nq, kTile), rows1 = w.nq - rows0;
-    const int vis0 = max(0, min(w.nk, w.see0 + rows0)), vis1 = rows1 > 0 ? max(0, min(w.nk, w.see0 + w.nq)) : 0;
+    const bool two = w.off1 >= 0;
+    auto horizon = [&](int off) { return max(0, min(w.nk, w.nk - w.nq + min(w.nq, off + kTile))); };
+    const int vis0 = horizon(w.off0), vis1 = two ? horizon(w.off1) : 0;
     const int n0 = found ? (vis0 + kTile - 1) / kTile : 0, n1 = found ? (vis1 + kTile - 1) / kTile : 0;
     const int n = max(n0, n1);
     // the last tile reaches behind the sequence's keys
@@ -187,10 +194,10 @@ __global__ void __launch_bounds__(kExpThreads, 1)
     if (warp == 1) {
         // ---- loads ----
         if (n > 0 && elect_one()) {
-            mbar_arrive_expect_tx(q_full, (rows1 > 0 ? 6 : 3) * kUnit);
-            for (int t = 0; t < (rows1 > 0 ? 2 : 1); ++t)
+            mbar_arrive_expect_tx(q_full, (two ? 6 : 3) * kUnit);
+            for (int t = 0; t < (two ? 2 : 1); ++t)
                 for (int c = 0; c < 3; ++c) {
-                    const int row = w.q0 + t * kTile;
+                    const int row = w.q0 + (t ? w.off1 : w.off0);
                     tma_tile_3d(smem_u32(smem + kQOff) + (3 * t + c) * kUnit, &q_map, q_full, 64 * c, p.q_swap ? row : h,
                                 p.q_swap ? h : row);
                 }
@@ -227,7 +234,7 @@ __global__ void __launch_bounds__(kExpThreads, 1)
             constexpr uint32_t kIdS = idesc_bf16(kTile, kTile, false, false);
             constexpr uint32_t kIdO = idesc_bf16(kTile, kVal, false, true);
             const uint32_t ring = smem_u32(smem + kRingOff), q_addr = smem_u32(smem + kQOff);
-            const int last = rows1 > 0 ? 1 : 0;      // the tile that reads a unit last
+            const int last = two ? 1 : 0;      // the tile that reads a unit last
             auto scores = [&](int t, int i) -> bool {
 #pragma unroll 1
                 for (int c = 0; c < 3; ++c) {
@@ -288,15 +295,15 @@ __global__ void __launch_bounds__(kExpThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(v_clean);
         }
-    } else if (warp >= 4 && found) {
+    } else if (warp >= 4 && found && (warp < 8 || two)) {
         // ---- softmax of tile t, one query a thread ----
         const int t = (warp - 4) >> 2, sw = warp & 3;
-        const int nt = t ? n1 : n0, row = t * kTile + 32 * sw + lane;
+        const int nt = t ? n1 : n0, off = (t ? w.off1 : w.off0) + 32 * sw, row = off + lane;   // query of the sequence
         const uint32_t lanes = static_cast<uint32_t>(32 * sw) << 16;
         const uint32_t s_col = tmem + lanes + t * kTile, o_col = tmem + lanes + (2 + t) * kTile;
-        const int see = min(w.nk, w.see0 + row + 1);      // keys this query sees (may be <= 0)
+        const int see = min(w.nk, w.nk - w.nq + row + 1);      // keys this query sees (may be <= 0)
         // all 32 queries of the warp see this many
-        const int see_all = min(w.nk, w.see0 + t * kTile + 32 * sw + 1);
+        const int see_all = min(w.nk, w.nk - w.nq + off + 1);
         float m = kNone, l = 0.0f;
         bool ok = true;
         const unsigned long long sc2 = f2_pack(p.scale_log2, p.scale_log2), one2 = f2_pack(1.0f, 1.0f);
@@ -417,7 +424,7 @@ __global__ void __launch_bounds__(kExpThreads, 1)
 
 }  // namespace
 
-cudaError_t launch_expanded(const ExpandedArgs& a, cudaStream_t st) {
+cudaError_t launch_expanded(const ExpandedArgs& a, int sms, cudaStream_t st) {
     EncodeTiledFn enc = encode_tiled_fn();
     if (!enc) return cudaErrorNotSupported;
     Params p{};
@@ -441,6 +448,9 @@ cudaError_t launch_expanded(const ExpandedArgs& a, cudaStream_t st) {
     static std::atomic<unsigned long long> done{0};
     cudaError_t e = set_smem_once(expanded_kernel, kSmem, done);
     if (e != cudaSuccess) return e;
+    // Where no CTA would wait for an SM, the longest one decides: a sequence's
+    // first and last tile together, second and last but one, and so on.
+    p.fold = a.total_q * a.heads <= static_cast<int64_t>(2 * kTile) * sms;
     // at most one partly filled block of queries a sequence
     const int64_t blocks = (a.total_q + 2 * kTile - 1) / (2 * kTile) + a.batch - 1;
     if (blocks * a.heads >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
