@@ -8,9 +8,12 @@
 // tile.  While one tile is in softmax, the tensor cores run the other's
 // products:  PV0(i) QK0(i + 1) PV1(i) QK1(i + 1) ...
 //   warp 0      one lane issues every MMA
-//   warp 1      one lane loads queries, keys and values by TMA: a ring of
-//               eight 16 KB units (128 keys x 64 key values, or 64 keys x 128
-//               values), in the order of their use
+//   warp 1      one lane loads queries, keys and values by TMA into a ring of
+//               eight 16 KB units: three of a tile's keys (128 keys x 64
+//               values), two of its values (64 keys x 128), in the order of
+//               their use.  Keys i + 1 take the units of values i - 1 (and one
+//               of keys i - 1, which are done with before those), values i + 1
+//               those of keys i, so two barriers order all reuse
 //   warp 2      zeroes the values behind a sequence's end in its last tile
 //               (weights there are 0, but 0 * inf is NaN)
 //   warps 4-7 and 8-11   softmax of the two tiles, one query a thread
@@ -127,26 +130,27 @@ __global__ void __launch_bounds__(kExpThreads, 1)
                     const Params p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kBarOff);   // [8]
-    uint64_t* empty = full + kUnits;                                // [8]
-    uint64_t* q_full = full + 16;
-    uint64_t* s_full = full + 17;      // [2]
-    uint64_t* p_full = full + 19;      // [2]
-    uint64_t* pv_done = full + 21;     // [2]
-    uint64_t* v_clean = full + 23;
-    uint64_t* drain = full + 24;
-    uint64_t* v_tail = full + 25;      // the last tile's values are on their way
-    uint32_t* sh_tmem = reinterpret_cast<uint32_t*>(full + 26);
-    int* sh_abort = reinterpret_cast<int*>(full + 27);
-    int* sh_item = reinterpret_cast<int*>(full + 28);   // found, then the item (6 values)
+    uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + kBarOff);   // [2], by tile parity
+    uint64_t* v_full = k_full + 2;     // [2]
+    uint64_t* k_done = k_full + 4;     // [2] both score products of a tile have read its keys
+    uint64_t* v_done = k_full + 6;     // [2]
+    uint64_t* s_full = k_full + 8;     // [2], by query tile
+    uint64_t* pv_done = k_full + 10;   // [2]
+    uint64_t* q_full = k_full + 12;
+    uint64_t* v_clean = k_full + 13;
+    uint64_t* v_tail = k_full + 14;    // the last tile's values are on their way
+    uint64_t* drain = k_full + 15;
+    uint64_t* p_full = k_full + 16;    // [2]
+    uint32_t* sh_tmem = reinterpret_cast<uint32_t*>(k_full + 18);
+    int* sh_abort = reinterpret_cast<int*>(k_full + 19);
+    int* sh_item = reinterpret_cast<int*>(k_full + 20);   // found, then the item (6 values)
     const int warp = warp_id(), lane = lane_id();
     const int h = blockIdx.x % p.heads, block = blockIdx.x / p.heads;
 
     if (warp == 0 && elect_one()) {
-        for (int i = 0; i < 2 * kUnits + 3; ++i) mbar_init(full + i, 1);
+        for (int i = 0; i < 16; ++i) mbar_init(k_full + i, 1);
         mbar_init(p_full, kSoftThreads);
         mbar_init(p_full + 1, kSoftThreads);
-        for (int i = 21; i < 26; ++i) mbar_init(full + i, 1);
         *sh_abort = 0;
         fence_mbar_init();
     }
@@ -203,30 +207,35 @@ __global__ void __launch_bounds__(kExpThreads, 1)
                 }
             const int hk = p.kn_one ? 0 : h, hv = p.v_one ? 0 : h;
             const uint32_t ring = smem_u32(smem + kRingOff);
-            uint32_t u = 0;
             bool ok = true;
-            for (int i = 0; i < n && ok; ++i) {
-                const int row = w.k0 + i * kTile;
-                for (int c = 0; c < 5; ++c, ++u) {
-                    const uint32_t sl = u % kUnits, dst = ring + sl * kUnit;
-                    if (!(ok = mbar_wait(empty + sl, ((u / kUnits) & 1) ^ 1, p.status, abort_flag))) break;
-                    mbar_arrive_expect_tx(full + sl, kUnit);
-                    if (c < 2) {
-                        tma_tile_3d(dst, &kn_map, full + sl, 64 * c, p.kn_swap ? row : hk, p.kn_swap ? hk : row);
-                    } else if (c == 2) {
-                        tma_tile_3d(dst, &kp_map, full + sl, 0, p.kp_swap ? row : 0, p.kp_swap ? 0 : row);
-                    } else {
-                        const int r = row + 64 * (c - 3);
-                        tma_tile_3d(dst, &v_map, full + sl, 0, p.v_swap ? r : hv, p.v_swap ? hv : r);
-                        tma_tile_3d(dst + kUnit / 2, &v_map, full + sl, 64, p.v_swap ? r : hv, p.v_swap ? hv : r);
-                    }
+            int i = 0;
+            for (; i < n; ++i) {
+                const int row = w.k0 + i * kTile, u = 5 * i;
+                auto unit = [&](int c) { return ring + ((u + c) % kUnits) * kUnit; };
+                // (of tile i - 2)
+                if (i >= 2 && !(ok = mbar_wait(v_done + (i & 1), ((i >> 1) & 1) ^ 1, p.status, abort_flag))) break;
+                uint64_t* full = k_full + (i & 1);
+                mbar_arrive_expect_tx(full, 3 * kUnit);
+                for (int c = 0; c < 2; ++c)
+                    tma_tile_3d(unit(c), &kn_map, full, 64 * c, p.kn_swap ? row : hk, p.kn_swap ? hk : row);
+                tma_tile_3d(unit(2), &kp_map, full, 0, p.kp_swap ? row : 0, p.kp_swap ? 0 : row);
+                // (of tile i - 1)
+                if (i >= 1 && !(ok = mbar_wait(k_done + ((i - 1) & 1), ((i - 1) >> 1) & 1, p.status, abort_flag))) break;
+                full = v_full + (i & 1);
+                mbar_arrive_expect_tx(full, 2 * kUnit);
+                for (int c = 0; c < 2; ++c) {
+                    const int r = row + 64 * c;
+                    tma_tile_3d(unit(3 + c), &v_map, full, 0, p.v_swap ? r : hv, p.v_swap ? hv : r);
+                    tma_tile_3d(unit(3 + c) + kUnit / 2, &v_map, full, 64, p.v_swap ? r : hv, p.v_swap ? hv : r);
                 }
             }
-            mbar_arrive(v_tail);
+            if (ok) mbar_arrive(v_tail);
             // copies in flight land before the CTA leaves
             mbar_wait(q_full, 0, p.status, nullptr);
-            for (uint32_t k = u > kUnits ? u - kUnits : 0; k < u; ++k)
-                mbar_wait(full + k % kUnits, (k / kUnits) & 1, p.status, nullptr);
+            for (int j = i > 1 ? i - 2 : 0; j <= i; ++j) {
+                if (j < n && (j < i || !ok)) mbar_wait(k_full + (j & 1), (j >> 1) & 1, p.status, nullptr);
+                if (j < i) mbar_wait(v_full + (j & 1), (j >> 1) & 1, p.status, nullptr);
+            }
         }
     } else if (warp == 0) {
         // ---- every MMA ----
@@ -235,45 +244,58 @@ __global__ void __launch_bounds__(kExpThreads, 1)
             constexpr uint32_t kIdO = idesc_bf16(kTile, kVal, false, true);
             const uint32_t ring = smem_u32(smem + kRingOff), q_addr = smem_u32(smem + kQOff);
             const int last = two ? 1 : 0;      // the tile that reads a unit last
-            auto scores = [&](int t, int i) -> bool {
+            auto scores = [&](int t, int i) {
 #pragma unroll 1
                 for (int c = 0; c < 3; ++c) {
-                    const uint32_t u = 5 * i + c, sl = u % kUnits;
-                    if (!mbar_wait(full + sl, (u / kUnits) & 1, p.status, abort_flag)) return false;
-                    tc_fence_after();
+                    const uint32_t unit = ring + ((5 * i + c) % kUnits) * kUnit;
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         mma_bf16(tmem + t * kTile, sdesc_sw128(q_addr + (3 * t + c) * kUnit + 32 * k),
-                                 sdesc_sw128(ring + sl * kUnit + 32 * k), kIdS, (c | k) != 0 ? 1u : 0u);
-                    if (t == last) mma_commit(empty + sl);
+                                 sdesc_sw128(unit + 32 * k), kIdS, (c | k) != 0 ? 1u : 0u);
                 }
+                if (t == last) mma_commit(k_done + (i & 1));
                 mma_commit(s_full + t);
-                return true;
             };
             auto values = [&](int t, int i) -> bool {
                 if (!mbar_wait(p_full + t, i & 1, p.status, abort_flag)) return false;
-#pragma unroll 1
+                tc_fence_after();
+#pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    const uint32_t u = 5 * i + 3 + c, sl = u % kUnits;
-                    if (!mbar_wait(full + sl, (u / kUnits) & 1, p.status, abort_flag)) return false;
-                    if (tail && i == n - 1 && !mbar_wait(v_clean, 0, p.status, abort_flag)) return false;
-                    tc_fence_after();
+                    const uint32_t unit = ring + ((5 * i + 3 + c) % kUnits) * kUnit;
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         mma_bf16_ts(tmem + (2 + t) * kTile, tmem + t * kTile + 32 * c + 8 * k,
-                                    sdesc_mn_sw128(ring + sl * kUnit + 2048 * k, kUnit / 2), kIdO,
-                                    (i | c | k) != 0 ? 1u : 0u);
-                    if (t == last) mma_commit(empty + sl);
+                                    sdesc_mn_sw128(unit + 2048 * k, kUnit / 2), kIdO, (i | c | k) != 0 ? 1u : 0u);
                 }
+                if (t == last) mma_commit(v_done + (i & 1));
                 mma_commit(pv_done + t);
                 return true;
             };
-            bool ok = mbar_wait(q_full, 0, p.status, abort_flag) && (n0 == 0 || scores(0, 0)) && (n1 == 0 || scores(1, 0));
+            // a key tile's copies are waited for once, by the query tile that
+            // comes first
+            auto keys_in = [&](int i) -> bool {
+                if (!mbar_wait(k_full + (i & 1), (i >> 1) & 1, p.status, abort_flag)) return false;
+                tc_fence_after();
+                return true;
+            };
+            bool ok = mbar_wait(q_full, 0, p.status, abort_flag) && keys_in(0);
+            if (ok) {
+                if (n0 > 0) scores(0, 0);
+                if (n1 > 0) scores(1, 0);
+            }
             for (int i = 0; i < n && ok; ++i) {
-                if (i < n0) ok = values(0, i);
-                if (ok && i + 1 < n0) ok = scores(0, i + 1);
+                ok = mbar_wait(v_full + (i & 1), (i >> 1) & 1, p.status, abort_flag);
+                if (ok && tail && i == n - 1) ok = mbar_wait(v_clean, 0, p.status, abort_flag);
+                if (ok && i < n0) ok = values(0, i);
+                if (ok && i + 1 < n0) {
+                    ok = keys_in(i + 1);
+                    if (ok) scores(0, i + 1);
+                }
                 if (ok && i < n1) ok = values(1, i);
-                if (ok && i + 1 < n1) ok = scores(1, i + 1);
+                if (ok && i + 1 < n1) {
+                    if (i + 1 >= n0) ok = keys_in(i + 1);
+                    if (ok) scores(1, i + 1);
+                }
             }
             mma_commit(drain);
             mbar_wait(drain, 0, p.status, nullptr);
@@ -284,10 +306,9 @@ __global__ void __launch_bounds__(kExpThreads, 1)
             const int keep = w.nk - (n - 1) * kTile;      // rows of the last tile that hold keys
             // only then are the units' earlier uses over and their parity tells
             bool ok = mbar_wait(v_tail, 0, p.status, abort_flag);
+            ok = ok && mbar_wait(v_full + ((n - 1) & 1), ((n - 1) >> 1) & 1, p.status, abort_flag);
             for (int c = 0; c < 2 && ok; ++c) {
-                const uint32_t u = 5 * (n - 1) + 3 + c, sl = u % kUnits;
-                if (!(ok = mbar_wait(full + sl, (u / kUnits) & 1, p.status, abort_flag))) break;
-                uint4* unit = reinterpret_cast<uint4*>(smem + kRingOff + sl * kUnit);
+                uint4* unit = reinterpret_cast<uint4*>(smem + kRingOff + (5 * (n - 1) + 3 + c) % kUnits * kUnit);
                 for (int r = max(0, keep - 64 * c); r < 64; ++r)
                     if (lane < 16) unit[(lane >> 3) * 512 + r * 8 + (lane & 7)] = make_uint4(0, 0, 0, 0);
             }
