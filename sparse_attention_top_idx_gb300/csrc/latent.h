@@ -33,7 +33,7 @@ struct AppendArgs {
     unsigned flags;
     int32_t* status;
 };
-cudaError_t launch_append(const AppendArgs& a, int sms, cudaStream_t st);
+cudaError_t launch_append(const AppendArgs& a, cudaStream_t st);
 
 // Absorbed attention: one row = one query of every head.  Keys come from a
 // slot list (block_table null) or from a paged context.

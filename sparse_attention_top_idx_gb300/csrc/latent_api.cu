@@ -124,11 +124,10 @@ idx_status idx_latent_append(const idx_latent_pool* pool, const void* latent_dev
     if (!aligned(latent_dev, 16) || !aligned(pe_dev, 16) || !mult8(latent_stride) || !mult8(pe_stride) ||
         !aligned(slot_mapping_dev, 8) || !aligned(positions_dev, 8) || !aligned(steps_dev, 8))
         return IDX_ERR_INVALID_ARG;
-    int sms = 0;
-    if (!sm_count(&sms)) return IDX_ERR_CUDA;
+    if ((n + 3) / 4 >= kInt31) return IDX_ERR_INVALID_ARG;
     AppendArgs a{latent_dev, pe_dev, pool->data_dev, positions_dev, slot_mapping_dev, steps_dev, latent_stride,
                  pe_stride, n, pool->num_blocks * pool->block_size, amplitude, flags, status_dev};
-    return status_of(launch_append(a, sms, static_cast<cudaStream_t>(stream)));
+    return status_of(launch_append(a, static_cast<cudaStream_t>(stream)));
 }
 
 size_t idx_latent_workspace_bytes(int64_t rows, int heads, int64_t max_keys) {
