@@ -752,7 +752,8 @@ constexpr int kJoinWarps = 8;
 template <int kW>
 __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const Params p, int N, int ctas) {
     __shared__ float acc[kW > 1 ? kJoinWarps : 1][IDX_LATENT_DIM];
-    __shared__ float sums[kJoinWarps];
+    __shared__ float factor[kJoinWarps][kMaxCtas];     // of each piece, 0 where there is nothing
+    __shared__ int from[kJoinWarps][kMaxCtas];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int64_t row = blockIdx.x;
@@ -788,43 +789,54 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const Params p, i
     // (one CTA: it wrote the result.)  A run may be empty; the row is the second
     // piece of its first CTA unless it begins with that CTA's run.
     const bool cut = live && c0 != c1;
-    auto piece = [&](int64_t c) -> int64_t {
-        const int64_t start = run_start(c, ctas, tt);
-        return start < run_start(c + 1, ctas, tt) ? (2 * c + (start < a ? 1 : 0)) * N + h : -1;
-    };
+    const int pieces = static_cast<int>(c1 - c0) + 1;
     float m = kNone, l = 0.0f;
     float4 o[4] = {};
     if (cut) {
-        for (int64_t c = c0 + lane; c <= c1; c += 32) {
-            const int64_t s = piece(c);
-            const float2 ml = s >= 0 ? p.part_ml[s] : make_float2(kNone, 0.0f);
-            if (ml.y != 0.0f) m = fmaxf(m, ml.x);
+        // every warp looks the pieces up, a lane a piece
+        constexpr int kRounds = (kMaxCtas + 31) / 32;
+        float2 ml[kRounds];
+#pragma unroll
+        for (int r = 0; r < kRounds; ++r) {
+            const int k = 32 * r + lane;
+            ml[r] = make_float2(kNone, 0.0f);
+            if (k >= pieces) continue;
+            const int64_t start = run_start(c0 + k, ctas, tt);
+            if (start == run_start(c0 + k + 1, ctas, tt)) continue;
+            from[warp][k] = static_cast<int>(2 * (c0 + k) + (start < a ? 1 : 0)) * N + h;
+            ml[r] = p.part_ml[from[warp][k]];
+            if (ml[r].y != 0.0f) m = fmaxf(m, ml[r].x);
         }
         for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
-        for (int64_t cb = c0 + wh; cb <= c1; cb += 4 * kW) {
+#pragma unroll
+        for (int r = 0; r < kRounds; ++r) {
+            const float f = ml[r].y != 0.0f ? exp2_fast(ml[r].x - m) : 0.0f;
+            if (f != 0.0f) l += ml[r].y * f;
+            if (32 * r + lane < pieces) factor[warp][32 * r + lane] = f;
+        }
+        for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(~0u, l, d);
+        __syncwarp();
+        for (int k0 = wh; k0 < pieces; k0 += 4 * kW) {
             float4 v[4][4];
-            float2 ml[4];
+            float f[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                const int64_t c = cb + u * kW, s = c <= c1 ? piece(c) : -1;
-                ml[u] = make_float2(kNone, 0.0f);
-                if (s < 0) continue;
-                ml[u] = p.part_ml[s];
-                const float4* src = reinterpret_cast<const float4*>(p.part_o + s * IDX_LATENT_DIM);
+                const int k = k0 + u * kW;
+                f[u] = k < pieces ? factor[warp][k] : 0.0f;
+                if (f[u] == 0.0f) continue;
+                const float4* src = reinterpret_cast<const float4*>(p.part_o + static_cast<int64_t>(from[warp][k]) * IDX_LATENT_DIM);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) v[u][q] = __ldg(src + 32 * q + lane);
             }
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                if (ml[u].y == 0.0f) continue;
-                const float f = exp2_fast(ml[u].x - m);
-                l += ml[u].y * f;
+                if (f[u] == 0.0f) continue;
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    o[q].x += v[u][q].x * f;
-                    o[q].y += v[u][q].y * f;
-                    o[q].z += v[u][q].z * f;
-                    o[q].w += v[u][q].w * f;
+                    o[q].x += v[u][q].x * f[u];
+                    o[q].y += v[u][q].y * f[u];
+                    o[q].z += v[u][q].z * f[u];
+                    o[q].w += v[u][q].w * f[u];
                 }
             }
         }
@@ -832,12 +844,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const Params p, i
     if constexpr (kW > 1) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) reinterpret_cast<float4*>(acc[warp])[32 * q + lane] = o[q];
-        if (lane == 0) sums[warp] = l;
         __syncthreads();
         if (wh != 0) return;
 #pragma unroll
         for (int k = 1; k < kW; ++k) {
-            l += sums[warp + k];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const float4 v = reinterpret_cast<const float4*>(acc[warp + k])[32 * q + lane];
