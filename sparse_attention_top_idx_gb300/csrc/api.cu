@@ -13,6 +13,7 @@
 #include "common.cuh"
 #include "dsaidx.h"
 #include "internal.h"
+#include "tensormap.h"
 
 using dsaidx::align_up;
 

@@ -177,12 +177,6 @@ inline cudaError_t set_smem_once(Kern kern, int bytes, std::atomic<unsigned long
     return e;
 }
 
-// The driver's tensor-map encoder, looked up at run time (null when missing).
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-EncodeTiledFn encode_tiled_fn();
-
 // Kernel launchers (one per translation unit).
 cudaError_t launch_store(const idx_cache* c, const void* k, const int64_t* slots, int64_t n,
                          int32_t* status, unsigned flags, cudaStream_t st);   // IDX_STORE_* flags

@@ -2,9 +2,11 @@
 // positive strides, 128-byte swizzled boxes of 64 values.
 #pragma once
 
+#include <stdint.h>
+
 #include <utility>
 
-#include "internal.h"
+#include "tensormap.h"
 
 namespace dsaidx {
 
