@@ -19,7 +19,8 @@
 //   warp 2     one lane issues the value products.  (One lane for both was the
 //              kernel's bound: its polling and 56 issues took 3400 cycles a
 //              tile.)
-//   warps 4-7  softmax and epilogue
+//   warps 4-7, at 64 heads 12-15 too  softmax, half of the heads each, and
+//              epilogue, half of the dimensions each
 //   warps 8-11 gather records, 16 keys of every tile each, with 16-byte
 //              asynchronous copies into a ring of chunk pairs (128 latent
 //              dimensions of 64 keys) and one of position chunks; masked keys
@@ -62,8 +63,10 @@ namespace {
 constexpr int kKeys = 64;                  // keys a tile
 constexpr int kChunk = kKeys * 128;        // bytes of a chunk: 64 keys x 64 values
 constexpr int kPair = 2 * kChunk;
-constexpr int kAttThreads = 384;
-constexpr int kSoftThreads = 128;
+// Softmax warpgroups: two at 64 heads (4096 rows of 1024 keys, 128 heads, 1.43
+// ms against 1.53, as a row's epilogue halves); at 16 a second one costs 3 %.
+constexpr int halves_of(int N) { return N == 64 ? 2 : 1; }
+constexpr int threads_of(int N) { return 256 + 128 * halves_of(N); }
 constexpr int kGatherThreads = 128;
 constexpr int kMaxCtas = 152;              // one an SM; CTAs never wait on one another
 constexpr int kMinRun = 2;                 // tiles a CTA, at least, where rows are cut
@@ -243,10 +246,11 @@ __device__ __forceinline__ int key_slot(const Params& p, int keys, int j, int64_
 }
 
 template <int N, int kCl>
-__global__ void __launch_bounds__(kAttThreads, 1)
+__global__ void __launch_bounds__(threads_of(N), 1)
     attend_kernel(const __grid_constant__ CUtensorMap ql_map, const __grid_constant__ CUtensorMap qp_map,
                   const Params p) {
     constexpr Plan kPlan = plan_of(N);
+    constexpr int kHalves = halves_of(N), kSoftThreads = 128 * kHalves, kGroupsM = 4 / kHalves;
     constexpr int kPairs = kPlan.pairs;
     constexpr int kSPitch = N < 32 ? 32 : N;   // TMEM columns of a score buffer
     constexpr int kSCol = 4 * N;               // first column behind the accumulators
@@ -339,7 +343,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
     Walk walk(p, sh_run[0], sh_run[1], sh_run[2], sh_run[3]);
     Work w;
 
-    if (warp >= 8) {
+    if (warp >= 8 && warp < 12) {
         // ---- gather: 16 keys of every tile ----
         // A copy instruction moves 128 bytes of four keys: lane / 8 is the key
         // among them, lane % 8 the 16-byte piece.
@@ -490,17 +494,19 @@ __global__ void __launch_bounds__(kAttThreads, 1)
             }
             if (item) mbar_wait(q_full, (item - 1) & 1, p.status, nullptr);
         }
-    } else if (warp >= 4 && warp < 8) {
+    } else if (warp >= 4) {
         // ---- softmax and epilogue ----
-        const int sw = warp - 4;
-        const int tid = threadIdx.x - 128;
+        const int sw = warp & 3, half = warp >> 3;      // lane quadrant; which half (one: all) of the heads
+        const int tid = 128 * half + (threadIdx.x & 127);
         const uint32_t lanes = static_cast<uint32_t>(32 * sw) << 16;
         const int quad = lane & 3, kr = lane >> 2;      // column pair and key row within the warp's 16
-        constexpr int kR = N / 8;                       // column groups of 8 heads
+        constexpr int kR = N / 8 / kHalves;             // this half's column groups of 8 heads
+        constexpr int kGroups = kR < 4 ? 1 : kR / 4;    // loads of 32 columns
+        const int hb = half * (N / kHalves);            // and its first head
         uint32_t it = 0;
         bool ok = true;
         while (ok && walk.next(p, w)) {
-            // head 8 r + 2 quad + e: maximum and this thread's share of the sum
+            // head hb + 8 r + 2 quad + e: maximum and this thread's share of the sum
             float mx[kR][2], sum[kR][2];
 #pragma unroll
             for (int r = 0; r < kR; ++r) {
@@ -510,14 +516,14 @@ __global__ void __launch_bounds__(kAttThreads, 1)
             for (int t = w.t0; t < w.t1; ++t, ++it) {
                 ok = ok && mbar_wait(s_full + (it & 1), (it >> 1) & 1, p.status, abort_flag);
                 tc_fence_after();
-                uint32_t raw[kR < 4 ? 1 : kR / 4][16];
+                uint32_t raw[kGroups][16];
 #pragma unroll
-                for (int g = 0; g < (kR < 4 ? 1 : kR / 4); ++g)
-                    tmem_ld_16x256b_x4(tmem + lanes + kSCol + (it & 1) * kSPitch + 32 * g, raw[g]);
+                for (int g = 0; g < (kGroups); ++g)
+                    tmem_ld_16x256b_x4(tmem + lanes + kSCol + (it & 1) * kSPitch + hb + 32 * g, raw[g]);
                 const uint32_t mask = masks[4 * (it & 3) + sw];
                 const bool va = (mask >> kr) & 1, vb = (mask >> (kr + 8)) & 1;
 #pragma unroll
-                for (int g = 0; g < (kR < 4 ? 1 : kR / 4); ++g) tmem_wait_ld16(raw[g]);
+                for (int g = 0; g < (kGroups); ++g) tmem_wait_ld16(raw[g]);
                 tc_fence_before();
                 mbar_arrive(s_empty + (it & 1));
                 // y[r][e]: key kr, y[r][2 + e]: key kr + 8; log2 of the weight
@@ -545,14 +551,14 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                             v = fmaxf(v, __shfl_xor_sync(~0u, v, 4));
                             v = fmaxf(v, __shfl_xor_sync(~0u, v, 8));
                             v = fmaxf(v, __shfl_xor_sync(~0u, v, 16));
-                            if (kr == 0) stat[sw * N + 8 * r + 2 * quad + e] = v;
+                            if (kr == 0) stat[sw * N + hb + 8 * r + 2 * quad + e] = v;
                         }
                     named_sync<1, kSoftThreads>();
 #pragma unroll
                     for (int r = 0; r < kR; ++r)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            const int h = 8 * r + 2 * quad + e;
+                            const int h = hb + 8 * r + 2 * quad + e;
                             float v = fmaxf(fmaxf(stat[h], stat[N + h]), fmaxf(stat[2 * N + h], stat[3 * N + h]));
                             v = fmaxf(v, mx[r][e]);
                             const float f = exp2_fast(mx[r][e] - v);
@@ -566,10 +572,11 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                         }
                     named_sync<1, kSoftThreads>();
                     if (t != w.t0) {
-                        // the accumulator's columns (heads) times their factors
+                        // the accumulators' columns (heads) times their factors,
+                        // half of the dimensions each
                         ok = mbar_wait(pv_done, (it - 1) & 1, p.status, abort_flag);
                         tc_fence_after();
-                        for (int c = 0; c < 4 * N; c += 16) {
+                        for (int c = kGroupsM * N * half; c < kGroupsM * N * (half + 1); c += 16) {
                             uint32_t v[16];
                             tmem_ld16_nowait(tmem + lanes + c, v);
                             tmem_wait_ld16(v);
@@ -598,8 +605,9 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                 uint8_t* pa = smem + kPlan.p_off + ka * 128 + 4 * quad;
 #pragma unroll
                 for (int r = 0; r < kR; ++r) {
-                    *reinterpret_cast<uint32_t*>(pa + ((r ^ (ka & 7)) << 4)) = pk[r][0];
-                    *reinterpret_cast<uint32_t*>(pa + 1024 + ((r ^ (ka & 7)) << 4)) = pk[r][1];
+                    const uint32_t at = ((half * kR + r) ^ (ka & 7)) << 4;
+                    *reinterpret_cast<uint32_t*>(pa + at) = pk[r][0];
+                    *reinterpret_cast<uint32_t*>(pa + 1024 + at) = pk[r][1];
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();
@@ -617,8 +625,8 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                     v += __shfl_xor_sync(~0u, v, 4);
                     v += __shfl_xor_sync(~0u, v, 8);
                     v += __shfl_xor_sync(~0u, v, 16);
-                    if (kr == 0) stat[sw * N + 8 * r + 2 * quad + e] = v;
-                    if (sw == 0 && kr == 0) stat[4 * N + 8 * r + 2 * quad + e] = mx[r][e];
+                    if (kr == 0) stat[sw * N + hb + 8 * r + 2 * quad + e] = v;
+                    if (sw == 0 && kr == 0) stat[4 * N + hb + 8 * r + 2 * quad + e] = mx[r][e];
                 }
             if (named_any<1, kSoftThreads>(!ok)) { ok = false; break; }
             if constexpr (kCl > 1) {
@@ -628,17 +636,18 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                 if (tid < N) ml = make_float2(stat[4 * N + tid], stat[tid] + stat[N + tid] + stat[2 * N + tid] + stat[3 * N + tid]);
                 named_sync<1, kSoftThreads>();
                 if (tid < N) reinterpret_cast<float2*>(stat)[tid] = ml;
-                float* share = reinterpret_cast<float*>(smem + kPlan.ring_off) + 32 * sw + lane;
+                float* share = reinterpret_cast<float*>(smem + kPlan.ring_off) + 128 * kGroupsM * half + 32 * sw + lane;
 #pragma unroll 1
                 for (int hc = 0; hc < N; hc += 16) {
-                    uint32_t v[4][16];
+                    uint32_t v[kGroupsM][16];
 #pragma unroll
-                    for (int m = 0; m < 4; ++m) tmem_ld16_nowait(tmem + lanes + m * N + hc, v[m]);
+                    for (int m = 0; m < kGroupsM; ++m) tmem_ld16_nowait(tmem + lanes + (kGroupsM * half + m) * N + hc, v[m]);
 #pragma unroll
-                    for (int m = 0; m < 4; ++m) {
+                    for (int m = 0; m < kGroupsM; ++m) {
                         tmem_wait_ld16(v[m]);
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) share[(hc + j) * IDX_LATENT_DIM + 128 * m] = __uint_as_float(v[m][j]);
+                        for (int j = 0; j < 16; ++j)
+                            share[(hc + j) * IDX_LATENT_DIM + 128 * m] = __uint_as_float(v[m][j]);
                     }
                 }
                 break;      // a cluster's CTA has one piece
@@ -656,18 +665,18 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                 stat[4 * N + tid] = w.slot >= 0 ? 1.0f : l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
             }
             named_sync<1, kSoftThreads>();
-            // lane = latent dimension, column = head: 16 heads at a time, the
-            // four groups of 128 dimensions in flight together
+            // lane = latent dimension, column = head: 16 heads at a time, this
+            // half's groups of 128 dimensions in flight together
 #pragma unroll 1
             for (int hc = 0; hc < N; hc += 16) {
-                uint32_t v[4][16];
+                uint32_t v[kGroupsM][16];
 #pragma unroll
-                for (int m = 0; m < 4; ++m) tmem_ld16_nowait(tmem + lanes + m * N + hc, v[m]);
-                const int d0 = 32 * sw + lane;
+                for (int m = 0; m < kGroupsM; ++m) tmem_ld16_nowait(tmem + lanes + (kGroupsM * half + m) * N + hc, v[m]);
+                const int d0 = 128 * kGroupsM * half + 32 * sw + lane;
                 if (w.slot >= 0) {
                     float* dst = p.part_o + (static_cast<int64_t>(w.slot) * N + hc) * IDX_LATENT_DIM + d0;
 #pragma unroll
-                    for (int m = 0; m < 4; ++m) {
+                    for (int m = 0; m < kGroupsM; ++m) {
                         tmem_wait_ld16(v[m]);
 #pragma unroll
                         for (int j = 0; j < 16; ++j) dst[j * IDX_LATENT_DIM + 128 * m] = __uint_as_float(v[m][j]);
@@ -683,7 +692,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
                 const int left = p.heads - h0 - hc - odd;      // heads from this lane's first one on
                 __nv_bfloat16* dst = p.out + (w.row * p.heads + h0 + hc + odd) * IDX_LATENT_DIM + (d0 & ~1);
 #pragma unroll
-                for (int m = 0; m < 4; ++m) {
+                for (int m = 0; m < kGroupsM; ++m) {
                     tmem_wait_ld16(v[m]);
 #pragma unroll
                     for (int j = 0; j < 16; j += 2) {
@@ -713,7 +722,7 @@ __global__ void __launch_bounds__(kAttThreads, 1)
         cluster_wait();
         const int64_t row = sh_run[2];
         const int h0 = static_cast<int>(sh_run[3]) * 64;
-        for (int i = threadIdx.x; i < kShare * (IDX_LATENT_DIM / 4); i += kAttThreads) {
+        for (int i = threadIdx.x; i < kShare * (IDX_LATENT_DIM / 4); i += threads_of(N)) {
             const int h = rank * kShare + i / (IDX_LATENT_DIM / 4), d = 4 * (i % (IDX_LATENT_DIM / 4));
             if (h0 + h >= p.heads) continue;
             float2 ml[kCl];
@@ -925,7 +934,7 @@ cudaError_t launch_n(const Params& p, const CUtensorMap& ql, const CUtensorMap& 
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
-    cfg.blockDim = dim3(kAttThreads, 1, 1);
+    cfg.blockDim = dim3(threads_of(N), 1, 1);
     cfg.dynamicSmemBytes = plan_of(N).total;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
