@@ -5,10 +5,9 @@
 // where there are few heads; a thread takes one work item of a head (a vector
 // of up to 16 bytes; with pairs half a head apart a vector and its partner
 // together, so that a turn in place has one owner) and keeps it and its token
-// over all its heads, so the cosines and sines it needs sit in registers for all its
-// heads and its addresses advance by one stride; the CTA computes each pair's
-// once (one integer multiply and one sincospi), while the first heads' values
-// are on their way.
+// over all its heads, so its addresses advance by one stride; the CTA computes
+// each pair's cosine and sine once (one integer multiply and one sincospi),
+// while the first heads' values are on their way.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -21,8 +20,8 @@ namespace dsaidx {
 namespace {
 
 // Most threads of a CTA.  8192 x 64 heads x 128, half of each turned in halves:
-// 52 us (5.1 TB/s) with 96 of 128, 56 with 192 of 256; 4000 x 64 x 192
-// interleaved 36 us against 40.
+// 49 us (5.5 TB/s); with 256 (192 used) some 7 % more, 4000 x 64 x 192
+// interleaved 40 us against 36.
 constexpr int kRopeThreads = 128;
 
 template <class T> __device__ __forceinline__ float to_f32(T v) { return static_cast<float>(v); }
@@ -35,6 +34,15 @@ template <class T, int kVec>
 struct alignas(sizeof(T) * kVec) Vec {
     T v[kVec];
 };
+
+// A pair's cosine and sine, read each time: kept in registers over the heads
+// they cost 16 of them, and with them loads in flight (8192 x 64 heads x 128,
+// half turned in halves: 49 us, 52 from registers).
+__device__ __forceinline__ float2 table(const float2* p) {
+    float2 v;
+    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(smem_u32(p)) : "memory");
+    return v;
+}
 
 struct RopeParams {
     const void* x;
@@ -61,7 +69,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
     using V = Vec<T, kVec>;
     constexpr int kPairs = kSplit ? kVec : kVec / 2;
     // heads in flight a thread; two vectors of a split pair are enough (two
-    // heads of them: 59 us in the case above, for want of registers)
+    // heads of them: 53 us in the case above, for want of registers)
     constexpr int kRopeHeads = kSplit ? 1 : 2;
     const int np = p.rot >> 1;
     const int64_t tok0 = static_cast<int64_t>(blockIdx.x) * p.tok_cta;
@@ -111,11 +119,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
     }
     __syncthreads();
     while (true) {
-        float2 c[kPairs];
-        if (turned) {
-#pragma unroll
-            for (int j = 0; j < kPairs; ++j) c[j] = cs[tl * np + item * kPairs + j];
-        }
+        const float2* c = cs + tl * np + item * kPairs;
         for (int h = h0; h < h1; h += kRopeHeads * p.hy) {
             if (h != h0) load(item, h);
 #pragma unroll
@@ -126,7 +130,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
                     if constexpr (kSplit) {
 #pragma unroll
                         for (int j = 0; j < kVec; ++j) {
-                            const float2 o = rope_turn(to_f32(a[u].v[j]), to_f32(b[u].v[j]), c[j]);
+                            const float2 o = rope_turn(to_f32(a[u].v[j]), to_f32(b[u].v[j]), table(c + j));
                             a[u].v[j] = from_f32<T>(o.x);
                             b[u].v[j] = from_f32<T>(o.y);
                         }
@@ -134,7 +138,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
                     } else {
 #pragma unroll
                         for (int j = 0; j < kVec / 2; ++j) {
-                            const float2 o = rope_turn(to_f32(a[u].v[2 * j]), to_f32(a[u].v[2 * j + 1]), c[j]);
+                            const float2 o = rope_turn(to_f32(a[u].v[2 * j]), to_f32(a[u].v[2 * j + 1]), table(c + j));
                             a[u].v[2 * j] = from_f32<T>(o.x);
                             a[u].v[2 * j + 1] = from_f32<T>(o.y);
                         }
@@ -158,8 +162,8 @@ cudaError_t launch_rope_t(RopeParams p, bool half, bool inplace, int sms, cudaSt
     const int most = p.items < kRopeThreads ? kRopeThreads / p.items : 1;
     // the heads of a token in rounds of hy, or several tokens' heads: the largest
     // hy that leaves the fewest threads idle in the last round, not below two
-    // thirds of the CTA (64 heads of 12 items: 8 rounds of 8 heads 52 us, 7 of
-    // 10 57 us)
+    // thirds of the CTA (64 heads of 12 items: 8 rounds of 8 heads take 8 %
+    // less than 7 of 10)
     p.hy = p.heads < most ? p.heads : most;
     for (int hy = p.hy - 1; hy >= 1 && 3 * hy >= 2 * most; --hy)
         if ((p.heads + hy - 1) / hy * hy < (p.heads + p.hy - 1) / p.hy * p.hy) p.hy = hy;
