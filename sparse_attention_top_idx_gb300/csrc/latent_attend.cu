@@ -43,8 +43,8 @@
 // partial sums in shared memory and join each other's, a share of the heads
 // each, through it.
 //
-// Measured: a tile takes 1.3 us at 16 heads (long contexts: 6.8 TB/s, bound by
-// HBM) and 1.45 us at 64 (4096 rows of 1024 keys, 128 heads, 1.49 ms, 784
+// Measured: a tile takes 1.3 us at 16 heads (long contexts: 6.6 TB/s, bound by
+// HBM) and 1.53 us at 64 (4096 rows of 1024 keys, 128 heads, 1.42 ms, 825
 // TFLOP/s: bound by the tensor cores, whose steps of 64 columns take 24 and 32
 // ns with two issuing warps against 16.4 at full rate).
 #include <cuda_bf16.h>

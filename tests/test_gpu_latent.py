@@ -567,3 +567,47 @@ def test_attend_repeats_bit_for_bit_cold():
             flush.zero_()
         out, lse = slots_call(cache, ql, qp, slots)
         assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+
+
+def test_results_without_lse_and_status():
+    g = gen(37)
+    pool = normal(g, 10, 64, REC)
+    ql, qp = queries(g, 6, 24)
+    slots = torch.randint(0, 640, (6, 200), generator=g, device="cuda")
+    cache = latent.LatentCache(pool)
+    want = slots_call(cache, ql, qp, slots)[0]
+    out = torch.empty_like(want)
+    latent.latent_attend_slots(cache, ql, qp, slots, SCALE, out, dsaidx.new_workspace(latent.workspace_bytes(6, 24, 200)))
+    assert torch.equal(out, want)
+    q, k, pe, v, cuq, cuk = expanded_inputs(g, [70, 3], [90, 3], 2)
+    want = expanded_call(q, k, pe, v, cuq, cuk)[0]
+    out = torch.empty_like(want)
+    latent.latent_attend_expanded(q, k, pe, v, cuq, cuk, SCALE, out)
+    assert torch.equal(out, want)
+
+
+def test_expanded_keys_and_values_shared_by_the_heads():
+    """Head stride 0: one key and value head for all."""
+    g = gen(38)
+    nq, nk, H = [150, 20], [200, 40], 6
+    q, k, pe, v, cuq, cuk = expanded_inputs(g, nq, nk, H)
+    k1, v1 = k[:, :1].expand(-1, H, -1), v[:, :1].expand(-1, H, -1)
+    got = expanded_call(q, k1, pe, v1, cuq, cuk)
+    check_expanded(*got, q, k1, pe, v1, nq, nk)
+    wide = normal(g, 240, 3 * PE)                       # a strided shared key part
+    got = expanded_call(q, k1, wide[:, PE:2 * PE], v, cuq, cuk)
+    check_expanded(*got, q, k1, wide[:, PE:2 * PE], v, nq, nk)
+
+
+def test_empty_calls_write_nothing():
+    g = gen(39)
+    cache = latent.LatentCache(normal(g, 2, 64, REC))
+    ws = dsaidx.new_workspace(latent.workspace_bytes(1, 16, 8))
+    none = torch.empty(0, 16, LAT, dtype=BF, device="cuda")
+    latent.latent_attend_slots(cache, none, torch.empty(0, 16, PE, dtype=BF, device="cuda"),
+                               torch.empty(0, 8, dtype=torch.int64, device="cuda"), SCALE, none, ws)
+    before = cache.pool.clone()
+    latent.latent_append(cache, normal(g, 0, LAT), normal(g, 0, PE), None, torch.empty(0, dtype=torch.int64, device="cuda"), None)
+    assert torch.equal(cache.pool, before)
+    q, k, pe, v, cuq, cuk = expanded_inputs(g, [0, 0], [0, 5], 2)
+    expanded_call(q, k, pe, v, cuq, cuk)

@@ -131,6 +131,7 @@ def test_attend_refusals(lib):
                          (3, A + 2, INVALID), (4, 1028, INVALID), (5, 66, INVALID), (6, None, INVALID), (6, A + 4, INVALID),
                          (8, -1, INVALID), (8, 2 ** 31, INVALID), (9, 0, INVALID), (9, 1025, INVALID), (10, -1, INVALID),
                          (10, 2 ** 24 + 1, INVALID), (11, math.nan, INVALID), (11, math.inf, INVALID), (12, None, INVALID),
+                         (1, 0, INVALID), (2, 0, INVALID), (4, -1024, INVALID), (5, 0, INVALID), (1, 2 ** 40, INVALID),
                          (12, A + 8, INVALID), (14, None, INVALID), (14, A + 128, INVALID), (15, ws - 1, TOO_SMALL)]:
         args = list(slots)
         args[i] = bad
@@ -154,7 +155,7 @@ def test_expanded_refusals(lib):
     good[14], good[15] = 4, 4
     for i, bad in [(0, None), (0, A + 8), (1, 1540), (2, 2 ** 31), (3, None), (3, A + 8), (4, -8), (5, 132), (6, None),
                    (7, 68), (8, None), (9, 12), (10, 4), (11, None), (11, A + 2), (12, None), (13, -1), (13, 4097),
-                   (14, -1), (14, 2 ** 31), (15, -1), (15, 2 ** 31), (16, 0), (16, 1025), (17, math.nan), (18, None),
+                   (1, 0), (2, 0), (4, 0), (7, 0), (9, 0), (14, -1), (14, 2 ** 31), (15, -1), (15, 2 ** 31), (16, 0), (16, 1025), (17, math.nan), (18, None),
                    (18, A + 8)]:
         args = list(good)
         args[i] = bad
