@@ -24,8 +24,9 @@
 //   warps 8-11 gather records, 16 keys of every tile each, with 16-byte
 //              asynchronous copies into a ring of chunk pairs (128 latent
 //              dimensions of 64 keys) and one of position chunks; masked keys
-//              are filled with zeros.  (TMA's row gather took 42 ns for four
-//              128-byte rows, 6.1 us a tile.)
+//              are filled with zeros.  Every thread reports its copies twice
+//              a tile (128 reports a pair took 5 % at 64 heads).  (TMA's row
+//              gather took 42 ns for four 128-byte rows, 6.1 us a tile.)
 // A chunk pair is freed by the value product that reads it last, so the next
 // tile's loads start while this tile's products run.
 //
@@ -43,10 +44,12 @@
 // partial sums in shared memory and join each other's, a share of the heads
 // each, through it.
 //
-// Measured: a tile takes 1.3 us at 16 heads (long contexts: 6.6 TB/s, bound by
-// HBM) and 1.53 us at 64 (4096 rows of 1024 keys, 128 heads, 1.42 ms, 825
-// TFLOP/s: bound by the tensor cores, whose steps of 64 columns take 24 and 32
-// ns with two issuing warps against 16.4 at full rate).
+// Measured: a tile takes 1.3 us at 16 heads (58 bytes a ns and SM, the rate of
+// the copies themselves: without products or without reading memory it stays;
+// long contexts: 6.6 TB/s, bound by HBM) and 1.46 us at 64 (4096 rows of 1024
+// keys, 128 heads, 1.41 ms, 827 TFLOP/s: near the copies' rate and that of the
+// tensor cores, whose steps of 64 columns take 24 and 32 ns with two issuing
+// warps against 16.4 at full rate).
 #include <cuda_bf16.h>
 
 #include <cmath>
@@ -88,7 +91,7 @@ __host__ __device__ constexpr Plan plan_of(int N) {
     p.pe_off = o;   o += 2 * kChunk;
     p.stat_off = o; o += 5 * N * 4;        // four warps' values and one for all
     p.mask_off = o; o += 4 * 8;
-    p.bar_off = o;  o += (2 * p.pairs + 20) * 8;
+    p.bar_off = o;  o += (p.pairs + 24) * 8;
     p.total = o + 1024;
     return p;
 }
@@ -257,31 +260,31 @@ __global__ void __launch_bounds__(threads_of(N), 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* bar = reinterpret_cast<uint64_t*>(smem + kPlan.bar_off);
-    uint64_t* pair_full = bar;
-    uint64_t* pair_empty = bar + kPairs;
-    uint64_t* pe_full = bar + 2 * kPairs;        // [2]
-    uint64_t* pe_empty = pe_full + 2;            // [2]
-    uint64_t* s_full = pe_full + 4;              // [2]
-    uint64_t* p_full = pe_full + 6;
-    uint64_t* pv_done = pe_full + 7;
-    uint64_t* q_full = pe_full + 8;
-    uint64_t* q_empty = pe_full + 9;
-    uint64_t* o_empty = pe_full + 10;
-    uint64_t* drain = pe_full + 11;              // [2]
-    uint64_t* s_empty = pe_full + 13;            // [2]
-    int64_t* sh_run = reinterpret_cast<int64_t*>(pe_full + 15);   // start, end, row, base
-    uint32_t* sh_tmem = reinterpret_cast<uint32_t*>(pe_full + 19);
+    uint64_t* pair_empty = bar;
+    uint64_t* pe_empty = bar + kPairs;           // [2]
+    uint64_t* half_full = pe_empty + 2;          // [2 tiles][2]: position chunk and two pairs, two pairs
+    uint64_t* s_full = pe_empty + 6;             // [2]
+    uint64_t* s_empty = pe_empty + 8;            // [2]
+    uint64_t* p_full = pe_empty + 10;
+    uint64_t* pv_done = pe_empty + 11;
+    uint64_t* q_full = pe_empty + 12;
+    uint64_t* q_empty = pe_empty + 13;
+    uint64_t* o_empty = pe_empty + 14;
+    uint64_t* drain = pe_empty + 15;             // [2]
+    int64_t* sh_run = reinterpret_cast<int64_t*>(pe_empty + 17);   // start, end, row, base
+    uint32_t* sh_tmem = reinterpret_cast<uint32_t*>(pe_empty + 21);
     int* sh_abort = reinterpret_cast<int*>(sh_tmem + 1);
     uint16_t* masks = reinterpret_cast<uint16_t*>(smem + kPlan.mask_off);   // [4 tiles][4]: 16 keys each
     float* stat = reinterpret_cast<float*>(smem + kPlan.stat_off);          // [5][N]
     const int warp = warp_id(), lane = lane_id();
 
     if (warp == 0 && elect_one()) {
-        for (int i = 0; i < kPairs; ++i) {
-            mbar_init(pair_full + i, kGatherThreads);
-            mbar_init(pair_empty + i, 1);
+        for (int i = 0; i < kPairs; ++i) mbar_init(pair_empty + i, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(pe_empty + i, 1);
+            mbar_init(s_full + i, 1);
         }
-        for (int i = 0; i < 6; ++i) mbar_init(pe_full + i, i < 2 ? kGatherThreads + 4 : 1);
+        for (int i = 0; i < 4; ++i) mbar_init(half_full + i, kGatherThreads + kGatherThreads / 32);
         mbar_init(p_full, kSoftThreads);
         mbar_init(pv_done, 1);
         mbar_init(q_full, 1);
@@ -380,12 +383,8 @@ __global__ void __launch_bounds__(threads_of(N), 1)
                 };
                 ok = mbar_wait(pe_empty + (it & 1), ((it >> 1) & 1) ^ 1, p.status, abort_flag);
                 if (!(ok = __all_sync(~0u, ok))) break;
+                if (lane == 0) masks[4 * (it & 3) + wq] = static_cast<uint16_t>(valid);
                 chunk(pe + (it & 1) * kChunk, 8);
-                copy_arrive(pe_full + (it & 1));
-                if (lane == 0) {
-                    masks[4 * (it & 3) + wq] = static_cast<uint16_t>(valid);
-                    mbar_arrive(pe_full + (it & 1));
-                }
 #pragma unroll 1
                 for (int m = 0; m < 4; ++m) {
                     ok = mbar_wait(pair_empty + sl, ph, p.status, abort_flag);
@@ -393,7 +392,12 @@ __global__ void __launch_bounds__(threads_of(N), 1)
                     const uint32_t dst = ring + sl * kPair;
                     chunk(dst, 2 * m);
                     chunk(dst + kChunk, 2 * m + 1);
-                    copy_arrive(pair_full + sl);
+                    if (m & 1) {
+                        // what this thread issued for the half, and the mask
+                        uint64_t* full = half_full + 2 * (it & 1) + (m >> 1);
+                        copy_arrive(full);
+                        if (lane == 0) mbar_arrive(full);
+                    }
                     if (++sl == kPairs) sl = 0, ph ^= 1;
                 }
                 if (!ok) break;
@@ -406,7 +410,7 @@ __global__ void __launch_bounds__(threads_of(N), 1)
             constexpr uint32_t kIdS = idesc_bf16(64, N, false, false);
             const uint32_t q_addr = smem_u32(smem + kPlan.q_off), ring = smem_u32(smem + kPlan.ring_off);
             const uint32_t pe_addr = smem_u32(smem + kPlan.pe_off);
-            uint32_t it = 0, item = 0, sl = 0, ph = 0;
+            uint32_t it = 0, item = 0, sl = 0;
             bool ok = true;
             while (ok && walk.next(p, w)) {
                 if (!(ok = mbar_wait(q_full, item & 1, p.status, abort_flag))) break;
@@ -414,7 +418,7 @@ __global__ void __launch_bounds__(threads_of(N), 1)
                     const uint32_t d = tmem + kSCol + (it & 1) * kSPitch;
                     // the softmax has read the scores before last
                     if (!(ok = mbar_wait(s_empty + (it & 1), ((it >> 1) & 1) ^ 1, p.status, abort_flag))) break;
-                    if (!(ok = mbar_wait(pe_full + (it & 1), (it >> 1) & 1, p.status, abort_flag))) break;
+                    if (!(ok = mbar_wait(half_full + 2 * (it & 1), (it >> 1) & 1, p.status, abort_flag))) break;
                     // the records were copied by other threads: order their
                     // writes before the tensor core's reads
                     fence_proxy_async_smem();
@@ -426,14 +430,16 @@ __global__ void __launch_bounds__(threads_of(N), 1)
                     mma_commit(pe_empty + (it & 1));
 #pragma unroll 1
                     for (int m = 0; m < 4; ++m) {
-                        if (!(ok = mbar_wait(pair_full + sl, ph, p.status, abort_flag))) break;
-                        fence_proxy_async_smem();
-                        tc_fence_after();
+                        if (m == 2) {
+                            if (!(ok = mbar_wait(half_full + 2 * (it & 1) + 1, (it >> 1) & 1, p.status, abort_flag))) break;
+                            fence_proxy_async_smem();
+                            tc_fence_after();
+                        }
 #pragma unroll
                         for (int k = 0; k < 8; ++k)
                             mma_bf16(d, sdesc_sw128(ring + sl * kPair + (k >> 2) * kChunk + 32 * (k & 3)),
                                      sdesc_sw128(q_addr + (2 * m + (k >> 2)) * N * 128 + 32 * (k & 3)), kIdS, 1u);
-                        if (++sl == kPairs) sl = 0, ph ^= 1;
+                        if (++sl == kPairs) sl = 0;
                     }
                     if (!ok) break;
                     mma_commit(s_full + (it & 1));
