@@ -24,7 +24,8 @@
  * key or row and faults nothing.  Status words are sticky: the library never
  * clears them.  Strides are in elements.  A row without a visible key has
  * out 0 and lse -inf.  Sums and softmax statistics are fp32.
- * Every call may be captured into a CUDA graph.
+ * Every call may be captured into a CUDA graph.  idx_kernel_timing records the
+ * attention calls' kernels too (outside capture).
  */
 #ifndef DSAIDX_LATENT_H
 #define DSAIDX_LATENT_H

@@ -71,7 +71,7 @@ constexpr int kPair = 2 * kChunk;
 constexpr int halves_of(int N) { return N == 64 ? 2 : 1; }
 constexpr int threads_of(int N) { return 256 + 128 * halves_of(N); }
 constexpr int kGatherThreads = 128;
-constexpr int kMaxCtas = 152;              // one an SM; CTAs never wait on one another
+constexpr int kMaxCtas = 152;              // one an SM; CTAs of different clusters never wait on one another
 constexpr int kMinRun = 2;                 // tiles a CTA, at least, where rows are cut
 constexpr float kNone = -3.0e38f;          // maximum of a head without a key so far
 constexpr float kGrow = 8.0f;              // log2 by which a score may pass the maximum

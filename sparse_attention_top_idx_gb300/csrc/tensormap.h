@@ -1,4 +1,4 @@
-// tensormap.h -- the driver's tensor-map encoder (defined in api.cu).
+// tensormap.h -- the CUDA driver API's tensor-map encoder (defined in api.cu).
 #pragma once
 
 #include <cuda.h>
