@@ -43,6 +43,7 @@ extern "C" {
 #define IDX_EXPANDED_V_DIM 128
 #define IDX_LATENT_MAX_HEADS 1024
 #define IDX_ROPE_MAX_DIM 1024
+#define IDX_ROPE_MAX_HEADS (1 << 24)
 
 /* Element types of idx_rope. */
 typedef enum idx_dtype { IDX_DT_BF16 = 0, IDX_DT_FP16 = 1, IDX_DT_FP32 = 2 } idx_dtype;
@@ -80,7 +81,7 @@ idx_status idx_rope_steps(int rot_dim, double base, int scaling, double factor, 
  * are contiguous).  positions_dev: [tokens] int64, any sign.  steps_dev: the
  * rot_dim / 2 steps of idx_rope_steps in device memory.  Angles are exact to
  * about 1e-7 radians; arithmetic in fp32, one rounding to the type.
- * head_dim 1..1024; heads >= 1; tokens * heads < 2^31 * 4.
+ * head_dim 1..1024; heads 1..2^24; tokens * heads < 2^33.
  */
 idx_status idx_rope(const void* x_dev, int64_t x_token_stride, int64_t x_head_stride, void* y_dev,
                     int64_t y_token_stride, int64_t y_head_stride, int dtype, int64_t tokens, int heads, int head_dim,

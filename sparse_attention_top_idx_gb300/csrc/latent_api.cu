@@ -96,7 +96,8 @@ idx_status idx_rope(const void* x_dev, int64_t x_token_stride, int64_t x_head_st
                     unsigned flags, void* stream) {
     if (dtype < IDX_DT_BF16 || dtype > IDX_DT_FP32 || (flags & ~(IDX_ROPE_HALF | IDX_ROPE_TRANSPOSE)) != 0u)
         return IDX_ERR_INVALID_ARG;
-    if (tokens < 0 || heads < 1 || head_dim < 1 || head_dim > IDX_ROPE_MAX_DIM) return IDX_ERR_INVALID_ARG;
+    if (tokens < 0 || heads < 1 || heads > IDX_ROPE_MAX_HEADS || head_dim < 1 || head_dim > IDX_ROPE_MAX_DIM)
+        return IDX_ERR_INVALID_ARG;
     if (rot_dim < 2 || rot_dim % 2 || offset < 0 || rot_dim > head_dim || offset > head_dim - rot_dim)
         return IDX_ERR_INVALID_ARG;
     if (tokens >= 4 * kInt31 / heads) return IDX_ERR_INVALID_ARG;

@@ -75,7 +75,7 @@ def test_rope_refusals(lib):
     #        x  xt   xh  y      yt   yh  dt T  H  D   pos steps rot off amp flags stream
     good = [A, 128, 64, A + 2, 128, 64, 0, 0, 2, 64, A, A, 64, 0, 1.0, 0, None]
     assert lib.idx_rope(*good) == OK                      # no tokens: nothing to do
-    for i, bad in [(6, 3), (6, -1), (7, -1), (7, 2 ** 32), (8, 0), (9, 0), (9, 1025), (12, 0), (12, 63), (12, 66), (13, 1),
+    for i, bad in [(6, 3), (6, -1), (7, -1), (7, 2 ** 32), (8, 0), (8, 2 ** 24 + 1), (9, 0), (9, 1025), (12, 0), (12, 63), (12, 66), (13, 1),
                    (13, -1), (15, 4)]:
         args = list(good)
         args[i] = bad
