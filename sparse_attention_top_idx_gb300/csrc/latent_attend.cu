@@ -619,9 +619,10 @@ __global__ void __launch_bounds__(threads_of(N), 1)
                 tc_fence_before();
                 mbar_arrive(p_full);
             }
-            if (!ok) break;
+            // A wait may have run out in some threads alone.  None of them leaves
+            // before the vote below, whose barrier counts every thread.
             // sums over the warp's keys, then over the four warps
-            ok = mbar_wait(pv_done, (it - 1) & 1, p.status, abort_flag) && ok;
+            ok = ok && mbar_wait(pv_done, (it - 1) & 1, p.status, abort_flag);
             tc_fence_after();
 #pragma unroll
             for (int r = 0; r < kR; ++r)
