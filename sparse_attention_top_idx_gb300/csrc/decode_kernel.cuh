@@ -211,6 +211,12 @@ __global__ void __maxnreg__(120) decode_kernel(const __grid_constant__ CUtensorM
     // (the first unit's query rows): a whole-cluster barrier, its wait after
     // the scan below
     cluster_arrive();
+    // Launched with programmatic serialization, the set-up above may overlap
+    // the kernels before this one in the stream.  Nothing below runs before
+    // they have finished and their writes are visible: any of them may have
+    // written the sequence lengths (a staged copy, two kernels back as well,
+    // since a kernel lets the next one start before it waits itself).
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     // units per sequence, scanned over the block: thread t holds sequences
     // [t * per, t * per + per) and the exclusive prefix of their units; with
     // one sequence per thread it keeps that sequence's length
@@ -245,11 +251,6 @@ __global__ void __maxnreg__(120) decode_kernel(const __grid_constant__ CUtensorM
     // the first half of the per-unit barrier (its wait follows the stream)
     cluster_arrive();
     if (tid == 0) DSAIDX_PHASE(0, 1);
-
-    // Launched with programmatic serialization, the set-up above may overlap
-    // the previous kernel in the stream (the key store); nothing below runs
-    // before that grid has finished and its writes are visible.
-    asm volatile("griddepcontrol.wait;" ::: "memory");
 
     uint32_t tcnt = 0;   // tiles streamed by this CTA so far (stage, phase and accumulator)
     uint32_t qcnt = 0;   // query loads (qbar / qready phases)
