@@ -1,5 +1,9 @@
-"""Calls from threads that have made none before: one thread after the other."""
+"""Calls from threads that have made none before: one thread after the other,
+and many at once as the first calls of a process."""
 import ctypes
+import os
+import subprocess
+import sys
 import threading
 
 import pytest
@@ -8,6 +12,8 @@ import torch
 from sparse_attention_top_idx_gb300 import dsaidx, latent
 
 pytestmark = pytest.mark.gpu
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 BF = torch.bfloat16
 
@@ -82,3 +88,69 @@ def test_call_in_a_new_thread(make):
     torch.cuda.synchronize()
     assert not failed, failed
     assert bool((out == 1).all())
+
+
+# Native threads that spin on one flag, so that they enter the call within a
+# fraction of a microsecond of each other (Python's are started one by one).
+HELPER = r"""
+#include <pthread.h>
+#include <stdatomic.h>
+#include <stddef.h>
+#include <stdint.h>
+typedef int (*create_fn)(void**, void*, int64_t, int, int, int);
+typedef int (*init_fn)(void*, size_t, void*);
+struct job { create_fn create; init_fn init; char* pool; int key_dtype; int code; void* handle; };
+static atomic_int ready, go;
+static void* run(void* p) {
+    struct job* j = p;
+    j->code = j->init(j->pool, 256, 0);      // the thread's start-up in the runtime
+    atomic_fetch_add(&ready, 1);
+    while (!atomic_load(&go)) { }
+    if (j->code == 0) j->code = j->create(&j->handle, j->pool, 4, 64, 128, j->key_dtype);
+    return 0;
+}
+int together(create_fn create, init_fn init, void* pool, int key_dtype, int n, int* codes, void** handles) {
+    pthread_t t[64];
+    struct job j[64];
+    if (n > 64) return 1;
+    for (int i = 0; i < n; ++i) {
+        j[i] = (struct job){create, init, pool, key_dtype, -1, 0};
+        if (pthread_create(&t[i], 0, run, &j[i])) return 1;
+    }
+    while (atomic_load(&ready) < n) { }
+    atomic_store(&go, 1);
+    for (int i = 0; i < n; ++i) {
+        pthread_join(t[i], 0);
+        codes[i] = j[i].code;
+        handles[i] = j[i].handle;
+    }
+    return 0;
+}
+"""
+
+CHILD = """
+import ctypes, sys
+import torch
+from sparse_attention_top_idx_gb300 import dsaidx
+H, L, n = ctypes.CDLL(sys.argv[1]), dsaidx.load(), 12
+pool = torch.zeros(4 * dsaidx.block_bytes(dsaidx.FP8, 64), dtype=torch.uint8, device="cuda")
+codes, handles = (ctypes.c_int * n)(), (ctypes.c_void_p * n)()
+H.together.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p]
+create, init = (ctypes.cast(f, ctypes.c_void_p) for f in (L.idx_cache_create, L.idx_workspace_init))
+assert H.together(create, init, pool.data_ptr(), dsaidx.FP8, n, codes, handles) == 0
+for h in handles:
+    if h: L.idx_cache_destroy(h)
+print(list(codes))
+"""
+
+
+@pytest.mark.parametrize("again", range(6))
+def test_many_threads_first_thing_in_a_process(again, tmp_path):
+    """What the library looks up once must be there for every thread that asks at the same time: index caches and the
+    attention calls share the tensor-map encoder."""
+    src, lib = tmp_path / "together.c", tmp_path / "libtogether.so"
+    src.write_text(HELPER)
+    subprocess.run(["gcc", "-O2", "-shared", "-fPIC", "-pthread", str(src), "-o", str(lib)], check=True)
+    r = subprocess.run([sys.executable, "-c", CHILD, str(lib)], cwd=ROOT, capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0, r.stderr[-2000:]
+    assert r.stdout.strip() == str([0] * 12)
