@@ -18,8 +18,9 @@
  * The expanded form takes each head's own keys and values.
  *
  * Conventions are those of dsaidx.h: caller-owned device memory, nothing
- * allocated or synchronised, host-side argument errors return before any
- * launch, and what only the device can see (a slot or block id outside the
+ * allocated or synchronised, every pointer in memory of the current device (the
+ * binding refuses others; a pool has no handle that would know), host-side
+ * argument errors return before any launch, and what only the device can see (a slot or block id outside the
  * pool, a length beyond its bound) sets the status word, skips the offending
  * key or row and faults nothing.  Status words are sticky: the library never
  * clears them.  Strides are in elements.  A row without a visible key has
