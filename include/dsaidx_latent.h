@@ -113,7 +113,9 @@ idx_status idx_latent_append(const idx_latent_pool* pool, const void* latent_dev
                              unsigned flags, int32_t* status_dev, void* stream);
 
 /* Workspace bytes of one absorbed attention call (slots: max_keys = topk;
- * paged: rows = batch, max_keys = max_seq_len).  0 on invalid arguments.  The
+ * paged: rows = batch, max_keys = max_seq_len), enough for every call of no
+ * more rows, heads and keys too, so that one workspace of the largest batch
+ * serves the smaller ones.  At most 40 MB.  0 on invalid arguments.  The
  * first word is the call's status (idx_read_device_status); zero the
  * workspace once with idx_workspace_init.  Concurrent calls must not share
  * one. */

@@ -57,7 +57,8 @@ struct AttendArgs {
     void* ws;                    // behind the header
 };
 cudaError_t launch_attend(const AttendArgs& a, cudaStream_t st);
-size_t attend_ws_bytes(int64_t rows, int heads, int64_t max_keys);
+size_t attend_ws_bytes(int64_t rows, int heads, int64_t max_keys);              // of this call and every smaller one
+size_t attend_ws_need(int64_t rows, int heads, int64_t max_keys, bool paged);   // of this call
 
 struct ExpandedArgs {
     const void* q;

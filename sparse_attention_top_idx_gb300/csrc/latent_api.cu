@@ -38,11 +38,11 @@ idx_status status_of(cudaError_t e) { return e == cudaSuccess ? IDX_OK : IDX_ERR
 // What the two absorbed calls check alike.
 idx_status attend_check(const idx_latent_pool* pool, const void* ql, int64_t ql_row, int64_t ql_head, const void* qp,
                         int64_t qp_row, int64_t qp_head, int64_t rows, int heads, int64_t max_keys, int64_t keys_cap,
-                        float scale, const void* out, const void* ws, size_t ws_bytes) {
+                        float scale, const void* out, const void* ws, size_t ws_bytes, bool paged) {
     if (!pool_ok(pool) || rows < 0 || heads < 1 || heads > IDX_LATENT_MAX_HEADS || max_keys < 0 || max_keys > keys_cap)
         return IDX_ERR_INVALID_ARG;
     if (!std::isfinite(scale)) return IDX_ERR_INVALID_ARG;
-    if (rows * ((heads + 63) / 64) >= kInt31 || rows >= kInt31) return IDX_ERR_INVALID_ARG;
+    if (rows >= kInt31 || rows * ((heads + 63) / 64) >= kInt31) return IDX_ERR_INVALID_ARG;
     if (rows == 0) return IDX_OK;
     if (!ql || !qp || !out || !ws) return IDX_ERR_INVALID_ARG;
     if (!aligned(ql, 16) || !aligned(qp, 16) || !aligned(out, 16) || !aligned(ws, 256)) return IDX_ERR_INVALID_ARG;
@@ -51,7 +51,7 @@ idx_status attend_check(const idx_latent_pool* pool, const void* ql, int64_t ql_
     const int64_t cap = int64_t(1) << 38;
     if (rows > 1 && (ql_row < 1 || ql_row > cap || qp_row < 1 || qp_row > cap)) return IDX_ERR_INVALID_ARG;
     if (heads > 1 && (ql_head < 1 || ql_head > cap || qp_head < 1 || qp_head > cap)) return IDX_ERR_INVALID_ARG;
-    if (ws_bytes < idx_latent_workspace_bytes(rows, heads, max_keys)) return IDX_ERR_WORKSPACE_TOO_SMALL;
+    if (ws_bytes < attend_ws_need(rows, heads, max_keys, paged)) return IDX_ERR_WORKSPACE_TOO_SMALL;
     return IDX_OK;
 }
 
@@ -133,6 +133,7 @@ idx_status idx_latent_append(const idx_latent_pool* pool, const void* latent_dev
 
 size_t idx_latent_workspace_bytes(int64_t rows, int heads, int64_t max_keys) {
     if (rows < 0 || heads < 1 || heads > IDX_LATENT_MAX_HEADS || max_keys < 0 || max_keys >= kInt31) return 0;
+    if (rows >= kInt31 || rows * ((heads + 63) / 64) >= kInt31) return 0;
     return attend_ws_bytes(rows, heads, max_keys);
 }
 
@@ -143,7 +144,7 @@ idx_status idx_latent_attend_slots(const idx_latent_pool* pool, const void* ql_d
                                    void* workspace_dev, size_t ws_bytes, void* stream) {
     const idx_status c = attend_check(pool, ql_dev, ql_row_stride, ql_head_stride, qp_dev, qp_row_stride,
                                       qp_head_stride, rows, heads, topk, int64_t(1) << 24, scale, out_dev,
-                                      workspace_dev, ws_bytes);
+                                      workspace_dev, ws_bytes, false);
     if (c != IDX_OK || rows == 0) return c;
     if ((!slots_dev && topk > 0) || !aligned(slots_dev, 8)) return IDX_ERR_INVALID_ARG;
     AttendArgs a{};
@@ -166,7 +167,7 @@ idx_status idx_latent_attend_paged(const idx_latent_pool* pool, const void* ql_d
     if (max_blocks_per_seq < 1) return IDX_ERR_INVALID_ARG;
     const idx_status c = attend_check(pool, ql_dev, ql_row_stride, ql_head_stride, qp_dev, qp_row_stride,
                                       qp_head_stride, batch, heads, max_seq_len, kInt31 - 256, scale, out_dev,
-                                      workspace_dev, ws_bytes);
+                                      workspace_dev, ws_bytes, true);
     if (c != IDX_OK || batch == 0) return c;
     if (!block_table_dev || !seq_lens_dev || !aligned(block_table_dev, 4) || !aligned(seq_lens_dev, 4))
         return IDX_ERR_INVALID_ARG;

@@ -892,6 +892,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const Params p, i
 // Heads of one score product.
 int width_of(int heads) { return heads <= 16 ? 16 : heads <= 32 ? 32 : 64; }
 
+// What joining cut rows costs, in tiles (measured, see shape_of).
+int join_tiles(int N) { return N == 64 ? 12 : 9; }
+
 // How the rows are spread over CTAs.
 struct Shape {
     int N, hgs, split, ctas, cluster;
@@ -912,7 +915,7 @@ Shape shape_of(int64_t rows, int heads, int64_t max_keys, bool paged) {
     // and 46 whole, 64 heads 82 and 60.  A paged batch is ragged, which the cut
     // evens out (32 x 4500 / 10000, 16 heads: 55 us, in fours 66), so long
     // contexts take no clusters.
-    const int64_t join = s.N == 64 ? 12 : 9;
+    const int64_t join = join_tiles(s.N);
     int64_t best = (items + g - 1) / g * nt;
     s.ctas = static_cast<int>(items < g ? items : g);
     for (int c = 2; c <= 8; c *= 2) {
@@ -985,16 +988,26 @@ cudaError_t launch_cl(const Params& p, const CUtensorMap& ql, const CUtensorMap&
 
 }  // namespace
 
+// What the call itself uses: partial sums and statistics of two pieces a CTA.
+static size_t ws_of(int64_t ctas, int N) {
+    return 256 + align_up(static_cast<size_t>(2 * ctas) * N * (IDX_LATENT_DIM + 2) * 4, 256);
+}
+
+size_t attend_ws_need(int64_t rows, int heads, int64_t max_keys, bool paged) {
+    const Shape s = shape_of(rows, heads, max_keys, paged);
+    return s.split == 1 ? ws_of(s.ctas, s.N) : 256;
+}
+
+// Rows are cut for some sizes and not for others, so that a call may need more
+// than a larger one.  What is asked for covers every call of no more rows,
+// heads and keys: rows of nt tiles are cut only where ceil(items nt / g) + join
+// is below ceil(items / g) nt, which takes nt > join + 1, and the CTAs of a cut
+// call grow with items nt.
 size_t attend_ws_bytes(int64_t rows, int heads, int64_t max_keys) {
-    // the same for both sources of keys
-    size_t most = 256;
-    for (const bool paged : {false, true}) {
-        const Shape s = shape_of(rows, heads, max_keys, paged);
-        if (s.split != 1) continue;
-        const size_t need = 256 + align_up(static_cast<size_t>(2) * s.ctas * s.N * (IDX_LATENT_DIM + 2) * 4, 256);
-        if (need > most) most = need;
-    }
-    return most;
+    const int64_t items = rows * ((heads + 63) / 64), nt = max_keys > 0 ? (max_keys + kKeys - 1) / kKeys : 1;
+    if (nt <= join_tiles(16) + 1) return 256;      // the smallest of the widths
+    const int64_t n = (items * nt + kMinRun - 1) / kMinRun;
+    return ws_of(n < kMaxCtas ? n : kMaxCtas, width_of(heads));
 }
 
 cudaError_t launch_attend(const AttendArgs& a, cudaStream_t st) {
