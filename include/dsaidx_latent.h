@@ -79,7 +79,9 @@ idx_status idx_rope_steps(int rot_dim, double base, int scaling, double factor, 
  * head_dim] by its token's position and writes y of the same shape (the other
  * elements are copied).  y == x with equal strides turns in place; otherwise
  * x and y must not overlap.  Any strides and alignment (elements of a head
- * are contiguous).  positions_dev: [tokens] int64, any sign.  steps_dev: the
+ * are contiguous), but no element is written twice: strides of y at which two
+ * heads (in place: their turned parts) share elements, as a broadcast head's
+ * stride of 0, are IDX_ERR_INVALID_ARG.  positions_dev: [tokens] int64, any sign.  steps_dev: the
  * rot_dim / 2 steps of idx_rope_steps in device memory.  Angles are exact to
  * about 1e-7 radians; arithmetic in fp32, one rounding to the type.
  * head_dim 1..1024; heads 1..2^24; tokens * heads < 2^33.

@@ -5,6 +5,7 @@
 
 #include "internal.h"
 #include "latent.h"
+#include "strides.h"
 
 using namespace dsaidx;
 
@@ -107,6 +108,9 @@ idx_status idx_rope(const void* x_dev, int64_t x_token_stride, int64_t x_head_st
     if (!aligned(x_dev, esize) || !aligned(y_dev, esize) || !aligned(positions_dev, 8) || !aligned(steps_dev, 8))
         return IDX_ERR_INVALID_ARG;
     if (x_dev == y_dev && (x_token_stride != y_token_stride || x_head_stride != y_head_stride))
+        return IDX_ERR_INVALID_ARG;
+    // what is written must be written once: the turned elements in place, else whole heads
+    if (!rows_apart(tokens, heads, x_dev == y_dev ? rot_dim : head_dim, y_token_stride, y_head_stride))
         return IDX_ERR_INVALID_ARG;
     int sms = 0;
     if (!sm_count(&sms)) return IDX_ERR_CUDA;

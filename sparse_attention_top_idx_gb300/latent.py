@@ -184,7 +184,8 @@ def rope(x: torch.Tensor, positions: torch.Tensor, plan: RopePlan, layout: int =
     """idx_rope: turn elements [offset, offset + plan.rot_dim) of every head of
     x [tokens, heads, head_dim] (bf16, fp16 or fp32, any strides) by its token's
     position [tokens] int64; into out (which gets the other elements too) or
-    in place.  transpose=True applies the transposed map: the gradient of the
+    in place.  What is written may not share elements between heads or tokens
+    (an expanded tensor in place, an expanded out).  transpose=True applies the transposed map: the gradient of the
     turn with respect to x, given the gradient of its result."""
     dtype, shape = x.dtype, x.shape
     code = _DTYPE.get(dtype)
