@@ -70,11 +70,16 @@ class SparseLayer:
         return out, lse
 
 
-def prompt(layer: SparseLayer, q, k_up, v_up, c, k_pe, positions, cu_seqlens):
+def prompt(layer: SparseLayer, q, k_up, v_up, c, k_pe, positions, cu_seqlens, in_place: bool = True):
     """Prompts no longer than the top-k select every key: expanded attention, without the indexer.  q [tokens,
-    heads, 192] with its last 64 elements not yet turned, c [tokens, 512], k_up and v_up [heads, 512, 128]."""
-    qp = q[:, :, latent.NOPE_DIM:]
-    latent.rope(qp, positions, layer.plan)                                   # in place
+    heads, 192] with its last 64 elements not yet turned, c [tokens, 512], k_up and v_up [heads, 512, 128].
+
+    q is the projection's output, which nothing else reads, so those 64 elements are turned where they are: the
+    caller's q has changed afterwards and must not be passed again.  in_place=False turns a copy and leaves q as
+    it was."""
+    if not in_place:
+        q = q.clone()
+    latent.rope(q[:, :, latent.NOPE_DIM:], positions, layer.plan)
     kp = latent.rope(k_pe[:, None], positions, layer.plan, out=torch.empty_like(k_pe)[:, None])[:, 0]
     k_nope = torch.einsum("tc,hcd->thd", c, k_up)
     v = torch.einsum("tc,hcd->thd", c, v_up)
