@@ -29,13 +29,24 @@ class SparseLayer:
     plan: latent.RopePlan
     block_table: torch.Tensor
     topk: int
+    scale: float = SCALE
 
     @staticmethod
-    def allocate(num_blocks: int, block_size: int, block_table: torch.Tensor, topk: int, key_dtype: int = dsaidx.FP8):
+    def allocate(num_blocks: int, block_size: int, block_table: torch.Tensor, topk: int, key_dtype: int = dsaidx.FP8,
+                 temperature: str = "logit"):
+        """YaRN's temperature multiplies the whole logit by amplitude^2.  Where all of a head is turned, turning it to
+        the length amplitude does that; here 64 of a key's 576 elements are turned, so the turned elements keep their
+        length and the softmax scale carries it.  temperature="turn" is for a model whose turned elements alone are
+        lengthened (their part of the logit then counts amplitude^2 times as much against the latent's)."""
+        if temperature not in ("logit", "turn"):
+            raise ValueError('temperature must be "logit" or "turn"')
+        yarn = dict(base=160000.0, scaling="yarn", factor=40.0, original_max_pos=4096)
+        amplitude = latent.rope_steps(latent.PE_DIM, **yarn)[1]
+        whole = temperature == "logit"
         return SparseLayer(dsaidx.IndexCache.allocate(num_blocks, block_size, key_dtype),
                            latent.LatentCache.allocate(num_blocks, block_size),
-                           latent.rope_plan(latent.PE_DIM, base=160000.0, scaling="yarn", factor=40.0,
-                                            original_max_pos=4096), block_table, topk)
+                           latent.rope_plan(latent.PE_DIM, amplitude=1.0 if whole else amplitude, **yarn),
+                           block_table, topk, SCALE * amplitude ** 2 if whole else SCALE)
 
     def append(self, index_keys, c, k_pe, positions, slots):
         """Store the index keys [n, 128] and the records (c [n, 512], k_pe [n, 64] not yet turned) of n tokens."""
@@ -56,7 +67,7 @@ class SparseLayer:
         out = torch.empty(B, H, latent.LATENT_DIM, dtype=torch.bfloat16, device=dev)
         lse = torch.empty(B, H, dtype=torch.float32, device=dev)
         aws = dsaidx.new_workspace(latent.workspace_bytes(B, H, k))
-        latent.latent_attend_slots(self.records, q_latent, turned, slots, SCALE, out, aws, lse=lse)
+        latent.latent_attend_slots(self.records, q_latent, turned, slots, self.scale, out, aws, lse=lse)
         return out, lse, idx, slots
 
     def decode_dense(self, q_latent, turned_q_pe, seq_lens, max_seq_len: int):
@@ -65,7 +76,7 @@ class SparseLayer:
         out = torch.empty(B, H, latent.LATENT_DIM, dtype=torch.bfloat16, device=q_latent.device)
         lse = torch.empty(B, H, dtype=torch.float32, device=q_latent.device)
         ws = dsaidx.new_workspace(latent.workspace_bytes(B, H, max_seq_len))
-        latent.latent_attend_paged(self.records, q_latent, turned_q_pe, self.block_table, seq_lens, max_seq_len, SCALE,
+        latent.latent_attend_paged(self.records, q_latent, turned_q_pe, self.block_table, seq_lens, max_seq_len, self.scale,
                                    out, ws, lse=lse)
         return out, lse
 
@@ -84,15 +95,18 @@ def prompt(layer: SparseLayer, q, k_up, v_up, c, k_pe, positions, cu_seqlens, in
     k_nope = torch.einsum("tc,hcd->thd", c, k_up)
     v = torch.einsum("tc,hcd->thd", c, v_up)
     out = torch.empty(*v.shape, dtype=torch.bfloat16, device=q.device)
-    latent.latent_attend_expanded(q, k_nope, kp, v, cu_seqlens, cu_seqlens, SCALE, out)
+    latent.latent_attend_expanded(q, k_nope, kp, v, cu_seqlens, cu_seqlens, layer.scale, out)
     return out
 
 
-def demo_layer(seq_lens, topk: int, heads: int, seed: int = 0, block_size: int = 64):
-    """A layer filled with seq_lens tokens a sequence and the inputs of one decode step."""
+def demo_layer(seq_lens, topk: int, heads: int, seed: int = 0, block_size: int = 64,
+               temperature: str = "turn"):
+    """A layer filled with seq_lens tokens a sequence and the inputs of one decode step.  The records are synthetic;
+    temperature is SparseLayer.allocate's."""
     W = wl.make_workload("step", seq_lens, [1] * len(seq_lens), topk=topk, bs=block_size, seed=seed)
     dev = "cuda"
-    layer = SparseLayer.allocate(W.num_blocks, block_size, torch.from_numpy(W.block_table).to(dev), topk)
+    layer = SparseLayer.allocate(W.num_blocks, block_size, torch.from_numpy(W.block_table).to(dev), topk,
+                                 temperature=temperature)
     g = torch.Generator(device=dev).manual_seed(seed)
     n = sum(seq_lens)
     kv = torch.randn(n, latent.RECORD, generator=g, device=dev).bfloat16()
@@ -108,7 +122,7 @@ def demo_layer(seq_lens, topk: int, heads: int, seed: int = 0, block_size: int =
 
 
 def main():
-    layer, step, _, _ = demo_layer([4500, 10000] * 4, topk=512, heads=128)
+    layer, step, _, _ = demo_layer([4500, 10000] * 4, topk=512, heads=128, temperature="logit")
     out, lse, idx, _ = layer.decode(**step)
     turned = latent.rope(step["q_pe"], step["positions"], layer.plan, out=torch.empty_like(step["q_pe"]))
     dense, dense_lse = layer.decode_dense(step["q_latent"], turned, step["seq_lens"], step["max_seq_len"])
