@@ -208,8 +208,10 @@ __global__ void __maxnreg__(120) decode_kernel(const __grid_constant__ CUtensorM
         tmem_relinquish();
     }
     // every CTA's barriers are initialised before any CTA sends it anything
-    // (the first unit's query rows): a whole-cluster barrier, its wait after
-    // the scan below
+    // (the first unit's query rows): a whole-cluster barrier
+    cluster_arrive();
+    cluster_wait();
+    // the first half of the per-unit barrier (its wait follows the stream)
     cluster_arrive();
     // Launched with programmatic serialization, the set-up above may overlap
     // the kernels before this one in the stream.  Nothing below runs before
@@ -247,9 +249,6 @@ __global__ void __maxnreg__(120) decode_kernel(const __grid_constant__ CUtensorM
         total += t;
     }
     const uint32_t tmem = ks->tmem_base;
-    cluster_wait();
-    // the first half of the per-unit barrier (its wait follows the stream)
-    cluster_arrive();
     if (tid == 0) DSAIDX_PHASE(0, 1);
 
     uint32_t tcnt = 0;   // tiles streamed by this CTA so far (stage, phase and accumulator)
