@@ -45,8 +45,8 @@ N_POOL_COPIES = 9
 # hash of the measured kernel's code (its translation unit and every header it
 # includes, comments left out) when they were taken; a stale hash reports null.
 NCU_TRAFFIC = {
-    ("decode", "cd4902da1e770c88"): 31444992 + 0,
-    ("longctx", "cd4902da1e770c88"): 277246976 + 2784256,
+    ("decode", "48a7f21120405f64"): 31445248 + 0,
+    ("longctx", "48a7f21120405f64"): 277248768 + 2736896,
     ("prefill", "9a835175a16cef1b"): 139506432 + 536455936,   # the scoring kernel
 }
 KERNEL_TU = {"decode": "decode.cu", "longctx": "decode.cu", "prefill": "prefill.cu"}
