@@ -24,7 +24,12 @@
  * pool, a length beyond its bound) sets the status word, skips the offending
  * key or row and faults nothing.  Status words are sticky: the library never
  * clears them.  Strides are in elements.  A row without a visible key has
- * out 0 and lse -inf.  Sums and softmax statistics are fp32.
+ * out 0 and lse -inf.  Sums and softmax statistics are fp32; the weights are
+ * rounded to bf16 (2^-8 relative) for the product with the values, so results
+ * are off by up to that beside their own rounding.  Waits between a kernel's
+ * roles end after 2 s with IDX_ERR_TIMEOUT; the longest one spans the keys one
+ * CTA takes of a row (1.3 to 2 us for 64 of them), so a row of tens of millions
+ * of keys that is not cut can run into it.
  * Every call may be captured into a CUDA graph.  idx_kernel_timing records the
  * attention calls' kernels too (outside capture).
  */
@@ -67,7 +72,10 @@ typedef enum idx_rope_scaling { IDX_ROPE_NONE = 0, IDX_ROPE_LINEAR = 1, IDX_ROPE
  *  Language Models", 2023): f_i (1 - r_i) + f_i / factor * r_i, r_i the ramp
  *  from pair floor(d(beta_fast)) to ceil(d(beta_slow)) with
  *  d(b) = rot_dim ln(original_max_pos / (2 pi b)) / (2 ln base), and the
- *  amplitude 0.1 ln(factor) + 1 (at factor > 1).
+ *  amplitude 0.1 ln(factor) + 1 (at factor > 1).  The ramp is linear in the pair
+ *  index, as models with this scaling are configured and trained; the paper's
+ *  text has it linear in original_max_pos / wavelength, which is another ramp
+ *  between the same two ends.
  * *amplitude_out (1 unless YARN) scales the turned values.
  * rot_dim even, 2..1024; base > 1; factor >= 1 for LINEAR and YARN.
  */

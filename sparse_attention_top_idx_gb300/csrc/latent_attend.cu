@@ -34,8 +34,8 @@
 // (weights stay below 256, in fp32 and in bf16 with the same relative error),
 // so most tiles need neither a maximum over keys nor a rescaled accumulator:
 // one barrier with an OR decides for all heads.  Weights are rounded to bf16
-// for the value product (relative 2^-9, as large as the rounding of the
-// result); their sums, the statistics and both accumulators are fp32.
+// for the value product (relative 2^-8 at most, as large as the rounding of
+// the result); their sums, the statistics and both accumulators are fp32.
 //
 // Few rows over many keys: the tiles of all rows form one line that is cut
 // into equal runs, one a CTA; a row that is cut leaves partial sums (fp32) in
@@ -44,12 +44,13 @@
 // partial sums in shared memory and join each other's, a share of the heads
 // each, through it.
 //
-// Measured: a tile takes 1.3 us at 16 heads (58 bytes a ns and SM, the rate of
+// Measured: a tile takes 1.26 us at 16 heads (58 bytes a ns and SM, the rate of
 // the copies themselves: without products or without reading memory it stays;
-// long contexts: 6.6 TB/s, bound by HBM) and 1.46 us at 64 (4096 rows of 1024
-// keys, 128 heads, 1.41 ms, 827 TFLOP/s: near the copies' rate and that of the
-// tensor cores, whose steps of 64 columns take 24 and 32 ns with two issuing
-// warps against 16.4 at full rate).
+// long contexts: 6.6 TB/s, bound by HBM) and 1.40 us at 64 (152 rows of 16,384
+// keys each).  4096 rows of 1024 keys, 128 heads: 1.38 ms, 846 TFLOP/s, 1.60 us
+// a tile with the rows' beginnings and ends; 1.37 us of it are the steps of the
+// products (36 of 64 keys x 64 heads at 24 ns, 16 of 128 dimensions x 64 heads
+// at 32 ns, two issuing warps; 10.4 and 20.8 ns at the measured 1912 TFLOP/s).
 #include <cuda_bf16.h>
 
 #include <cmath>

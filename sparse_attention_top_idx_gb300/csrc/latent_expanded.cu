@@ -24,14 +24,16 @@
 // A row's maximum moves only when a score passes it by 2^8 (weights stay
 // below 256 in fp32, and bf16 rounds them with the same relative error), so
 // that most tiles take one pass over the scores and leave the accumulator
-// alone.  Weights are rounded to bf16 for the value product (relative 2^-9,
-// as large as the rounding of the result); their sums are taken before that.
+// alone.  Weights are rounded to bf16 for the value product (relative 2^-8 at
+// most, as large as the rounding of the result); their sums are taken before
+// that.
 //
-// Measured: 8192 queries on 22,000 keys, 16 heads, 1.02 ms, 1476 TFLOP/s, bound
-// by the tensor cores.  Every wait and commit of the issuing lane counts: with
-// a barrier a unit (twelve waits a key tile instead of four) it took 1.15 ms;
-// with a second issuing warp, one a query tile, 1.46 ms, as the tiles then run
-// in step and neither covers the other's softmax.
+// Measured: 8192 queries on 22,000 keys, 16 heads, 1.05 to 1.06 ms, 1410 to 1430
+// TFLOP/s, bound by the tensor cores.  Every wait and commit of the issuing lane
+// counts (all on the box where this kernel took 1.02 ms): with a barrier a unit
+// (twelve waits a key tile instead of four) 1.15 ms; with a second issuing warp,
+// one a query tile, 1.46 ms, as the tiles then run in step and neither covers
+// the other's softmax.
 #include <cuda_bf16.h>
 
 #include <cmath>
