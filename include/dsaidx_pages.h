@@ -1,0 +1,123 @@
+/*
+ * dsaidx_pages.h -- C ABI of libdsaidx's pages: which blocks of the paged
+ * caches are whose.  One block table names the same block in every pool it
+ * serves (index keys, latent records, of every layer), so a page is a block id
+ * and what it holds is its block in each pool.
+ *
+ * refs_dev [num_blocks] int32 says how many table entries name a page; 0 is a
+ * free page.  That array is the whole state: a page is taken by naming it in a
+ * table and setting its count, and the free pages taken are always the ones
+ * with the lowest ids, handed out in the order of the rows.  Every entry >= 0
+ * of a table row counts as one reference; entries behind a row's pages are -1.
+ * Full pages may be shared by several rows, as nothing is written to them any
+ * more; a partly filled last page belongs to one row alone, so that appends
+ * need no check.
+ *
+ * Conventions are those of dsaidx.h: caller-owned device memory, nothing
+ * allocated or synchronised, host-side argument errors before any launch,
+ * sticky status words for what only the device can see, calls may be captured
+ * into CUDA graphs.  Calls on the same refs or tables must not overlap.  Block
+ * tables are [rows, max_blocks_per_seq] int32, contiguous.
+ */
+#ifndef DSAIDX_PAGES_H
+#define DSAIDX_PAGES_H
+
+#include "dsaidx.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+#define IDX_PAGES_MAX_ROWS 65536         /* rows of one call */
+#define IDX_PAGES_MAX_POOLS 128          /* pools of one idx_pages_copy */
+#define IDX_PAGES_MAX_BLOCKS (1 << 28)
+#define IDX_PAGES_MAX_CELLS (1 << 30)    /* entries of a block table */
+
+/* A pool: num_blocks blocks of block_bytes (a multiple of 16), 16-byte
+ * aligned. */
+typedef struct idx_page_pool {
+    void* data_dev;
+    int64_t block_bytes;
+} idx_page_pool;
+
+/* Workspace bytes of idx_pages_fork / _extend / _compact over num_blocks pages
+ * and at most `rows` rows.  0 on invalid arguments.  The first word is the
+ * call's status; zero the workspace once with idx_workspace_init. */
+size_t idx_pages_workspace_bytes(int64_t num_blocks, int rows);
+
+/*
+ * Forks rows: row i of the new table continues row parents_dev[i] of the old
+ * one (-1: an empty row; the same parent may come many times).  Its full pages
+ * are shared (their counts go up by one each); where the parent's last page is
+ * partly filled the row gets a free page of its own and pairs_dev[i] = (old
+ * page, new page), else (-1, -1): idx_pages_copy then copies the contents.
+ * new_lens_dev[i] is the parent's length, entries behind the row's pages are
+ * -1.  The old rows stay as they are; what the new rows held before is not
+ * looked at (idx_pages_free them first).
+ * Device checks (status, and the row is empty): a parent outside [-1,
+ * old_rows), a length that is negative or beyond its table row or the new one,
+ * no free page left (then no row behind it that needs one gets any).  A page
+ * id outside the pool sets the status and its entry becomes -1.
+ * The tables, lengths and refs must not overlap one another.
+ */
+idx_status idx_pages_fork(int32_t* refs_dev, int64_t num_blocks, int block_size, const int32_t* table_dev,
+                          int old_rows, int max_blocks_per_seq, const int32_t* seq_lens_dev,
+                          const int32_t* parents_dev, int rows, int32_t* new_table_dev, int new_max_blocks_per_seq,
+                          int32_t* new_lens_dev, int32_t* pairs_dev, void* workspace_dev, size_t ws_bytes,
+                          void* stream);
+
+/*
+ * Gives every row the pages that take it from seq_lens_dev[i] to
+ * longer_dev[i] tokens and sets seq_lens_dev[i] to it.  Device checks (status,
+ * and the row stays as it is): a length that is negative, falls or passes the
+ * table row, or not enough free pages for the row (then no row behind it that
+ * needs pages gets any).
+ */
+idx_status idx_pages_extend(int32_t* refs_dev, int64_t num_blocks, int block_size, int32_t* table_dev, int rows,
+                            int max_blocks_per_seq, int32_t* seq_lens_dev, const int32_t* longer_dev,
+                            void* workspace_dev, size_t ws_bytes, void* stream);
+
+/*
+ * Ends rows: every entry >= 0 of each row named in which_dev [n] (null: rows 0
+ * to n - 1) gives its reference back and becomes -1, and the row's length
+ * becomes 0.  A row named twice ends once.  Device checks (status_dev,
+ * nullable): a row outside the table (skipped), a page outside the pool or
+ * already free (its entry becomes -1, no count changes).
+ */
+idx_status idx_pages_free(int32_t* refs_dev, int64_t num_blocks, int32_t* table_dev, int rows,
+                          int max_blocks_per_seq, int32_t* seq_lens_dev, const int32_t* which_dev, int n,
+                          int32_t* status_dev, void* stream);
+
+/*
+ * Moves the pages in use to the front: with n of them, the k-th page in use
+ * from id n on goes to the k-th free page below n; the others keep their ids.
+ * Writes the counts and the table after the move (in place where new_refs_dev
+ * == refs_dev or new_table_dev == table_dev, otherwise neither overlaps
+ * another), map_dev[num_blocks] = the new id of every page (-1: free), pairs_dev
+ * [num_blocks / 2] = (old page, new page) of the pages that moved, by old id,
+ * and (-1, -1) behind them, and *count_dev = their number.  Then
+ * idx_pages_copy moves the contents: no page is both read and written.
+ * Tables elsewhere that name these pages follow through map_dev.
+ * Device check: a table entry >= 0 that names no page in use becomes -1 and
+ * sets the status.
+ */
+idx_status idx_pages_compact(const int32_t* refs_dev, int64_t num_blocks, const int32_t* table_dev, int rows,
+                             int max_blocks_per_seq, int32_t* new_refs_dev, int32_t* new_table_dev, int32_t* map_dev,
+                             int32_t* pairs_dev, int32_t* count_dev, void* workspace_dev, size_t ws_bytes,
+                             void* stream);
+
+/*
+ * Copies page pairs_dev[i][0] to page pairs_dev[i][1] in every pool, i < n, or
+ * i < *count_dev where count_dev is not null (and at most n).  Pairs with a
+ * negative page are skipped; one with a page outside the pool too, and sets
+ * status_dev (nullable).  Pairs take no order: no page may be written twice or
+ * be both read and written.
+ */
+idx_status idx_pages_copy(const idx_page_pool* pools, int num_pools, int64_t num_blocks, const int32_t* pairs_dev,
+                          int64_t n, const int32_t* count_dev, int32_t* status_dev, void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* DSAIDX_PAGES_H */

@@ -1,0 +1,92 @@
+/*
+ * dsaidx_qlatent.h -- C ABI of libdsaidx's latent cache in 8 bits: the paged
+ * records of dsaidx_latent.h at 644 bytes a token instead of 1152, their
+ * append, their read-back and the absorbed attention over them.
+ *
+ *   record[slot] = scale * [ c (512 x fp8 e4m3) | p (64 x bf16) ]
+ *   s[t, h, j]   = softmax_scale * (ql[t, h] . scale_j c_j + qp[t, h] . scale_j p_j)
+ *   out[t, h]    = sum_j softmax_j(s) scale_j c_j       lse[t, h] = ln sum_j exp s
+ *
+ * One scale a token (the latent is the one key and value "head" of all query
+ * heads), a power of two: a block of tokens with a common scale would have to
+ * re-encode earlier tokens when a later one is larger, and as the codes are
+ * floating-point numbers themselves a finer scale would buy nothing but range.
+ * A power of two also leaves the position part exact: p is held divided by the
+ * scale, in bf16.
+ *
+ * A block of block_size tokens holds block_size records of 640 bytes (512
+ * codes, 64 bf16) and behind them block_size fp32 scales; blocks are
+ * idx_qlatent_block_bytes apart (a multiple of 128).  Slots, block tables,
+ * status words, strides, workspaces (idx_latent_workspace_bytes), streams and
+ * errors are those of dsaidx_latent.h, and the pool is its idx_latent_pool
+ * with blocks of this layout.
+ *
+ * Accuracy: scores are products of the stored values with the query held as
+ * two e4m3 numbers under a power of two of each (row, head), which leaves
+ * 2^-22 of the head's largest |ql| at most; sums and softmax statistics are
+ * fp32; weights are held in 9 significant bits (three e5m2 numbers) for the
+ * product with the values, weights below 2^-26 of the row's largest weight
+ * times scale in fewer, below 2^-28 in none.  A non-finite ql makes its head's
+ * results NaN.
+ */
+#ifndef DSAIDX_QLATENT_H
+#define DSAIDX_QLATENT_H
+
+#include "dsaidx_latent.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+#define IDX_QLATENT_ROW_BYTES 640        /* a record without its scale */
+
+/* Bytes of a block of block_size (1..65536) tokens: 644 a token, rounded up to
+ * 128; 0 on an invalid size. */
+size_t idx_qlatent_block_bytes(int block_size);
+
+/*
+ * Encodes and writes the records of n tokens.  Arguments are
+ * idx_latent_append's.  scale = 2^e with the least e at which no |latent|
+ * exceeds 448 * 2^e, within [-32, 120] (2^0 for a latent of zeros); codes are
+ * latent / scale, rounded to nearest even; p is k_pe turned by its position
+ * (fp32, one rounding to bf16) or as it is, divided by the scale.  Non-finite
+ * latents become NaN codes and do not count for the scale.  A slot given twice
+ * holds one of its tokens' codes, position values and scale, not necessarily
+ * of the same one.
+ */
+idx_status idx_qlatent_append(const idx_latent_pool* pool, const void* latent_dev, int64_t latent_stride,
+                              const void* pe_dev, int64_t pe_stride, const int64_t* positions_dev,
+                              const int64_t* slot_mapping_dev, int64_t n, const uint64_t* steps_dev, float amplitude,
+                              unsigned flags, int32_t* status_dev, void* stream);
+
+/*
+ * Reads back the records at n slots: out_dev [n, 576] bf16 (row stride
+ * out_stride, a multiple of 8 and at least 576; 16-byte aligned) =
+ * [latent 512 | turned key 64] as idx_latent_append would have held them, the
+ * latents rounded to their codes.  A negative slot gives a row of zeros, one
+ * beyond the pool too and sets status_dev (nullable).  Exact where the scale
+ * is a power of two.
+ */
+idx_status idx_qlatent_read(const idx_latent_pool* pool, const int64_t* slots_dev, int64_t n, void* out_dev,
+                            int64_t out_stride, int32_t* status_dev, void* stream);
+
+/* idx_latent_attend_slots over records in 8 bits. */
+idx_status idx_qlatent_attend_slots(const idx_latent_pool* pool, const void* ql_dev, int64_t ql_row_stride,
+                                    int64_t ql_head_stride, const void* qp_dev, int64_t qp_row_stride,
+                                    int64_t qp_head_stride, const int64_t* slots_dev, int64_t slots_stride,
+                                    int64_t rows, int heads, int topk, float scale, void* out_dev, float* lse_dev,
+                                    void* workspace_dev, size_t ws_bytes, void* stream);
+
+/* idx_latent_attend_paged over records in 8 bits. */
+idx_status idx_qlatent_attend_paged(const idx_latent_pool* pool, const void* ql_dev, int64_t ql_row_stride,
+                                    int64_t ql_head_stride, const void* qp_dev, int64_t qp_row_stride,
+                                    int64_t qp_head_stride, const int32_t* block_table_dev, int max_blocks_per_seq,
+                                    const int32_t* seq_lens_dev, int batch, int max_seq_len, int heads, float scale,
+                                    void* out_dev, float* lse_dev, void* workspace_dev, size_t ws_bytes,
+                                    void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* DSAIDX_QLATENT_H */

@@ -3,60 +3,11 @@
 // is allocated and no stream synchronised.
 #include <cmath>
 
-#include "internal.h"
 #include "latent.h"
+#include "latent_check.h"
 #include "strides.h"
 
 using namespace dsaidx;
-
-namespace {
-
-bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
-bool mult8(int64_t s) { return s % 8 == 0; }
-
-constexpr int64_t kInt31 = int64_t(1) << 31;
-
-// Number of SMs of the current device, asked for once a device.
-bool sm_count(int* sms) {
-    static std::atomic<int> known[64];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return false;
-    const bool kept = dev >= 0 && dev < 64;
-    if (kept && (*sms = known[dev].load(std::memory_order_relaxed)) > 0) return true;
-    if (cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return false;
-    if (kept) known[dev].store(*sms, std::memory_order_relaxed);
-    return true;
-}
-
-bool pool_ok(const idx_latent_pool* p) {
-    if (!p || !p->data_dev || !aligned(p->data_dev, 128)) return false;
-    if (p->block_size < 1 || p->block_size > 65536 || p->num_blocks < 1 || p->num_blocks >= kInt31) return false;
-    return p->num_blocks * p->block_size < kInt31;
-}
-
-idx_status status_of(cudaError_t e) { return e == cudaSuccess ? IDX_OK : IDX_ERR_CUDA; }
-
-// What the two absorbed calls check alike.
-idx_status attend_check(const idx_latent_pool* pool, const void* ql, int64_t ql_row, int64_t ql_head, const void* qp,
-                        int64_t qp_row, int64_t qp_head, int64_t rows, int heads, int64_t max_keys, int64_t keys_cap,
-                        float scale, const void* out, const void* ws, size_t ws_bytes, bool paged) {
-    if (!pool_ok(pool) || rows < 0 || heads < 1 || heads > IDX_LATENT_MAX_HEADS || max_keys < 0 || max_keys > keys_cap)
-        return IDX_ERR_INVALID_ARG;
-    if (!std::isfinite(scale)) return IDX_ERR_INVALID_ARG;
-    if (rows >= kInt31 || rows * ((heads + 63) / 64) >= kInt31) return IDX_ERR_INVALID_ARG;
-    if (rows == 0) return IDX_OK;
-    if (!ql || !qp || !out || !ws) return IDX_ERR_INVALID_ARG;
-    if (!aligned(ql, 16) || !aligned(qp, 16) || !aligned(out, 16) || !aligned(ws, 256)) return IDX_ERR_INVALID_ARG;
-    if (!mult8(ql_row) || !mult8(ql_head) || !mult8(qp_row) || !mult8(qp_head)) return IDX_ERR_INVALID_ARG;
-    // strides that are stepped over: positive and within a tensor map's range
-    const int64_t cap = int64_t(1) << 38;
-    if (rows > 1 && (ql_row < 1 || ql_row > cap || qp_row < 1 || qp_row > cap)) return IDX_ERR_INVALID_ARG;
-    if (heads > 1 && (ql_head < 1 || ql_head > cap || qp_head < 1 || qp_head > cap)) return IDX_ERR_INVALID_ARG;
-    if (ws_bytes < attend_ws_need(rows, heads, max_keys, paged)) return IDX_ERR_WORKSPACE_TOO_SMALL;
-    return IDX_OK;
-}
-
-}  // namespace
 
 extern "C" {
 
@@ -148,7 +99,7 @@ idx_status idx_latent_attend_slots(const idx_latent_pool* pool, const void* ql_d
                                    void* workspace_dev, size_t ws_bytes, void* stream) {
     const idx_status c = attend_check(pool, ql_dev, ql_row_stride, ql_head_stride, qp_dev, qp_row_stride,
                                       qp_head_stride, rows, heads, topk, int64_t(1) << 24, scale, out_dev,
-                                      workspace_dev, ws_bytes, false);
+                                      workspace_dev, ws_bytes, false, attend_ws_need);
     if (c != IDX_OK || rows == 0) return c;
     if ((!slots_dev && topk > 0) || !aligned(slots_dev, 8)) return IDX_ERR_INVALID_ARG;
     AttendArgs a{};
@@ -171,7 +122,7 @@ idx_status idx_latent_attend_paged(const idx_latent_pool* pool, const void* ql_d
     if (max_blocks_per_seq < 1) return IDX_ERR_INVALID_ARG;
     const idx_status c = attend_check(pool, ql_dev, ql_row_stride, ql_head_stride, qp_dev, qp_row_stride,
                                       qp_head_stride, batch, heads, max_seq_len, kInt31 - 256, scale, out_dev,
-                                      workspace_dev, ws_bytes, true);
+                                      workspace_dev, ws_bytes, true, attend_ws_need);
     if (c != IDX_OK || batch == 0) return c;
     if (!block_table_dev || !seq_lens_dev || !aligned(block_table_dev, 4) || !aligned(seq_lens_dev, 4))
         return IDX_ERR_INVALID_ARG;

@@ -1,0 +1,653 @@
+// pages.cu -- idx_pages_*: counts, block tables and contents of the pages that
+// the paged caches share (declared in include/dsaidx_pages.h).
+//
+// Fork and extend are two kernels.  take_kernel lists the free pages in the
+// order of their ids (one cluster: each CTA counts its share of the counts,
+// the shares are added up through distributed shared memory, then each lists
+// its own) and, beside it, how many pages the rows before each row need.  The
+// second kernel reads both: row i's pages are entries [before_i, before_i +
+// need_i) of the list, so that who gets what depends on nothing but the counts
+// and the rows.  Compaction ranks pages in the same way.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "common.cuh"
+#include "dsaidx_pages.h"
+#include "internal.h"
+
+namespace dsaidx {
+
+namespace {
+
+constexpr int kScanCtas = 8;          // CTAs of the cluster that looks the counts through
+constexpr int kScanThreads = 1024;
+constexpr int kScanWarps = kScanThreads / 32;
+constexpr int kRowThreads = 256;      // table kernels: columns a CTA
+constexpr int kCopyThreads = 256;
+constexpr int kCopyVecs = 4;          // 16-byte vectors a thread has in flight
+constexpr int kSlice = kCopyThreads * kCopyVecs * 16;
+
+__host__ __device__ __forceinline__ int pages_of(int64_t tokens, int block_size) {
+    return static_cast<int>((tokens + block_size - 1) / block_size);
+}
+
+// Behind the workspace's header: free pages found, then `before` [rows] and
+// the list of free pages.
+struct Taken {
+    int32_t* found;
+    int32_t* before;
+    int32_t* list;
+};
+
+struct Rows {
+    int32_t* refs;
+    const int32_t* table;      // of the parents (extend: of the rows)
+    const int32_t* lens;
+    const int32_t* parents;    // null: extend
+    const int32_t* longer;     // null: fork
+    int32_t* new_table;
+    int32_t* new_lens;
+    int32_t* pairs;
+    int32_t* status;
+    int num_blocks, block_size, old_rows, mbps, rows, new_mbps;
+    int cap;                   // entries of the list that can be asked for
+    Taken taken;
+};
+
+// What row i is: its length before and after, and the pages it needs; false
+// where a device check fails.
+struct RowNeed {
+    int parent, length, after, need;
+};
+__device__ __forceinline__ bool row_need(const Rows& a, int i, RowNeed& r) {
+    r.need = r.length = r.after = 0;
+    r.parent = i;
+    if (a.longer == nullptr) {
+        r.parent = a.parents[i];
+        if (r.parent == -1) return true;
+        if (r.parent < 0 || r.parent >= a.old_rows) return false;
+        const int n = a.lens[r.parent];
+        if (n < 0 || n > static_cast<int64_t>(a.mbps) * a.block_size || n > static_cast<int64_t>(a.new_mbps) * a.block_size)
+            return false;
+        r.length = r.after = n;
+        r.need = n % a.block_size != 0;
+        return true;
+    }
+    const int n = a.lens[i], m = a.longer[i];
+    if (n < 0 || m < n || m > static_cast<int64_t>(a.mbps) * a.block_size) return false;
+    r.length = n;
+    r.after = m;
+    r.need = pages_of(m, a.block_size) - pages_of(n, a.block_size);
+    return true;
+}
+
+// Sum over the block and, per thread, the sum of the threads before it.
+__device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total) {
+    const int lane = lane_id(), warp = warp_id();
+    int x = v;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int u = __shfl_up_sync(~0u, x, d);
+        if (lane >= d) x += u;
+    }
+    __syncthreads();       // the sums of a scan before are read
+    if (lane == 31) warp_sums[warp] = x;
+    __syncthreads();
+    int w = warp_sums[lane & (kScanWarps - 1)];
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int u = __shfl_up_sync(~0u, w, d);
+        if (lane >= d) w += u;
+    }
+    total = __shfl_sync(~0u, w, 31);
+    const int before = __shfl_sync(~0u, w, warp > 0 ? warp - 1 : 0);
+    return x - v + (warp > 0 ? before : 0);
+}
+
+// Sum of `mine` over the CTAs of the cluster before this one, and over all.
+__device__ __forceinline__ int cluster_scan(int mine, int* slot, int& total) {
+    __syncthreads();
+    if (threadIdx.x == 0) *slot = mine;
+    cluster_arrive();
+    cluster_wait();
+    const int rank = static_cast<int>(cluster_rank());
+    int before = 0;
+    total = 0;
+#pragma unroll
+    for (int r = 0; r < kScanCtas; ++r) {
+        const int v = static_cast<int>(dsmem_ld_u32(dsmem_addr(slot, r)));
+        if (r < rank) before += v;
+        total += v;
+    }
+    // read by all before anyone writes it again or leaves
+    cluster_arrive();
+    cluster_wait();
+    return before;
+}
+
+// A warp's share of the pages: `steps` groups of 128 from `first` on, four
+// pages a lane.  Pages past the end count as neither free nor in use.
+struct Share {
+    int first, steps;
+};
+__device__ __forceinline__ Share share_of(int num_blocks) {
+    const int groups = (num_blocks + 127) / 128;
+    const int per = (groups + kScanCtas * kScanWarps - 1) / (kScanCtas * kScanWarps);
+    const int w = static_cast<int>(cluster_rank()) * kScanWarps + warp_id();
+    const int from = w * per < groups ? w * per : groups, to = from + per < groups ? from + per : groups;
+    return {from * 128, to - from};
+}
+__device__ __forceinline__ int4 counts_at(const int32_t* refs, int num_blocks, int p) {
+    if (p + 4 <= num_blocks) return *reinterpret_cast<const int4*>(refs + p);
+    int4 v = make_int4(-1, -1, -1, -1);
+    if (p < num_blocks) v.x = refs[p];
+    if (p + 1 < num_blocks) v.y = refs[p + 1];
+    if (p + 2 < num_blocks) v.z = refs[p + 2];
+    return v;
+}
+__device__ __forceinline__ int warp_before(int v, int& total) {
+    int x = v;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int u = __shfl_up_sync(~0u, x, d);
+        if (lane_id() >= d) x += u;
+    }
+    total = __shfl_sync(~0u, x, 31);
+    return x - v;
+}
+
+__global__ void __launch_bounds__(kScanThreads, 1) take_kernel(const Rows a) {
+    __shared__ int warp_sums[32];
+    __shared__ int slot;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (blockIdx.x >= kScanCtas) {
+        // the other cluster: what the rows before each row need
+        if (blockIdx.x > kScanCtas) return;
+        int before = 0;
+        for (int i0 = 0; i0 < a.rows; i0 += kScanThreads) {
+            const int i = i0 + threadIdx.x;
+            RowNeed r{0, 0, 0, 0};
+            if (i < a.rows && !row_need(a, i, r)) r.need = 0;
+            int total;
+            const int at = block_scan(r.need, warp_sums, total);
+            // no more than the pool has are ever given, so sums stop there
+            if (i < a.rows) a.taken.before[i] = before + at;
+            before = min(before + total, a.num_blocks + 1);
+        }
+        return;
+    }
+    const Share s = share_of(a.num_blocks);
+    const int lane = lane_id();
+    int mine = 0;
+    for (int k = 0; k < s.steps; ++k) {
+        const int4 v = counts_at(a.refs, a.num_blocks, s.first + 128 * k + 4 * lane);
+        mine += (v.x == 0) + (v.y == 0) + (v.z == 0) + (v.w == 0);
+    }
+    int in_cta, found, in_warp;
+    const int at_thread = block_scan(mine, warp_sums, in_cta);
+    const int at_cta = cluster_scan(in_cta, &slot, found);
+    int at = at_cta + __shfl_sync(~0u, at_thread, 0);
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.taken.found = found;
+    for (int k = 0; k < s.steps && at < a.cap; ++k) {
+        const int p = s.first + 128 * k + 4 * lane;
+        const int4 v = counts_at(a.refs, a.num_blocks, p);
+        const int c = (v.x == 0) + (v.y == 0) + (v.z == 0) + (v.w == 0);
+        int to = at + warp_before(c, in_warp);
+        if (v.x == 0 && to < a.cap) a.taken.list[to] = p;
+        to += v.x == 0;
+        if (v.y == 0 && to < a.cap) a.taken.list[to] = p + 1;
+        to += v.y == 0;
+        if (v.z == 0 && to < a.cap) a.taken.list[to] = p + 2;
+        to += v.z == 0;
+        if (v.w == 0 && to < a.cap) a.taken.list[to] = p + 3;
+        at += in_warp;
+    }
+}
+
+// Row blockIdx.x, columns [blockIdx.y * kRowThreads, ...) and every
+// gridDim.y-th such piece.
+__global__ void __launch_bounds__(kRowThreads) fork_kernel(const Rows a) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int i = blockIdx.x;
+    RowNeed r;
+    bool ok = row_need(a, i, r);
+    const int before = a.taken.before[i];
+    if (ok && r.need > 0) ok = before < *a.taken.found;
+    if (!ok) r.length = r.need = 0;
+    const int full = r.length / a.block_size;
+    const int32_t* old = a.table + static_cast<int64_t>(r.length > 0 ? r.parent : 0) * a.mbps;
+    int32_t* row = a.new_table + static_cast<int64_t>(i) * a.new_mbps;
+    for (int j = blockIdx.y * kRowThreads + threadIdx.x; j < a.new_mbps; j += gridDim.y * kRowThreads) {
+        int page = -1;
+        if (j < full) {
+            page = old[j];
+            if (page < 0 || page >= a.num_blocks) {
+                set_status(a.status, IDX_ERR_DEVICE_CHECK);
+                page = -1;
+            } else {
+                atomicAdd(a.refs + page, 1);
+            }
+        } else if (j == full && r.need > 0) {
+            page = a.taken.list[before];
+            a.refs[page] = 1;
+        }
+        row[j] = page;
+    }
+    if (blockIdx.y == 0 && threadIdx.x == 0) {
+        if (!ok) set_status(a.status, IDX_ERR_DEVICE_CHECK);
+        a.new_lens[i] = r.length;
+        int from = -1, to = -1;
+        if (r.need > 0) {
+            from = old[full];
+            to = a.taken.list[before];
+            if (from < 0 || from >= a.num_blocks) {
+                set_status(a.status, IDX_ERR_DEVICE_CHECK);
+                from = to = -1;
+            }
+        }
+        a.pairs[2 * i] = from;
+        a.pairs[2 * i + 1] = to;
+    }
+}
+
+// A warp a row.
+__global__ void __launch_bounds__(kRowThreads) extend_kernel(const Rows a) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int i = blockIdx.x * (kRowThreads / 32) + warp_id(), lane = lane_id();
+    if (i >= a.rows) return;
+    RowNeed r;
+    bool ok = row_need(a, i, r);
+    const int before = a.taken.before[i];
+    if (ok && r.need > 0) ok = before + r.need <= *a.taken.found;
+    if (!ok) {
+        if (lane == 0) set_status(a.status, IDX_ERR_DEVICE_CHECK);
+        return;
+    }
+    int32_t* row = a.new_table + static_cast<int64_t>(i) * a.mbps + pages_of(r.length, a.block_size);
+    for (int j = lane; j < r.need; j += 32) {
+        const int page = a.taken.list[before + j];
+        row[j] = page;
+        a.refs[page] = 1;
+    }
+    __syncwarp();          // every lane has read the length
+    if (lane == 0) a.new_lens[i] = r.after;
+}
+
+struct FreeArgs {
+    int32_t* refs;
+    int32_t* table;
+    int32_t* lens;
+    const int32_t* which;
+    int32_t* status;
+    int num_blocks, rows, mbps, n;
+};
+__global__ void __launch_bounds__(kRowThreads) free_kernel(const FreeArgs a) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int row = a.which == nullptr ? static_cast<int>(blockIdx.x) : a.which[blockIdx.x];
+    const bool first = blockIdx.y == 0 && threadIdx.x == 0;
+    if (row < 0 || row >= a.rows) {
+        if (first) set_status(a.status, IDX_ERR_DEVICE_CHECK);
+        return;
+    }
+    if (first) a.lens[row] = 0;
+    int32_t* t = a.table + static_cast<int64_t>(row) * a.mbps;
+    for (int j = blockIdx.y * kRowThreads + threadIdx.x; j < a.mbps; j += gridDim.y * kRowThreads) {
+        // a row named twice: one of the two takes the entry
+        const int page = a.which == nullptr ? t[j] : atomicExch(t + j, -1);
+        if (page < 0) continue;
+        if (a.which == nullptr) t[j] = -1;
+        if (page >= a.num_blocks) {
+            set_status(a.status, IDX_ERR_DEVICE_CHECK);
+        } else if (atomicSub(a.refs + page, 1) <= 0) {
+            atomicAdd(a.refs + page, 1);
+            set_status(a.status, IDX_ERR_DEVICE_CHECK);
+        }
+    }
+}
+
+struct CompactArgs {
+    const int32_t* refs;
+    const int32_t* table;
+    int32_t* new_refs;
+    int32_t* new_table;
+    int32_t* map;
+    int2* pairs;
+    int32_t* count;
+    int32_t* status;
+    int num_blocks;
+    int64_t cells;
+};
+
+// One cluster.  Pages in use are counted (n); then those from n on and the
+// free ones below n are ranked, each list in the order of the ids.
+__global__ void __launch_bounds__(kScanThreads, 1) compact_kernel(const CompactArgs a) {
+    __shared__ int warp_sums[32];
+    __shared__ int slot;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const Share s = share_of(a.num_blocks);
+    const int lane = lane_id();
+    int mine = 0, in_cta, n, moves, holes, in_warp;
+    for (int k = 0; k < s.steps; ++k) {
+        const int4 v = counts_at(a.refs, a.num_blocks, s.first + 128 * k + 4 * lane);
+        mine += (v.x > 0) + (v.y > 0) + (v.z > 0) + (v.w > 0);
+    }
+    block_scan(mine, warp_sums, in_cta);
+    cluster_scan(in_cta, &slot, n);
+    int from = 0, to = 0;
+    for (int k = 0; k < s.steps; ++k) {
+        const int p = s.first + 128 * k + 4 * lane;
+        const int4 v = counts_at(a.refs, a.num_blocks, p);
+        const int c[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            from += c[e] > 0 && p + e >= n;
+            to += c[e] <= 0 && p + e < n;
+        }
+    }
+    int at_from = __shfl_sync(~0u, block_scan(from, warp_sums, in_cta), 0);
+    at_from += cluster_scan(in_cta, &slot, moves);
+    int at_to = __shfl_sync(~0u, block_scan(to, warp_sums, in_cta), 0);
+    at_to += cluster_scan(in_cta, &slot, holes);       // as many
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.count = moves;
+    for (int k = 0; k < s.steps; ++k) {
+        const int p = s.first + 128 * k + 4 * lane;
+        const int4 v = counts_at(a.refs, a.num_blocks, p);
+        const int c[4] = {v.x, v.y, v.z, v.w};
+        int cf = 0, ct = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            cf += c[e] > 0 && p + e >= n;
+            ct += c[e] <= 0 && p + e < n;
+        }
+        int f = at_from + warp_before(cf, in_warp);
+        at_from += in_warp;
+        int t = at_to + warp_before(ct, in_warp);
+        at_to += in_warp;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (p + e >= a.num_blocks) continue;
+            const bool used = c[e] > 0;
+            if (p + e >= n && used) {
+                a.pairs[f++].x = p + e;                // its count moves below
+                continue;
+            }
+            a.map[p + e] = used ? p + e : -1;
+            if (p + e < n && !used) {
+                a.pairs[t++].y = p + e;
+                continue;
+            }
+            a.new_refs[p + e] = used ? c[e] : 0;
+        }
+    }
+    // the cluster's lists are complete
+    cluster_arrive();
+    cluster_wait();
+    for (int k = blockIdx.x * kScanThreads + threadIdx.x; k < a.num_blocks / 2; k += kScanCtas * kScanThreads) {
+        if (k >= moves) {
+            a.pairs[k] = make_int2(-1, -1);
+            continue;
+        }
+        const int2 v = __ldcg(a.pairs + k);
+        const int held = a.refs[v.x];
+        a.map[v.x] = v.y;
+        a.new_refs[v.y] = held;
+        a.new_refs[v.x] = 0;
+    }
+}
+
+__global__ void __launch_bounds__(kRowThreads) remap_kernel(const CompactArgs a) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kRowThreads + threadIdx.x; i < a.cells;
+         i += static_cast<int64_t>(gridDim.x) * kRowThreads) {
+        int page = a.table[i];
+        if (page >= 0) {
+            page = page < a.num_blocks ? a.map[page] : -1;
+            if (page < 0) set_status(a.status, IDX_ERR_DEVICE_CHECK);
+        } else {
+            page = -1;
+        }
+        a.new_table[i] = page;
+    }
+}
+
+struct CopyArgs {
+    uint8_t* base[IDX_PAGES_MAX_POOLS];
+    int64_t bytes[IDX_PAGES_MAX_POOLS];       // of a block
+    int first[IDX_PAGES_MAX_POOLS + 1];       // slices of a page in the pools before
+    const int2* pairs;
+    const int32_t* count;
+    int32_t* status;
+    int64_t n, num_blocks;
+    int pools;
+};
+
+// Bound by memory: each page read and written once.  A unit of work is 16 KB of
+// a page in one pool, every thread four 16-byte vectors in flight.
+__global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const __grid_constant__ CopyArgs a) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    int64_t n = a.n;
+    if (a.count != nullptr) n = max(int64_t(0), min(n, static_cast<int64_t>(*a.count)));
+    const int slices = a.first[a.pools];
+    for (int64_t u = blockIdx.x; u < n * slices; u += gridDim.x) {
+        const int64_t i = u / slices;
+        const int s = static_cast<int>(u - i * slices);
+        const int2 pair = a.pairs[i];
+        if (pair.x < 0 || pair.y < 0) continue;
+        if (pair.x >= a.num_blocks || pair.y >= a.num_blocks) {
+            if (threadIdx.x == 0) set_status(a.status, IDX_ERR_DEVICE_CHECK);
+            continue;
+        }
+        int k = 0, above = a.pools;            // first[k] <= s < first[k + 1]
+        while (above - k > 1) {
+            const int mid = (k + above) >> 1;
+            if (a.first[mid] <= s) k = mid; else above = mid;
+        }
+        const int64_t bytes = a.bytes[k], at = static_cast<int64_t>(s - a.first[k]) * kSlice + 16 * threadIdx.x;
+        const uint8_t* src = a.base[k] + pair.x * bytes + at;
+        uint8_t* dst = a.base[k] + pair.y * bytes + at;
+        uint4 v[kCopyVecs];
+#pragma unroll
+        for (int e = 0; e < kCopyVecs; ++e)
+            if (at + e * kCopyThreads * 16 < bytes) v[e] = __ldcs(reinterpret_cast<const uint4*>(src + e * kCopyThreads * 16));
+#pragma unroll
+        for (int e = 0; e < kCopyVecs; ++e)
+            if (at + e * kCopyThreads * 16 < bytes) __stcs(reinterpret_cast<uint4*>(dst + e * kCopyThreads * 16), v[e]);
+    }
+}
+
+bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+bool word(const void* p) { return p != nullptr && aligned(p, 4); }
+// Two arrays of int32 that share no element.
+bool apart(const void* a, int64_t na, const void* b, int64_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return na <= 0 || nb <= 0 || x + 4 * static_cast<uintptr_t>(na) <= y || y + 4 * static_cast<uintptr_t>(nb) <= x;
+}
+bool pool_size_ok(int64_t num_blocks) { return num_blocks >= 1 && num_blocks <= IDX_PAGES_MAX_BLOCKS; }
+// Sums over the rows of a table stay below 2^31.
+bool table_ok(int rows, int mbps) {
+    return rows >= 0 && rows <= IDX_PAGES_MAX_ROWS && mbps >= 1 && int64_t(rows) * mbps <= IDX_PAGES_MAX_CELLS;
+}
+idx_status status_of(cudaError_t e) { return e == cudaSuccess ? IDX_OK : IDX_ERR_CUDA; }
+
+size_t workspace(int64_t num_blocks, int rows) {
+    return align_up(kWsHeaderBytes + 4 * (static_cast<size_t>(rows) + static_cast<size_t>(num_blocks)) + 4, 256);
+}
+Taken taken_of(void* ws, int rows) {
+    int32_t* w = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + kWsHeaderBytes);
+    return {w, w + 1, w + 1 + rows};
+}
+
+template <class... Params, class... Args>
+cudaError_t launch(void (*kernel)(Params...), dim3 grid, int threads, int cluster, cudaStream_t st, const Args&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// CTAs along a row of n columns: enough that few rows fill the device too.
+unsigned row_pieces(int rows, int n) {
+    const int all = (n + kRowThreads - 1) / kRowThreads, want = (1216 + rows - 1) / rows;
+    return static_cast<unsigned>(all < want ? all : want);
+}
+
+}  // namespace
+
+}  // namespace dsaidx
+
+using namespace dsaidx;
+
+extern "C" {
+
+size_t idx_pages_workspace_bytes(int64_t num_blocks, int rows) {
+    if (!pool_size_ok(num_blocks) || rows < 0 || rows > IDX_PAGES_MAX_ROWS) return 0;
+    return workspace(num_blocks, rows);
+}
+
+idx_status idx_pages_fork(int32_t* refs_dev, int64_t num_blocks, int block_size, const int32_t* table_dev,
+                          int old_rows, int max_blocks_per_seq, const int32_t* seq_lens_dev,
+                          const int32_t* parents_dev, int rows, int32_t* new_table_dev, int new_max_blocks_per_seq,
+                          int32_t* new_lens_dev, int32_t* pairs_dev, void* workspace_dev, size_t ws_bytes,
+                          void* stream) {
+    if (!pool_size_ok(num_blocks) || block_size < 1 || block_size > 65536 || !table_ok(old_rows, max_blocks_per_seq) ||
+        !table_ok(rows, new_max_blocks_per_seq))
+        return IDX_ERR_INVALID_ARG;
+    if (rows == 0) return IDX_OK;
+    if (!word(refs_dev) || !aligned(refs_dev, 16) || !word(parents_dev) || !word(new_table_dev) || !word(new_lens_dev) ||
+        !word(pairs_dev) || workspace_dev == nullptr || !aligned(workspace_dev, 256))
+        return IDX_ERR_INVALID_ARG;
+    if (old_rows > 0 && (!word(table_dev) || !word(seq_lens_dev))) return IDX_ERR_INVALID_ARG;
+    const void* arrays[] = {refs_dev, new_table_dev, new_lens_dev, pairs_dev, table_dev, seq_lens_dev, parents_dev};
+    const int64_t sizes[] = {num_blocks, int64_t(rows) * new_max_blocks_per_seq, rows, int64_t(2) * rows,
+                             int64_t(old_rows) * max_blocks_per_seq, old_rows, rows};
+    for (int i = 0; i < 4; ++i)                // what is written
+        for (int j = i + 1; j < 7; ++j)
+            if (!apart(arrays[i], sizes[i], arrays[j], sizes[j])) return IDX_ERR_INVALID_ARG;
+    if (ws_bytes < workspace(num_blocks, rows)) return IDX_ERR_WORKSPACE_TOO_SMALL;
+    const Rows a{refs_dev, table_dev, seq_lens_dev, parents_dev, nullptr, new_table_dev, new_lens_dev, pairs_dev,
+                 static_cast<int32_t*>(workspace_dev), static_cast<int>(num_blocks), block_size, old_rows,
+                 max_blocks_per_seq, rows, new_max_blocks_per_seq,
+                 static_cast<int>(rows < num_blocks ? rows : num_blocks), taken_of(workspace_dev, rows)};
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = launch(take_kernel, dim3(2 * kScanCtas), kScanThreads, kScanCtas, st, a);
+    if (e != cudaSuccess) return status_of(e);
+    return status_of(launch(fork_kernel, dim3(rows, row_pieces(rows, new_max_blocks_per_seq)), kRowThreads, 1, st, a));
+}
+
+idx_status idx_pages_extend(int32_t* refs_dev, int64_t num_blocks, int block_size, int32_t* table_dev, int rows,
+                            int max_blocks_per_seq, int32_t* seq_lens_dev, const int32_t* longer_dev,
+                            void* workspace_dev, size_t ws_bytes, void* stream) {
+    if (!pool_size_ok(num_blocks) || block_size < 1 || block_size > 65536 || !table_ok(rows, max_blocks_per_seq))
+        return IDX_ERR_INVALID_ARG;
+    if (rows == 0) return IDX_OK;
+    if (!word(refs_dev) || !aligned(refs_dev, 16) || !word(table_dev) || !word(seq_lens_dev) || !word(longer_dev) ||
+        workspace_dev == nullptr || !aligned(workspace_dev, 256))
+        return IDX_ERR_INVALID_ARG;
+    const int64_t cells = int64_t(rows) * max_blocks_per_seq;
+    if (!apart(refs_dev, num_blocks, table_dev, cells) || !apart(refs_dev, num_blocks, seq_lens_dev, rows) ||
+        !apart(refs_dev, num_blocks, longer_dev, rows) || !apart(table_dev, cells, seq_lens_dev, rows) ||
+        !apart(table_dev, cells, longer_dev, rows) || !apart(seq_lens_dev, rows, longer_dev, rows))
+        return IDX_ERR_INVALID_ARG;
+    if (ws_bytes < workspace(num_blocks, rows)) return IDX_ERR_WORKSPACE_TOO_SMALL;
+    const Rows a{refs_dev, table_dev, seq_lens_dev, nullptr, longer_dev, table_dev, seq_lens_dev, nullptr,
+                 static_cast<int32_t*>(workspace_dev), static_cast<int>(num_blocks), block_size, rows,
+                 max_blocks_per_seq, rows, max_blocks_per_seq, static_cast<int>(num_blocks), taken_of(workspace_dev, rows)};
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = launch(take_kernel, dim3(2 * kScanCtas), kScanThreads, kScanCtas, st, a);
+    if (e != cudaSuccess) return status_of(e);
+    return status_of(launch(extend_kernel, dim3((rows + kRowThreads / 32 - 1) / (kRowThreads / 32)), kRowThreads, 1, st, a));
+}
+
+idx_status idx_pages_free(int32_t* refs_dev, int64_t num_blocks, int32_t* table_dev, int rows,
+                          int max_blocks_per_seq, int32_t* seq_lens_dev, const int32_t* which_dev, int n,
+                          int32_t* status_dev, void* stream) {
+    if (!pool_size_ok(num_blocks) || !table_ok(rows, max_blocks_per_seq) || n < 0 || n > IDX_PAGES_MAX_ROWS ||
+        (which_dev == nullptr && n > rows))
+        return IDX_ERR_INVALID_ARG;
+    if (n == 0) return IDX_OK;
+    if (!word(refs_dev) || !aligned(which_dev, 4) || !aligned(status_dev, 4)) return IDX_ERR_INVALID_ARG;
+    if (rows > 0 && (!word(table_dev) || !word(seq_lens_dev))) return IDX_ERR_INVALID_ARG;
+    const FreeArgs a{refs_dev, table_dev, seq_lens_dev, which_dev, status_dev, static_cast<int>(num_blocks), rows,
+                     max_blocks_per_seq, n};
+    return status_of(launch(free_kernel, dim3(n, row_pieces(n, max_blocks_per_seq)), kRowThreads, 1,
+                            static_cast<cudaStream_t>(stream), a));
+}
+
+idx_status idx_pages_compact(const int32_t* refs_dev, int64_t num_blocks, const int32_t* table_dev, int rows,
+                             int max_blocks_per_seq, int32_t* new_refs_dev, int32_t* new_table_dev, int32_t* map_dev,
+                             int32_t* pairs_dev, int32_t* count_dev, void* workspace_dev, size_t ws_bytes,
+                             void* stream) {
+    if (!pool_size_ok(num_blocks) || !table_ok(rows, max_blocks_per_seq)) return IDX_ERR_INVALID_ARG;
+    if (!word(refs_dev) || !aligned(refs_dev, 16) || !word(new_refs_dev) || !word(map_dev) || !word(count_dev) ||
+        workspace_dev == nullptr || !aligned(workspace_dev, 256))
+        return IDX_ERR_INVALID_ARG;
+    if (num_blocks > 1 && (!word(pairs_dev) || !aligned(pairs_dev, 8))) return IDX_ERR_INVALID_ARG;
+    if (rows > 0 && (!word(table_dev) || !word(new_table_dev))) return IDX_ERR_INVALID_ARG;
+    const int64_t cells = int64_t(rows) * max_blocks_per_seq;
+    const void* arrays[] = {new_refs_dev, new_table_dev, map_dev, pairs_dev, count_dev, refs_dev, table_dev};
+    const int64_t sizes[] = {num_blocks, cells, num_blocks, num_blocks / 2 * 2, 1, num_blocks, cells};
+    for (int i = 0; i < 5; ++i)                // what is written
+        for (int j = i + 1; j < 7; ++j) {
+            const bool in_place = (i == 0 && j == 5) || (i == 1 && j == 6);
+            if (!(in_place && arrays[i] == arrays[j]) && !apart(arrays[i], sizes[i], arrays[j], sizes[j]))
+                return IDX_ERR_INVALID_ARG;
+        }
+    if (ws_bytes < kWsHeaderBytes) return IDX_ERR_WORKSPACE_TOO_SMALL;
+    const CompactArgs a{refs_dev, table_dev, new_refs_dev, new_table_dev, map_dev, reinterpret_cast<int2*>(pairs_dev),
+                        count_dev, static_cast<int32_t*>(workspace_dev), static_cast<int>(num_blocks), cells};
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = launch(compact_kernel, dim3(kScanCtas), kScanThreads, kScanCtas, st, a);
+    if (e != cudaSuccess || cells == 0) return status_of(e);
+    const int64_t grid = (cells + kRowThreads - 1) / kRowThreads;
+    return status_of(launch(remap_kernel, dim3(static_cast<unsigned>(grid < 1216 ? grid : 1216)), kRowThreads, 1, st, a));
+}
+
+idx_status idx_pages_copy(const idx_page_pool* pools, int num_pools, int64_t num_blocks, const int32_t* pairs_dev,
+                          int64_t n, const int32_t* count_dev, int32_t* status_dev, void* stream) {
+    if (num_pools < 0 || num_pools > IDX_PAGES_MAX_POOLS || !pool_size_ok(num_blocks) || n < 0 || n > IDX_PAGES_MAX_BLOCKS)
+        return IDX_ERR_INVALID_ARG;
+    if (num_pools > 0 && pools == nullptr) return IDX_ERR_INVALID_ARG;
+    CopyArgs a;
+    int64_t slices = 0;
+    for (int k = 0; k < num_pools; ++k) {
+        const int64_t b = pools[k].block_bytes;
+        if (pools[k].data_dev == nullptr || !aligned(pools[k].data_dev, 16) || b < 16 || b % 16 || b > (int64_t(1) << 32))
+            return IDX_ERR_INVALID_ARG;
+        a.base[k] = static_cast<uint8_t*>(pools[k].data_dev);
+        a.bytes[k] = b;
+        a.first[k] = static_cast<int>(slices);
+        slices += (b + kSlice - 1) / kSlice;
+    }
+    a.first[num_pools] = static_cast<int>(slices);
+    if (n == 0 || num_pools == 0) return IDX_OK;
+    if (!word(pairs_dev) || !aligned(pairs_dev, 8) || !aligned(count_dev, 4) || !aligned(status_dev, 4))
+        return IDX_ERR_INVALID_ARG;
+    a.pairs = reinterpret_cast<const int2*>(pairs_dev);
+    a.count = count_dev;
+    a.status = status_dev;
+    a.n = n;
+    a.num_blocks = num_blocks;
+    a.pools = num_pools;
+    const int64_t units = n * slices, most = 152 * 8;
+    return status_of(launch(copy_pages_kernel, dim3(static_cast<unsigned>(units < most ? units : most)), kCopyThreads, 1,
+                            static_cast<cudaStream_t>(stream), a));
+}
+
+}  // extern "C"

@@ -1,7 +1,8 @@
-"""ctypes binding of libdsaidx's latent attention (include/dsaidx_latent.h):
-rotary positions, the append to a paged latent cache, and attention over the
-indexer's selected slots, over whole paged contexts (absorbed form) and over
-prompts (expanded form).
+"""ctypes binding of libdsaidx's latent attention (include/dsaidx_latent.h and,
+for records in 8 bits, include/dsaidx_qlatent.h): rotary positions, the append
+to a paged latent cache, and attention over the indexer's selected slots, over
+whole paged contexts (absorbed form) and over prompts (expanded form).  The
+calls on a cache take a LatentCache (bf16) or a QuantLatentCache (8 bits).
 
 Argument marshalling only, as in dsaidx: tensors are checked for device (one
 for all of a call's tensors, the current one), dtype and shape and passed as
@@ -20,6 +21,7 @@ from . import dsaidx
 from .dsaidx import IdxError
 
 HEADER = os.path.join(os.path.dirname(dsaidx.HEADER), "dsaidx_latent.h")
+QUANT_HEADER = os.path.join(os.path.dirname(dsaidx.HEADER), "dsaidx_qlatent.h")
 
 LATENT_DIM = 512
 PE_DIM = 64
@@ -60,16 +62,23 @@ def load():
     L.idx_latent_attend_paged.argtypes = [POOL, P, I64, I64, P, I64, I64, P, I, P, I, I, I, F, P, P, P, SZ, P]
     L.idx_latent_attend_expanded.argtypes = [P, I64, I64, P, I64, I64, P, I64, P, I64, I64, P, P, I, I64, I64, I, F,
                                              P, P, P, P]
+    L.idx_qlatent_block_bytes.argtypes = [I]
+    L.idx_qlatent_block_bytes.restype = SZ
+    L.idx_qlatent_append.argtypes = L.idx_latent_append.argtypes
+    L.idx_qlatent_read.argtypes = [POOL, P, I64, P, I64, P, P]
+    L.idx_qlatent_attend_slots.argtypes = L.idx_latent_attend_slots.argtypes
+    L.idx_qlatent_attend_paged.argtypes = L.idx_latent_attend_paged.argtypes
     for f in (L.idx_rope_steps, L.idx_rope, L.idx_latent_append, L.idx_latent_attend_slots,
-              L.idx_latent_attend_paged, L.idx_latent_attend_expanded):
+              L.idx_latent_attend_paged, L.idx_latent_attend_expanded, L.idx_qlatent_append, L.idx_qlatent_read,
+              L.idx_qlatent_attend_slots, L.idx_qlatent_attend_paged):
         f.restype = I
     _bound = L
     return L
 
 
-def header_functions():
-    """Names of the functions include/dsaidx_latent.h declares."""
-    src = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
+def header_functions(header: str = HEADER):
+    """Names of the functions include/dsaidx_latent.h (or another header) declares."""
+    src = re.sub(r"/\*.*?\*/", "", open(header).read(), flags=re.S)
     return sorted(set(re.findall(r"\b(idx_[a-z_]+)\s*\(", src)))
 
 
@@ -212,6 +221,7 @@ def rope(x: torch.Tensor, positions: torch.Tensor, plan: RopePlan, layout: int =
 class LatentCache:
     """A caller-owned pool of latent records: a bf16 CUDA tensor
     [num_blocks, block_size, 576], each record [latent 512 | turned key 64]."""
+    calls = ("idx_latent_append", "idx_latent_attend_slots", "idx_latent_attend_paged")
 
     def __init__(self, pool: torch.Tensor):
         self.device = _dev(pool, "pool")
@@ -228,12 +238,41 @@ class LatentCache:
         return LatentCache(torch.zeros(num_blocks, block_size, RECORD, dtype=torch.bfloat16, device=device))
 
 
-def latent_append(cache: LatentCache, latent: torch.Tensor, k_pe: torch.Tensor, positions: Optional[torch.Tensor],
+def quant_block_bytes(block_size: int) -> int:
+    """idx_qlatent_block_bytes: bytes of a block of records in 8 bits (0: no such size)."""
+    return int(load().idx_qlatent_block_bytes(block_size))
+
+
+class QuantLatentCache:
+    """A caller-owned pool of latent records in 8 bits: a uint8 CUDA tensor
+    [num_blocks, quant_block_bytes(block_size)], each record scale * [512 codes
+    (e4m3) | turned key 64 (bf16)].  For latent_append, latent_read,
+    latent_attend_slots and latent_attend_paged."""
+    calls = ("idx_qlatent_append", "idx_qlatent_attend_slots", "idx_qlatent_attend_paged")
+
+    def __init__(self, pool: torch.Tensor, block_size: int):
+        self.device = _dev(pool, "pool")
+        _dense(pool, torch.uint8, "pool", self.device)
+        nb = quant_block_bytes(block_size)
+        if nb == 0 or pool.dim() != 2 or pool.shape[1] != nb:
+            raise ValueError("pool must be [num_blocks, %d] for blocks of %d tokens" % (nb, block_size))
+        self.pool = pool
+        self.num_blocks, self.block_size = int(pool.shape[0]), block_size
+        self._desc = _Pool(pool.data_ptr(), self.num_blocks, block_size)
+        self.desc = ctypes.byref(self._desc)   # what the calls take
+
+    @staticmethod
+    def allocate(num_blocks: int, block_size: int, device="cuda"):
+        return QuantLatentCache(torch.zeros(num_blocks, quant_block_bytes(block_size), dtype=torch.uint8, device=device),
+                                block_size)
+
+
+def latent_append(cache, latent: torch.Tensor, k_pe: torch.Tensor, positions: Optional[torch.Tensor],
                   slot_mapping: torch.Tensor, plan: Optional[RopePlan], layout: int = INTERLEAVED,
                   status: Optional[torch.Tensor] = None, stream=None):
-    """idx_latent_append: write n tokens' records (latent [n, 512], k_pe
-    [n, 64], rows may be strided) to their slots, k_pe turned by positions
-    [n] int64 on the way (copied where plan is None)."""
+    """idx_latent_append, idx_qlatent_append: write n tokens' records (latent
+    [n, 512], k_pe [n, 64], rows may be strided) to their slots, k_pe turned by
+    positions [n] int64 on the way (copied where plan is None), in the cache's format."""
     n, dev = latent.shape[0], _dev(latent, "latent")
     if cache.device != dev:
         _elsewhere("cache", cache.device, dev)
@@ -248,16 +287,35 @@ def latent_append(cache: LatentCache, latent: torch.Tensor, k_pe: torch.Tensor, 
             raise ValueError("plan must turn %d elements" % PE_DIM)
         pos, steps = _dense(positions, torch.int64, "positions", dev, (n,)), plan.on_device(dev)
         amplitude = plan.amplitude
-    err = (_bound or load()).idx_latent_append(cache.desc, lp, ls[0], kp, ks[0], pos,
-                                               _dense(slot_mapping, torch.int64, "slot_mapping", dev, (n,)), n, steps,
-                                               amplitude, layout, _maybe(status, torch.int32, "status", dev),
-                                               _stream(stream, dev))
+    name = cache.calls[0]
+    err = getattr(_bound or load(), name)(cache.desc, lp, ls[0], kp, ks[0], pos,
+                                          _dense(slot_mapping, torch.int64, "slot_mapping", dev, (n,)), n, steps,
+                                          amplitude, layout, _maybe(status, torch.int32, "status", dev),
+                                          _stream(stream, dev))
     if err:
-        raise IdxError(err, "idx_latent_append")
+        raise IdxError(err, name)
+
+
+def latent_read(cache: QuantLatentCache, slots: torch.Tensor, out: torch.Tensor,
+                status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """idx_qlatent_read: the records at slots [n] int64 into out [n, 576] bf16
+    (rows may be strided), [latent 512 | turned key 64]; zeros where a slot is negative."""
+    if not isinstance(cache, QuantLatentCache):
+        raise TypeError("cache must be a QuantLatentCache")
+    n, dev = slots.shape[0], _dev(slots, "slots")
+    if cache.device != dev:
+        _elsewhere("cache", cache.device, dev)
+    op, os_ = _strided(out, torch.bfloat16, "out", dev, (n, RECORD))
+    err = (_bound or load()).idx_qlatent_read(cache.desc, _dense(slots, torch.int64, "slots", dev, (n,)), n, op,
+                                              os_[0] if n > 1 else RECORD, _maybe(status, torch.int32, "status", dev),
+                                              _stream(stream, dev))
+    if err:
+        raise IdxError(err, "idx_qlatent_read")
+    return out
 
 
 def workspace_bytes(rows: int, heads: int, max_keys: int) -> int:
-    """idx_latent_workspace_bytes: workspace of one absorbed attention call."""
+    """idx_latent_workspace_bytes: workspace of one absorbed attention call over either kind of cache."""
     return int(load().idx_latent_workspace_bytes(rows, heads, max_keys))
 
 
@@ -276,10 +334,10 @@ def _absorbed(cache, q_latent, q_pe, out, lse, workspace):
              _dense(workspace, torch.uint8, "workspace", dev), workspace.numel()))
 
 
-def latent_attend_slots(cache: LatentCache, q_latent: torch.Tensor, q_pe: torch.Tensor, slots: torch.Tensor,
+def latent_attend_slots(cache, q_latent: torch.Tensor, q_pe: torch.Tensor, slots: torch.Tensor,
                         scale: float, out: torch.Tensor, workspace: torch.Tensor,
                         lse: Optional[torch.Tensor] = None, stream=None):
-    """idx_latent_attend_slots: each row's queries (q_latent [rows, heads, 512],
+    """idx_latent_attend_slots, idx_qlatent_attend_slots: each row's queries (q_latent [rows, heads, 512],
     q_pe [rows, heads, 64]) attend over the records at its slots [rows, topk]
     int64 (the out_slot of the score calls; negative entries are skipped).
     out [rows, heads, 512] bf16, lse [rows, heads] fp32."""
@@ -288,22 +346,22 @@ def latent_attend_slots(cache: LatentCache, q_latent: torch.Tensor, q_pe: torch.
         raise ValueError("slots must be [rows, topk]")
     topk = slots.shape[1]
     sp, ss = _strided(slots, torch.int64, "slots", dev, (T, topk))
-    _check(load().idx_latent_attend_slots(cache.desc, *query, sp, ss[0], T, H, topk, scale, *result,
-                                          _stream(stream, dev)), "idx_latent_attend_slots")
+    name = cache.calls[1]
+    _check(getattr(load(), name)(cache.desc, *query, sp, ss[0], T, H, topk, scale, *result, _stream(stream, dev)), name)
 
 
-def latent_attend_paged(cache: LatentCache, q_latent: torch.Tensor, q_pe: torch.Tensor, block_table: torch.Tensor,
+def latent_attend_paged(cache, q_latent: torch.Tensor, q_pe: torch.Tensor, block_table: torch.Tensor,
                         seq_lens: torch.Tensor, max_seq_len: int, scale: float, out: torch.Tensor,
                         workspace: torch.Tensor, lse: Optional[torch.Tensor] = None, stream=None):
-    """idx_latent_attend_paged: one query a sequence over all its records
+    """idx_latent_attend_paged, idx_qlatent_attend_paged: one query a sequence over all its records
     (block_table [batch, max_blocks_per_seq], seq_lens [batch] int32)."""
     dev, T, H, query, result = _absorbed(cache, q_latent, q_pe, out, lse, workspace)
     if block_table.dim() != 2 or block_table.shape[0] != T:
         raise ValueError("block_table must be [batch, max_blocks_per_seq]")
-    _check(load().idx_latent_attend_paged(cache.desc, *query, _dense(block_table, torch.int32, "block_table", dev),
-                                          block_table.shape[1], _dense(seq_lens, torch.int32, "seq_lens", dev, (T,)), T,
-                                          max_seq_len, H, scale, *result, _stream(stream, dev)),
-           "idx_latent_attend_paged")
+    name = cache.calls[2]
+    _check(getattr(load(), name)(cache.desc, *query, _dense(block_table, torch.int32, "block_table", dev),
+                                 block_table.shape[1], _dense(seq_lens, torch.int32, "seq_lens", dev, (T,)), T,
+                                 max_seq_len, H, scale, *result, _stream(stream, dev)), name)
 
 
 def latent_attend_expanded(q: torch.Tensor, k_nope: torch.Tensor, k_pe: torch.Tensor, v: torch.Tensor,

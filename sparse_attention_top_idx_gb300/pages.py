@@ -1,0 +1,175 @@
+"""ctypes binding of libdsaidx's pages (include/dsaidx_pages.h): which blocks of
+the paged caches are whose.
+
+One block table serves every pool of a PageSet (index keys and latent records,
+of every layer), so a page is a block id.  Rows are forked (full pages shared, a
+partly filled one copied), extended, freed, and the pool is compacted; the
+contents move with copy().  Argument marshalling only, as in dsaidx and latent;
+workspaces come from dsaidx.new_workspace.
+"""
+from __future__ import annotations
+
+import ctypes
+import os
+from typing import Optional, Sequence
+
+import torch
+
+from . import dsaidx
+from .dsaidx import IdxError
+from .latent import _dense, _dev, _elsewhere, _maybe, _stream
+
+HEADER = os.path.join(os.path.dirname(dsaidx.HEADER), "dsaidx_pages.h")
+
+MAX_POOLS = 128      # IDX_PAGES_MAX_POOLS
+
+
+class _PagePool(ctypes.Structure):
+    _fields_ = [("data_dev", ctypes.c_void_p), ("block_bytes", ctypes.c_int64)]
+
+
+_bound = None
+
+
+def load():
+    """The library with the argument types of the calls of this module."""
+    global _bound
+    L = dsaidx.load()
+    if _bound is L:
+        return L
+    P, I, I64, SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
+    L.idx_pages_workspace_bytes.argtypes = [I64, I]
+    L.idx_pages_workspace_bytes.restype = SZ
+    L.idx_pages_fork.argtypes = [P, I64, I, P, I, I, P, P, I, P, I, P, P, P, SZ, P]
+    L.idx_pages_extend.argtypes = [P, I64, I, P, I, I, P, P, P, SZ, P]
+    L.idx_pages_free.argtypes = [P, I64, P, I, I, P, P, I, P, P]
+    L.idx_pages_compact.argtypes = [P, I64, P, I, I, P, P, P, P, P, P, SZ, P]
+    L.idx_pages_copy.argtypes = [ctypes.POINTER(_PagePool), I, I64, P, I64, P, P, P]
+    for f in (L.idx_pages_fork, L.idx_pages_extend, L.idx_pages_free, L.idx_pages_compact, L.idx_pages_copy):
+        f.restype = I
+    _bound = L
+    return L
+
+
+def workspace_bytes(num_blocks: int, rows: int) -> int:
+    """idx_pages_workspace_bytes: workspace of one fork, extend or compact call."""
+    return int(load().idx_pages_workspace_bytes(num_blocks, rows))
+
+
+def _check(code: int, what: str):
+    if code:
+        raise IdxError(code, what)
+
+
+class PageSet:
+    """The counts of the pages (refs [num_blocks] int32) and the pools they are
+    blocks of: contiguous CUDA tensors of any type, num_blocks blocks each (an
+    IndexCache's pool, a LatentCache's, ...)."""
+
+    def __init__(self, refs: torch.Tensor, block_size: int, pools: Sequence[torch.Tensor] = ()):
+        self.device = _dev(refs, "refs")
+        self._refs = _dense(refs, torch.int32, "refs", self.device)
+        if refs.dim() != 1 or refs.numel() == 0:
+            raise ValueError("refs must be [num_blocks]")
+        self.refs, self.block_size, self.num_blocks = refs, int(block_size), refs.numel()
+        self.pools = list(pools)
+        if len(self.pools) > MAX_POOLS:
+            raise ValueError("at most %d pools" % MAX_POOLS)
+        self._desc = (_PagePool * max(len(self.pools), 1))()
+        for k, t in enumerate(self.pools):
+            at = _dense(t, getattr(t, "dtype", None), "pools[%d]" % k, self.device)
+            nbytes = t.numel() * t.element_size()
+            if nbytes == 0 or nbytes % self.num_blocks or nbytes // self.num_blocks % 16:
+                raise ValueError("pools[%d] must be %d blocks of a multiple of 16 bytes" % (k, self.num_blocks))
+            self._desc[k] = _PagePool(at, nbytes // self.num_blocks)
+
+    @staticmethod
+    def allocate(num_blocks: int, block_size: int, pools: Sequence[torch.Tensor] = (), device="cuda"):
+        """A set whose pages are all free."""
+        return PageSet(torch.zeros(num_blocks, dtype=torch.int32, device=device), block_size, pools)
+
+
+def _table(ps: PageSet, table, lens, name: str):
+    """Device, shape and addresses of a table and its rows' lengths."""
+    dev = _dev(table, name)
+    if ps.device != dev:
+        _elsewhere("page set", ps.device, dev)
+    if table.dim() != 2:
+        raise ValueError("%s must be [rows, max_blocks_per_seq]" % name)
+    rows, width = table.shape
+    return dev, rows, width, _dense(table, torch.int32, name, dev), (
+        None if lens is None else _dense(lens, torch.int32, "the lengths of " + name, dev, (rows,)))
+
+
+def fork(ps: PageSet, block_table: torch.Tensor, seq_lens: torch.Tensor, parents: torch.Tensor,
+         new_table: torch.Tensor, new_lens: torch.Tensor, pairs: torch.Tensor, workspace: torch.Tensor, stream=None):
+    """idx_pages_fork: row i of new_table [n, new_max_blocks_per_seq] continues
+    row parents[i] (int32, -1: an empty row) of block_table: full pages are
+    shared, a partly filled one becomes pairs[i] = (its page, a free page), to be
+    copied by copy(ps, pairs).  What new_table held is overwritten: free it first."""
+    dev, old, width, tp, lp = _table(ps, block_table, seq_lens, "block_table")
+    _, n, new_width, ntp, nlp = _table(ps, new_table, new_lens, "new_table")
+    _check((_bound or load()).idx_pages_fork(ps._refs, ps.num_blocks, ps.block_size, tp, old, width, lp,
+                                             _dense(parents, torch.int32, "parents", dev, (n,)), n, ntp, new_width, nlp,
+                                             _dense(pairs, torch.int32, "pairs", dev, (n, 2)),
+                                             _dense(workspace, torch.uint8, "workspace", dev), workspace.numel(),
+                                             _stream(stream, dev)), "idx_pages_fork")
+
+
+def extend(ps: PageSet, block_table: torch.Tensor, seq_lens: torch.Tensor, longer: torch.Tensor,
+           workspace: torch.Tensor, stream=None):
+    """idx_pages_extend: give every row the pages that take it from seq_lens to
+    longer [rows] int32 tokens; seq_lens becomes longer."""
+    dev, rows, width, tp, lp = _table(ps, block_table, seq_lens, "block_table")
+    _check((_bound or load()).idx_pages_extend(ps._refs, ps.num_blocks, ps.block_size, tp, rows, width, lp,
+                                               _dense(longer, torch.int32, "longer", dev, (rows,)),
+                                               _dense(workspace, torch.uint8, "workspace", dev), workspace.numel(),
+                                               _stream(stream, dev)), "idx_pages_extend")
+
+
+def free(ps: PageSet, block_table: torch.Tensor, seq_lens: torch.Tensor, which: Optional[torch.Tensor] = None,
+         status: Optional[torch.Tensor] = None, stream=None):
+    """idx_pages_free: end the rows named in which [n] int32 (None: all): their
+    pages' references go back, their entries become -1 and their lengths 0."""
+    dev, rows, width, tp, lp = _table(ps, block_table, seq_lens, "block_table")
+    n = rows if which is None else which.numel()
+    _check((_bound or load()).idx_pages_free(ps._refs, ps.num_blocks, tp, rows, width, lp,
+                                             _maybe(which, torch.int32, "which", dev, (n,)), n,
+                                             _maybe(status, torch.int32, "status", dev), _stream(stream, dev)),
+           "idx_pages_free")
+
+
+def compact(ps: PageSet, block_table: torch.Tensor, new_refs: torch.Tensor, new_table: torch.Tensor,
+            page_map: torch.Tensor, pairs: torch.Tensor, count: torch.Tensor, workspace: torch.Tensor, stream=None):
+    """idx_pages_compact: move the pages in use to the front.  new_refs and
+    new_table (which may be ps.refs and block_table) get the counts and the table
+    after it, page_map [num_blocks] every page's new id (-1: free), pairs
+    [num_blocks / 2, 2] (old, new) of those that move, count [1] their number;
+    copy(ps, pairs, count=count) then moves the contents."""
+    dev, rows, width, tp, _ = _table(ps, block_table, None, "block_table")
+    i32 = torch.int32
+    _check((_bound or load()).idx_pages_compact(ps._refs, ps.num_blocks, tp, rows, width,
+                                                _dense(new_refs, i32, "new_refs", dev, (ps.num_blocks,)),
+                                                _dense(new_table, i32, "new_table", dev, (rows, width)),
+                                                _dense(page_map, i32, "page_map", dev, (ps.num_blocks,)),
+                                                _dense(pairs, i32, "pairs", dev, (max(ps.num_blocks // 2, 1), 2)),
+                                                _dense(count, i32, "count", dev, (1,)),
+                                                _dense(workspace, torch.uint8, "workspace", dev), workspace.numel(),
+                                                _stream(stream, dev)), "idx_pages_compact")
+
+
+def copy(ps: PageSet, pairs: torch.Tensor, count: Optional[torch.Tensor] = None,
+         status: Optional[torch.Tensor] = None, stream=None):
+    """idx_pages_copy: copy page pairs[i, 0] to page pairs[i, 1] (pairs [n, 2]
+    int32) in every pool of the set; pairs with a negative page are skipped, as
+    are those from count [1] int32 on.  No page may be written twice or be both
+    read and written."""
+    dev = _dev(pairs, "pairs")
+    if ps.device != dev:
+        _elsewhere("page set", ps.device, dev)
+    n = pairs.shape[0]
+    _check((_bound or load()).idx_pages_copy(ps._desc, len(ps.pools), ps.num_blocks,
+                                             _dense(pairs, torch.int32, "pairs", dev, (n, 2)), n,
+                                             _maybe(count, torch.int32, "count", dev, (1,)),
+                                             _maybe(status, torch.int32, "status", dev), _stream(stream, dev)),
+           "idx_pages_copy")
