@@ -39,6 +39,7 @@ extern "C" {
 #endif
 
 #define IDX_QLATENT_ROW_BYTES 640        /* a record without its scale */
+#define IDX_QLATENT_MAX_POOL_BYTES (INT64_C(1) << 39)
 
 /* Bytes of a block of block_size (1..65536) tokens: 644 a token, rounded up to
  * 128; 0 on an invalid size. */

@@ -6,6 +6,15 @@
 
 using namespace dsaidx;
 
+namespace {
+
+// Records begin at multiples of 128 bytes, which the kernels count in 32 bits.
+bool qpool_ok(const idx_latent_pool* p) {
+    return pool_ok(p) && p->num_blocks <= IDX_QLATENT_MAX_POOL_BYTES / qlatent_block_bytes(p->block_size);
+}
+
+}  // namespace
+
 extern "C" {
 
 size_t idx_qlatent_block_bytes(int block_size) {
@@ -17,7 +26,7 @@ idx_status idx_qlatent_append(const idx_latent_pool* pool, const void* latent_de
                               const void* pe_dev, int64_t pe_stride, const int64_t* positions_dev,
                               const int64_t* slot_mapping_dev, int64_t n, const uint64_t* steps_dev, float amplitude,
                               unsigned flags, int32_t* status_dev, void* stream) {
-    if (!pool_ok(pool) || n < 0 || (flags & ~IDX_ROPE_HALF) != 0u) return IDX_ERR_INVALID_ARG;
+    if (!qpool_ok(pool) || n < 0 || (flags & ~IDX_ROPE_HALF) != 0u) return IDX_ERR_INVALID_ARG;
     if (n == 0) return IDX_OK;
     if (!latent_dev || !pe_dev || !slot_mapping_dev || (steps_dev && !positions_dev)) return IDX_ERR_INVALID_ARG;
     if (!aligned(latent_dev, 16) || !aligned(pe_dev, 16) || !mult8(latent_stride) || !mult8(pe_stride) ||
@@ -32,7 +41,7 @@ idx_status idx_qlatent_append(const idx_latent_pool* pool, const void* latent_de
 
 idx_status idx_qlatent_read(const idx_latent_pool* pool, const int64_t* slots_dev, int64_t n, void* out_dev,
                             int64_t out_stride, int32_t* status_dev, void* stream) {
-    if (!pool_ok(pool) || n < 0 || (n + 3) / 4 >= kInt31 || out_stride < IDX_LATENT_RECORD || !mult8(out_stride))
+    if (!qpool_ok(pool) || n < 0 || (n + 3) / 4 >= kInt31 || out_stride < IDX_LATENT_RECORD || !mult8(out_stride))
         return IDX_ERR_INVALID_ARG;
     if (n == 0) return IDX_OK;
     if (!slots_dev || !out_dev || !aligned(slots_dev, 8) || !aligned(out_dev, 16) || !aligned(status_dev, 4))
@@ -47,6 +56,7 @@ idx_status idx_qlatent_attend_slots(const idx_latent_pool* pool, const void* ql_
                                     int64_t qp_head_stride, const int64_t* slots_dev, int64_t slots_stride,
                                     int64_t rows, int heads, int topk, float scale, void* out_dev, float* lse_dev,
                                     void* workspace_dev, size_t ws_bytes, void* stream) {
+    if (!qpool_ok(pool)) return IDX_ERR_INVALID_ARG;
     const idx_status c = attend_check(pool, ql_dev, ql_row_stride, ql_head_stride, qp_dev, qp_row_stride,
                                       qp_head_stride, rows, heads, topk, int64_t(1) << 24, scale, out_dev,
                                       workspace_dev, ws_bytes, false, qattend_ws_need);
@@ -71,6 +81,7 @@ idx_status idx_qlatent_attend_paged(const idx_latent_pool* pool, const void* ql_
                                     void* out_dev, float* lse_dev, void* workspace_dev, size_t ws_bytes,
                                     void* stream) {
     if (max_blocks_per_seq < 1) return IDX_ERR_INVALID_ARG;
+    if (!qpool_ok(pool)) return IDX_ERR_INVALID_ARG;
     const idx_status c = attend_check(pool, ql_dev, ql_row_stride, ql_head_stride, qp_dev, qp_row_stride,
                                       qp_head_stride, batch, heads, max_seq_len, kInt31 - 256, scale, out_dev,
                                       workspace_dev, ws_bytes, true, qattend_ws_need);

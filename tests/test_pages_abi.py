@@ -51,7 +51,7 @@ def pool(data=A, blocks=4, bs=64):
 
 
 @pytest.mark.parametrize("bad", [dict(data=None), dict(data=A + 64), dict(blocks=0), dict(blocks=2 ** 31), dict(bs=0),
-                                 dict(bs=65537), dict(blocks=2 ** 27, bs=64)])
+                                 dict(bs=65537), dict(blocks=2 ** 27, bs=64), dict(blocks=1 << 24, bs=64)])
 def test_pool_refusals(lib, bad):
     assert lib.idx_qlatent_append(pool(**bad), A, 512, A, 64, A, A, 1, A, 1.0, 0, None, None) == INVALID
     assert lib.idx_qlatent_read(pool(**bad), A, 1, A, 576, None, None) == INVALID
