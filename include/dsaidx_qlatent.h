@@ -24,10 +24,10 @@
  * Accuracy: scores are products of the stored values with the query held as
  * two e4m3 numbers under a power of two of each (row, head), which leaves
  * 2^-22 of the head's largest |ql| at most; sums and softmax statistics are
- * fp32; weights are held in 9 significant bits (three e5m2 numbers) for the
- * product with the values, weights below 2^-26 of the row's largest weight
- * times scale in fewer, below 2^-28 in none.  A non-finite ql makes its head's
- * results NaN.
+ * fp32; a key's weight times its scale is held in 9 significant bits (three
+ * e5m2 numbers) for the product with its codes, below 2^-14 of the largest such
+ * product of the head in fewer, below 2^-24 in none.  A non-finite ql makes its
+ * head's results NaN.
  */
 #ifndef DSAIDX_QLATENT_H
 #define DSAIDX_QLATENT_H

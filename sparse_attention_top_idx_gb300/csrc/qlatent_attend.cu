@@ -4,13 +4,13 @@
 // with records s [c | p]:
 //   D   = c (q_hi + q_lo / 16) + p q_p      [64 keys, heads]
 //   y   = f s D - m,  w = 2^y               f: the head's factor, softmax scale and log2(e)
-//   O^T = c^T W,  W = w s 2^11 / s_max      [512, heads]       out = O s_max 2^-11 / sum w
+//   O^T = c^T W,  W = w s 2^7 / s_max       [512, heads]       out = O s_max 2^-7 / sum w
 // The codes are operands as they are: nothing is decoded.  What stands on the
 // other side is split into 8-bit numbers instead, which is exact or nearly so:
 //   queries   a bf16 under a power of two of its head is the sum of two e4m3,
 //             the second times 16 (to 2^-22 of the head's largest);
 //   weights   9 significant bits are the sum of three e5m2, whose 32 binades
-//             hold weights down to 2^-28 of the largest (two e4m3 would hold 8
+//             hold weights down to 2^-24 of the largest (two e4m3 would hold 8
 //             bits down to 2^-9 of it and lose a long context's small weights).
 // The parts are further columns of the same product, up to 32 heads: a step
 // of 64 keys x 32 columns takes 12.3 ns, of 64 columns 16.4, of 128 columns
@@ -22,21 +22,27 @@
 // One persistent CTA an SM, warp-specialised:
 //   warp 0     one lane issues the score products
 //   warp 2     one lane issues the value products
+//   warps 1, 3 copy a row's queries and split half of them
 //   warps 4-7, at 64 heads 12-15 too  softmax, half of the heads each, and
 //              epilogue, half of the dimensions each; a thread has one key
 //   warps 8-11 gather records, 16 keys of every tile each, with 16-byte
 //              asynchronous copies into a ring of tiles (four chunks of 128
-//              codes of 64 keys, one of the position parts), and split a row's
-//              queries while its first tiles are on their way
+//              codes of 64 keys, one of the position parts), and split the other
+//              half of a row's queries while its first tiles are on their way
 //
-// The running maximum of a head moves only when a score passes it by 2^4, so
-// most tiles need neither a maximum over keys nor a rescaled accumulator.
+// The running maximum of a head and the largest scale move only when a weight
+// times its scale is about to leave e5m2's range, 2^8 above them, so most tiles
+// need neither a maximum over keys nor a rescaled accumulator.  (Moving at 2^4
+// would hold weights down to 2^-28, and took 2.33 us a tile against 1.59 at 64
+// heads: nearly every tile moved some head's maximum.)
 // Statistics, sums and accumulators are fp32.  Rows are whole, shared by a
 // cluster or cut into equal runs as in latent_rows.cuh.
 #include <cuda_fp16.h>
 
+#include <algorithm>
 #include <cmath>
 
+#include "latent_map.h"
 #include "latent_rows.cuh"
 #include "qlatent.h"
 
@@ -45,31 +51,43 @@ namespace dsaidx {
 namespace {
 
 constexpr int kChunk = kKeys * 128;        // bytes of a chunk: 128 codes or 64 bf16 of 64 keys
-constexpr int kStage = 5 * kChunk;         // a tile: four chunks of codes, one of position parts
-constexpr int kFactors = 3;                // rows whose heads' factors are held: the softmax may be two rows behind
+constexpr int kTileChunks = 5;             // a tile: one chunk of position parts, four of codes
+constexpr int kFactors = 2;                // rows whose heads' factors are held
 constexpr int halves_of(int N) { return N == 64 ? 2 : 1; }      // softmax warpgroups
 constexpr int threads_of(int N) { return 256 + 128 * halves_of(N); }
 constexpr int kGatherThreads = 128;
-constexpr float kGrow = 4.0f;              // log2 by which a score may pass the maximum
-constexpr float kTop = 2048.0f;            // a weight of 1 under the largest scale: 2^4 above it is below fp16's largest
+// A head's weights times scales are held relative to a reference, at 2^7 where
+// they equal it and under 2^15 (half of the largest e5m2) in any case.  What
+// passes that moves the reference of its head, and of those it has passed by
+// 2^kNear, to the largest.
+constexpr float kMost = 32768.0f, kNear = 4.0f;
+constexpr uint32_t kMost16 = 0x7800u;      // kMost in fp16
+constexpr float kNoScale = 0x1p-100f;      // no unit for the scales yet
+constexpr float kMostScale = 0x1p30f;      // a scale above the unit at which that moves, up to kTopUnit
+constexpr float kTopUnit = 0x1p58f;        // 2^90 above the least scale that counts, so that weights stay finite
+constexpr float kLeast = 0x1p-32f;         // the format's least; less (a record never written) counts as that
+constexpr float kMostWeight = 0x1p100f;
 
-// Shared memory: queries (hi and lo rows), two weight tiles, the ring, then
-// scales, factors, statistics, masks and barriers.
+// Shared memory: queries (hi and lo rows), two weight tiles, the ring of
+// chunks, then scales, factors, statistics, masks and barriers.
 struct QPlan {
-    int stages, p_bytes, p_off, ring_off, scale_off, factor_off, stat_off, mask_off, bar_off, total;
+    int slots, tiles, p_bytes, p_off, ring_off, scale_off, factor_off, stat_off, mask_off, bar_off, total;
 };
 __host__ __device__ constexpr QPlan qplan_of(int N) {
     QPlan p{};
-    p.stages = N == 64 ? 3 : 4;
+    p.slots = N == 64 ? 15 : N == 32 ? 21 : 24;
+    // scales and masks of a tile are written when its last chunk's slot is
+    // free, so that many tiles' are held at once
+    p.tiles = (p.slots + kTileChunks - 1) / kTileChunks;
     p.p_bytes = N == 16 ? 4096 : N == 32 ? 8192 : 3 * 4096;
     int o = 5 * 2 * N * 128;
     p.p_off = o;      o += 2 * p.p_bytes;
-    p.ring_off = o;   o += p.stages * kStage;
-    p.scale_off = o;  o += p.stages * kKeys * 4;
+    p.ring_off = o;   o += p.slots * kChunk;
+    p.scale_off = o;  o += p.tiles * kKeys * 4;
     p.factor_off = o; o += kFactors * N * 4;
     p.stat_off = o;   o += 5 * N * 4 + 16;     // four warps' values and one for all; the warps' largest scales
-    p.mask_off = o;   o += p.stages * 8;
-    p.bar_off = o;    o += (2 * p.stages + 21) * 8;
+    p.mask_off = o;   o += p.tiles * 8;
+    p.bar_off = o;    o += (p.tiles + p.slots + 19) * 8;
     p.total = o;
     return p;
 }
@@ -79,10 +97,9 @@ static_assert(qplan_of(64).ring_off % 1024 == 0 && qplan_of(32).ring_off % 1024 
               "the swizzle's period");
 
 struct QParams : RowParams {
-    const uint16_t* ql;
-    const uint16_t* qp;
-    int64_t ql_row, ql_head, qp_row, qp_head;
     int64_t block_bytes;
+    int ql_swap, qp_swap;      // the map's middle dimension is the row
+    float room;        // where a reference is held
 };
 
 // MN-major operand of 64-byte rows with the 64-byte swizzle: rows are the K
@@ -123,6 +140,35 @@ __device__ __forceinline__ void tmem_wait_halves(uint32_t (&r)[8]) {
                  : "memory");
 }
 
+// One column of this thread's lane.
+__device__ __forceinline__ void tmem_ld1_nowait(uint32_t taddr, uint32_t& r) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr) : "memory");
+}
+__device__ __forceinline__ void tmem_st1(uint32_t taddr, uint32_t r) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(r) : "memory");
+}
+template <int n>
+__device__ __forceinline__ void tmem_wait_all(uint32_t (&r)[n]) {
+#pragma unroll
+    for (int i = 0; i < n; ++i) asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(r[i])::"memory");
+}
+
+// kParts groups of 16 columns, kPitch apart, and their sum.
+template <int kParts, int kPitch>
+__device__ __forceinline__ void load_parts(uint32_t taddr, uint32_t (&v)[kParts][16]) {
+#pragma unroll
+    for (int k = 0; k < kParts; ++k) tmem_ld16_nowait(taddr + k * kPitch, v[k]);
+}
+template <int kParts>
+__device__ __forceinline__ void sum_parts(uint32_t (&v)[kParts][16], float (&o)[16]) {
+#pragma unroll
+    for (int k = 0; k < kParts; ++k) {
+        tmem_wait_ld16(v[k]);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) o[j] = k ? o[j] + __uint_as_float(v[k][j]) : __uint_as_float(v[k][j]);
+    }
+}
+
 __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -149,10 +195,21 @@ __device__ __forceinline__ uint32_t from_e4m3x2(uint32_t v) {
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(v)));
     return h;
 }
-// Two fp16 rounded to the three significant bits of e5m2, whose codes are the
-// upper bytes: the magnitudes' low bytes are rounded to nearest.
-__device__ __forceinline__ uint32_t to_e5m2(uint32_t h) { return h + 0x00800080u; }
+// The upper byte of an fp16 is the e5m2 of its three leading bits.
 constexpr uint32_t kUpper = 0xFF00FF00u;
+
+// Two fp32 products and sums at once.
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 f2_mul(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 f2_add(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 
 __device__ __forceinline__ void copy4_or_zero(uint32_t dst, const void* src, uint32_t bytes) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -176,61 +233,152 @@ __device__ __forceinline__ float over_keys(float (&v)[kH], Op op) {
     return v[0];
 }
 
-// Splits one head's query: 16 latent elements a lane (u, v) and a pair of
-// position elements (p), for row h of the hi rows and row N + h of the lo rows.
-// Returns the factor of its scores.
+// Splits the queries of heads [first, first + n) where they are.  Their latent
+// parts were copied as they are (bf16), 64 values of every head into each
+// eighth of the operand's rows, so that a head's raw bytes are just those that
+// its hi and lo rows take: a warp reads a head and writes it back split, 16
+// values a lane.  (Read by plain loads instead, two heads ahead, a head took
+// 500 to 1200 cycles: trips to L2.)
 template <int N>
-__device__ __forceinline__ float split_query(uint8_t* q, int h, const uint4& u, const uint4& v, uint32_t p, float scale_log2) {
+__device__ __forceinline__ void split_heads(uint8_t* q, int first, int n, float scale_log2, float* factor) {
     const int lane = lane_id();
-    const uint32_t w[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
-    uint32_t top = 0;
+#pragma unroll 2
+    for (int h = first; h < first + n; ++h) {
+        // raw: pieces 2 (lane % 4) and the next of 64 values; split: piece lane % 8 of 128
+        uint8_t* raw = q + (lane >> 2) * (N * 128) + h * 128;
+        uint8_t* row = q + (lane >> 3) * (2 * N * 128) + h * 128 + (((lane & 7) ^ (h & 7)) << 4);
+        uint8_t* pe = q + 4 * (2 * N * 128) + h * 128 + (((lane >> 2) ^ (h & 7)) << 4) + 4 * (lane & 3);
+        const uint4 u = *reinterpret_cast<const uint4*>(raw + (((2 * (lane & 3)) ^ (h & 7)) << 4));
+        const uint4 v = *reinterpret_cast<const uint4*>(raw + (((2 * (lane & 3) + 1) ^ (h & 7)) << 4));
+        const uint32_t p = *reinterpret_cast<const uint32_t*>(pe);
+        const uint32_t w[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+        uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = __vmaxu2(top, w[i] & 0x7FFF7FFFu);
-    top = __reduce_max_sync(~0u, max(top & 0xFFFFu, top >> 16));
-    // 2^-a brings the largest to [128, 256); a >= -60, so that the position
-    // part stays finite
-    const uint32_t e = max(top >> 7, 74u);
-    const float down = __uint_as_float((261u - e) << 23);
-    uint32_t hi[4], lo[4];
+        for (int i = 0; i < 8; ++i) top = __vmaxu2(top, w[i] & 0x7FFF7FFFu);
+        top = __reduce_max_sync(~0u, max(top & 0xFFFFu, top >> 16));      // (also: every lane has read)
+        // 2^-a brings the largest to [128, 256); a >= -60, so that the position
+        // part stays finite
+        const uint32_t e = max(top >> 7, 74u);
+        const float down = __uint_as_float((261u - e) << 23);
+        uint32_t hi[4], lo[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        uint32_t a[2], b[2];
+        for (int i = 0; i < 4; ++i) {
+            uint32_t a[2], b[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const uint32_t x = w[2 * i + k];
+                const uint32_t f = f16x2(__uint_as_float(x << 16) * down, __uint_as_float(x & 0xFFFF0000u) * down);
+                a[k] = e4m3x2(f);
+                b[k] = e4m3x2(mul_f16x2(sub_f16x2(f, from_e4m3x2(a[k])), 0x4C004C00u));      // 16
+            }
+            hi[i] = a[0] | a[1] << 16;
+            lo[i] = b[0] | b[1] << 16;
+        }
+        *reinterpret_cast<uint4*>(row) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(row + N * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        // half of the position part in the hi rows, the other half (times 16) in the lo rows
+        const float p0 = __uint_as_float(p << 16) * (0.5f * down), p1 = __uint_as_float(p & 0xFFFF0000u) * (0.5f * down);
+        *reinterpret_cast<uint32_t*>(pe) = bf16x2(p0, p1);
+        *reinterpret_cast<uint32_t*>(pe + N * 128) = bf16x2(16.0f * p0, 16.0f * p1);
+        if (lane == 0)
+            factor[h] = top >= 0x7F80u ? __uint_as_float(0x7FFFFFFFu) : scale_log2 * __uint_as_float((e - 7u) << 23);
+    }
+}
+
+// What a wait does that is not over at once, and a step to the next piece of
+// work: one copy each, out of the loops' code (see the note on its size).
+__device__ __noinline__ bool wait_longer(uint64_t* bar, uint32_t parity, int32_t* status, volatile int* abort_flag) {
+    return mbar_wait(bar, parity, status, abort_flag);
+}
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int32_t* status, volatile int* abort_flag) {
+    return mbar_try_wait(bar, parity) || wait_longer(bar, parity, status, abort_flag);
+}
+__device__ __noinline__ bool next_piece(const QParams* p, Walk* walk, Work* w) { return walk->next(*p, *w); }
+struct Pieces {
+    const QParams* p;
+    Walk walk;
+    __device__ __forceinline__ bool next(Work& w) {
+        Work got;
+        const bool more = next_piece(p, &walk, &got);
+        w = got;
+        return more;
+    }
+};
+
+// When a row's queries may be written.
+struct QueryTurn {
+    uint32_t item = 0;      // rows so far
+    uint32_t it = 0;        // tiles of the rows before
+    int before = 0;         // tiles of the row before
+    // Whole warps.  The scores of the row before are done; and the factors of the
+    // row before it, which make room for this row's, are not needed any more: as
+    // the softmax is at most two tiles behind the scores, that leaves it open
+    // only where the row before has one or two tiles.  Then the weights of the
+    // last tile but one have to be there.  (Their barrier goes on no further: its
+    // next phase is this row's first tile.)
+    __device__ __forceinline__ bool wait(uint64_t* q_empty, uint64_t* p_full, int32_t* status, volatile int* abort_flag) {
+        bool ok = dsaidx::wait(q_empty, (item & 1) ^ 1, status, abort_flag);
+        if (before <= 2 && it > 1) ok = dsaidx::wait(p_full + (it & 1), ((it - 2) >> 1) & 1, status, abort_flag) && ok;
+        return __all_sync(~0u, ok);
+    }
+    __device__ __forceinline__ void next(const Work& w) {
+        before = w.t1 - w.t0;
+        it += before;
+        ++item;
+    }
+};
+
+// Weights e = 2^(dot f scale - m) of one key's heads, and their products with
+// `by` as the sum of three e5m2 each: the three leading bits, the next three
+// significant ones and the rest rounded, 2^-9 of the product off at most.
+// True where a product is too large (or not a number).
+template <int kH>
+__device__ __forceinline__ bool weigh(const f2 (&dot)[kH / 2], const float* factor, float scale, const f2 (&minus_m)[kH / 2], float by,
+                                      f2 (&e)[kH / 2], uint32_t (&part)[3][kH / 4]) {
+    const f2 scale2 = f2_pack(scale, scale), by2 = f2_pack(by, by);
+    uint32_t most = 0;
+#pragma unroll
+    for (int i = 0; i < kH / 4; ++i) {
+        const float4 f = reinterpret_cast<const float4*>(factor)[i];
+        uint32_t r[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            const uint32_t x = w[2 * i + k];
-            const uint32_t f = f16x2(__uint_as_float(x << 16) * down, __uint_as_float(x & 0xFFFF0000u) * down);
-            a[k] = e4m3x2(f);
-            b[k] = e4m3x2(mul_f16x2(sub_f16x2(f, from_e4m3x2(a[k])), 0x4C004C00u));      // 16
+            const float2 y = f2_unpack(f2_fma(dot[2 * i + k], f2_mul(k ? f2_pack(f.z, f.w) : f2_pack(f.x, f.y), scale2), minus_m[2 * i + k]));
+            e[2 * i + k] = f2_pack(exp2_fast(y.x), exp2_fast(y.y));
+            const float2 w = f2_unpack(f2_mul(e[2 * i + k], by2));
+            r[k] = f16x2(w.x, w.y);
+            most = __vmaxu2(most, r[k]);
         }
-        hi[i] = a[0] | a[1] << 16;
-        lo[i] = b[0] | b[1] << 16;
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            const uint32_t a = k == 2 ? r[0] + 0x00800080u : r[0], b = k == 2 ? r[1] + 0x00800080u : r[1];
+            part[k][i] = __byte_perm(a, b, 0x7531);
+            if (k == 2) break;
+            r[0] = sub_f16x2(r[0], a & kUpper);
+            r[1] = sub_f16x2(r[1], b & kUpper);
+        }
     }
-    // lane's 16 bytes: piece lane % 8 of chunk lane / 8
-    uint8_t* row = q + (lane >> 3) * (2 * N * 128) + h * 128 + (((lane & 7) ^ (h & 7)) << 4);
-    *reinterpret_cast<uint4*>(row) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-    *reinterpret_cast<uint4*>(row + N * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-    // half of the position part in the hi rows, the other half (times 16) in the lo rows
-    const float p0 = __uint_as_float(p << 16) * (0.5f * down), p1 = __uint_as_float(p & 0xFFFF0000u) * (0.5f * down);
-    uint8_t* pe = q + 4 * (2 * N * 128) + h * 128 + (((lane >> 2) ^ (h & 7)) << 4) + 4 * (lane & 3);
-    *reinterpret_cast<uint32_t*>(pe) = bf16x2(p0, p1);
-    *reinterpret_cast<uint32_t*>(pe + N * 128) = bf16x2(16.0f * p0, 16.0f * p1);
-    return top >= 0x7F80u ? __uint_as_float(0x7FFFFFFFu) : scale_log2 * __uint_as_float((e - 7u) << 23);
+    return max(most & 0xFFFFu, most >> 16) > kMost16;
 }
 
 template <int N, int kCl>
-__global__ void __launch_bounds__(threads_of(N), 1) qattend_kernel(const QParams p) {
+__global__ void __launch_bounds__(threads_of(N), 1)
+    qattend_kernel(const __grid_constant__ CUtensorMap ql_map, const __grid_constant__ CUtensorMap qp_map,
+                   const __grid_constant__ QParams p) {
     constexpr QPlan kPlan = qplan_of(N);
-    constexpr int kStages = kPlan.stages;
+    constexpr int kSlots = kPlan.slots, kTiles = kPlan.tiles;
     constexpr int kHalves = halves_of(N), kSoftThreads = 128 * kHalves, kGroupsM = 4 / kHalves;
     constexpr bool kWide = N == 64;            // the weights' parts share the accumulators
     constexpr int kOCols = kWide ? N : 3 * N;  // accumulator columns of 128 dimensions
     constexpr int kSCol = 4 * kOCols;          // first column behind the accumulators
     constexpr int kH = N / kHalves / 2;        // heads a softmax thread
+    // heads a warp splits: of the four that gather, of the two that do nothing else
+    constexpr int kSplit = N == 64 ? 14 : N / 8, kSplitAux = (N - 4 * kSplit) / 2;
     extern __shared__ __align__(1024) uint8_t smem[];
     uint64_t* bar = reinterpret_cast<uint64_t*>(smem + kPlan.bar_off);
-    uint64_t* full = bar;                        // [stages]
-    uint64_t* empty = full + kStages;            // [stages]
-    uint64_t* s_full = empty + kStages;          // [2]
+    uint64_t* full = bar;                        // [tiles]
+    uint64_t* empty = full + kTiles;             // [slots]
+    uint64_t* s_full = empty + kSlots;           // [2]
     uint64_t* s_empty = s_full + 2;              // [2]
     uint64_t* p_full = s_full + 4;               // [2]
     uint64_t* pv_done = s_full + 6;              // [2]
@@ -238,20 +386,19 @@ __global__ void __launch_bounds__(threads_of(N), 1) qattend_kernel(const QParams
     uint64_t* q_empty = s_full + 9;
     uint64_t* o_empty = s_full + 10;
     uint64_t* drain = s_full + 11;               // [2]
-    int64_t* sh_run = reinterpret_cast<int64_t*>(s_full + 13);   // start, end, row, base
-    uint32_t* sh_tmem = reinterpret_cast<uint32_t*>(s_full + 17);
+    uint64_t* q_raw = s_full + 13;
+    int64_t* sh_run = reinterpret_cast<int64_t*>(s_full + 14);   // start, end, row, base
+    uint32_t* sh_tmem = reinterpret_cast<uint32_t*>(s_full + 18);
     int* sh_abort = reinterpret_cast<int*>(sh_tmem + 1);
-    uint16_t* masks = reinterpret_cast<uint16_t*>(smem + kPlan.mask_off);   // [stages][4]: 16 keys each
-    float* scales = reinterpret_cast<float*>(smem + kPlan.scale_off);       // [stages][64]
+    uint16_t* masks = reinterpret_cast<uint16_t*>(smem + kPlan.mask_off);   // [tiles][4]: 16 keys each
+    float* scales = reinterpret_cast<float*>(smem + kPlan.scale_off);       // [tiles][64]
     float* factors = reinterpret_cast<float*>(smem + kPlan.factor_off);     // [kFactors][N]
     float* stat = reinterpret_cast<float*>(smem + kPlan.stat_off);          // [5][N], [4]
     const int warp = warp_id(), lane = lane_id();
 
     if (warp == 0 && elect_one()) {
-        for (int i = 0; i < kStages; ++i) {
-            mbar_init(full + i, kGatherThreads + kGatherThreads / 32);
-            mbar_init(empty + i, 1);
-        }
+        for (int i = 0; i < kTiles; ++i) mbar_init(full + i, kGatherThreads + kGatherThreads / 32);
+        for (int i = 0; i < kSlots; ++i) mbar_init(empty + i, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(s_full + i, 1);
             mbar_init(s_empty + i, kSoftThreads);
@@ -259,8 +406,9 @@ __global__ void __launch_bounds__(threads_of(N), 1) qattend_kernel(const QParams
             mbar_init(pv_done + i, 1);
             mbar_init(drain + i, 1);
         }
-        mbar_init(q_full, kGatherThreads);
+        mbar_init(q_full, kGatherThreads + 64);
         mbar_init(q_empty, 1);
+        mbar_init(q_raw, 1);
         mbar_init(o_empty, kSoftThreads);
         *sh_abort = 0;
         fence_mbar_init();
@@ -268,6 +416,10 @@ __global__ void __launch_bounds__(threads_of(N), 1) qattend_kernel(const QParams
     if (warp == 1) {
         tmem_alloc(sh_tmem, 512);
         tmem_relinquish();
+    }
+    if (warp == 2 && elect_one()) {
+        tma_prefetch_desc(&ql_map);
+        tma_prefetch_desc(&qp_map);
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -307,7 +459,7 @@ __global__ void __launch_bounds__(threads_of(N), 1) qattend_kernel(const QParams
     tc_fence_after();
     const uint32_t tmem = *sh_tmem;
     volatile int* abort_flag = sh_abort;
-    Walk walk(p, sh_run[0], sh_run[1], sh_run[2], sh_run[3]);
+    Pieces walk{&p, Walk(p, sh_run[0], sh_run[1], sh_run[2], sh_run[3])};
     Work w;
 
     if (warp >= 8 && warp < 12) {
@@ -319,105 +471,139 @@ __global__ void __launch_bounds__(threads_of(N), 1) qattend_kernel(const QParams
         const uint32_t ring = smem_u32(smem + kPlan.ring_off), sc_addr = smem_u32(scales);
         const int none = static_cast<int>(p.num_slots), j = 16 * wq + (lane & 15);
         const uint32_t block_units = static_cast<uint32_t>(p.block_bytes / 128);
-        uint32_t it = 0, item = 0, st = 0, ph = 1;    // tiles, rows, stage and the parity that frees it
+        uint32_t tb = 0;                              // the tile's buffer of scales and masks
+        uint32_t sl = 0, ph = 1;                      // ring slot and the parity that frees it
+        QueryTurn turn;
         bool ok = true;
-        while (ok && walk.next(p, w)) {
+        while (ok && walk.next(w)) {
             if (p.block_table != nullptr && w.keys == 0 && lane == 0 && __ldg(p.seq_lens + w.row) != 0)
                 set_status(p.status, IDX_ERR_DEVICE_CHECK);
-            int64_t entry = key_entry(p, w.row, w.keys, w.t0 * kKeys + j);
-            // the queries are split behind the copies of the second tile
+            // Keys are looked up for two tiles at once, lanes 0-15 for the first.
+            // What names them is read two and four tiles ahead: a trip to memory
+            // takes longer than a tile, and a register that a load has yet to
+            // fill cannot be moved either.
+            const int two = lane >> 4;
+            auto entry_of = [&](int t) { return t < w.t1 ? key_entry(p, w.row, w.keys, t * kKeys + j) : int64_t(-1); };
+            int64_t entry = entry_of(w.t0 + two), next = entry_of(w.t0 + 2 + two);
+            // the queries are written behind the copies of the second tile
             const int split_at = min(w.t0 + 1, w.t1 - 1);
-            for (int t = w.t0; t < w.t1; ++t, ++it) {
-                const int slot = key_slot(p, w.keys, t * kKeys + j, entry);
-                const uint32_t valid = __ballot_sync(~0u, slot != none) & 0xFFFFu;
+            for (int t0 = w.t0; ok && t0 < w.t1; t0 += 2) {
+                const int slot = t0 + two < w.t1 ? key_slot(p, w.keys, (t0 + two) * kKeys + j, entry) : none;
+                entry = next;
+                next = entry_of(t0 + 4 + two);
+                const uint32_t both = __ballot_sync(~0u, slot != none);
                 // a record begins a multiple of 128 bytes into the pool
                 const uint32_t own = slot == none ? 0u : static_cast<uint32_t>(slot);
                 const uint32_t block = own / static_cast<uint32_t>(p.block_size), at = own - block * p.block_size;
                 const uint32_t unit = block * block_units + at * (kQRow / 128);
                 const uint8_t* sc = p.pool + block * p.block_bytes + static_cast<int64_t>(p.block_size) * kQRow + 4 * at;
-                const uint8_t* src[4];
+#pragma unroll 1
+                for (int i = 0; i < 2 && t0 + i < w.t1; ++i) {
+                    const uint32_t valid = (both >> (16 * i)) & 0xFFFFu;
+                    const uint8_t* src[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    src[k] = p.pool + static_cast<int64_t>(__shfl_sync(~0u, unit, 4 * k + sub)) * 128 + 16 * piece;
-                if (t + 1 < w.t1) entry = key_entry(p, w.row, w.keys, (t + 1) * kKeys + j);
-                ok = mbar_wait(empty + st, ph, p.status, abort_flag);
-                if (!(ok = __all_sync(~0u, ok))) break;
-                const uint32_t dst = ring + st * kStage;
+                    for (int k = 0; k < 4; ++k)
+                        src[k] = p.pool + static_cast<int64_t>(__shfl_sync(~0u, unit, 16 * i + 4 * k + sub)) * 128 + 16 * piece;
+                    // the tile's slots, a lane each
+                    const bool wraps = sl + lane >= kSlots;
+                    ok = lane >= kTileChunks || wait(empty + (wraps ? sl + lane - kSlots : sl + lane), ph ^ wraps, p.status, abort_flag);
+                    if (!(ok = __all_sync(~0u, ok))) break;
+                    // the position parts first: they are freed first
+                    int c = 4 * 128;
+#pragma unroll 1
+                    for (int m = 0; m < kTileChunks; ++m) {
+                        const uint32_t dst = ring + sl * kChunk;
+                        if (valid == 0xFFFFu) {
 #pragma unroll
-                for (int c = 0; c < 5; ++c) {
-                    if (valid == 0xFFFFu) {
+                            for (int k = 0; k < 4; ++k) copy16(dst + ((k & 1) ? odd : even) + 512 * k, src[k] + c);
+                        } else {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) copy16(dst + c * kChunk + ((k & 1) ? odd : even) + 512 * k, src[k] + 128 * c);
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            copy16_or_zero(dst + c * kChunk + ((k & 1) ? odd : even) + 512 * k, src[k] + 128 * c,
-                                           (valid >> (4 * k + sub)) & 1 ? 16 : 0);
+                            for (int k = 0; k < 4; ++k)
+                                copy16_or_zero(dst + ((k & 1) ? odd : even) + 512 * k, src[k] + c, (valid >> (4 * k + sub)) & 1 ? 16 : 0);
+                        }
+                        c = m * 128;
+                        if (++sl == kSlots) sl = 0, ph ^= 1;
+                    }
+                    if (two == i) copy4_or_zero(sc_addr + (tb * kKeys + j) * 4, sc, slot == none ? 0 : 4);
+                    if (lane == 0) masks[4 * tb + wq] = static_cast<uint16_t>(valid);
+                    copy_arrive(full + tb);
+                    if (lane == 0) mbar_arrive(full + tb);
+                    if (++tb == kTiles) tb = 0;
+                    if (t0 + i == split_at) {
+                        if (!(ok = turn.wait(q_empty, p_full, p.status, abort_flag))) break;
+                        if (!(ok = __all_sync(~0u, wait(q_raw, turn.item & 1, p.status, abort_flag)))) break;
+                        split_heads<N>(smem, wq * kSplit, kSplit, p.scale_log2, factors + turn.item % kFactors * N);
+                        fence_proxy_async_smem();
+                        mbar_arrive(q_full);
+                        turn.next(w);
                     }
                 }
-                if (lane < 16) copy4_or_zero(sc_addr + (st * kKeys + j) * 4, sc, slot == none ? 0 : 4);
-                if (lane == 0) masks[4 * st + wq] = static_cast<uint16_t>(valid);
-                copy_arrive(full + st);
-                if (lane == 0) mbar_arrive(full + st);
-                if (++st == kStages) st = 0, ph ^= 1;
-                if (t != split_at) continue;
-                ok = mbar_wait(q_empty, (item & 1) ^ 1, p.status, abort_flag);
-                if (!(ok = __all_sync(~0u, ok))) break;
-                float* factor = factors + item % kFactors * N;
-                const int h0 = w.hg * 64;
-#pragma unroll 2
-                for (int h = wq; h < N; h += 4) {
-                    uint4 u = make_uint4(0u, 0u, 0u, 0u), v = u;
-                    uint32_t x = 0u;
-                    if (h0 + h < p.heads) {
-                        const uint4* lat = reinterpret_cast<const uint4*>(p.ql + w.row * p.ql_row + (h0 + h) * p.ql_head);
-                        u = __ldg(lat + 2 * lane);
-                        v = __ldg(lat + 2 * lane + 1);
-                        x = __ldg(reinterpret_cast<const uint32_t*>(p.qp + w.row * p.qp_row + (h0 + h) * p.qp_head) + lane);
-                    }
-                    const float f = split_query<N>(smem, h, u, v, x, p.scale_log2);
-                    if (lane == 0) factor[h] = f;
-                }
-                fence_proxy_async_smem();
-                mbar_arrive(q_full);
-                ++item;
             }
         }
         copy_wait_all();
+    } else if (warp == 1 || warp == 3) {
+        // ---- queries: their copies, and the other heads ----
+        const int h0 = 4 * kSplit + (warp >> 1) * kSplitAux;
+        QueryTurn turn;
+        bool ok = true;
+        while (ok && walk.next(w)) {
+            if (!(ok = turn.wait(q_empty, p_full, p.status, abort_flag))) break;
+            if (warp == 1 && elect_one()) {
+                mbar_arrive_expect_tx(q_raw, 9 * N * 128);
+                const uint32_t q_addr = smem_u32(smem);
+                const int h = w.hg * 64, row = static_cast<int>(w.row);
+                for (int c = 0; c < 8; ++c)
+                    tma_tile_3d(q_addr + c * N * 128, &ql_map, q_raw, 64 * c, p.ql_swap ? row : h, p.ql_swap ? h : row);
+                tma_tile_3d(q_addr + 8 * N * 128, &qp_map, q_raw, 0, p.qp_swap ? row : h, p.qp_swap ? h : row);
+            }
+            __syncwarp();
+            if (!(ok = __all_sync(~0u, wait(q_raw, turn.item & 1, p.status, abort_flag)))) break;
+            split_heads<N>(smem, h0, kSplitAux, p.scale_log2, factors + turn.item % kFactors * N);
+            fence_proxy_async_smem();
+            mbar_arrive(q_full);
+            turn.next(w);
+        }
+        // no copy may be on its way when the shared memory goes
+        if (!ok && warp == 1) wait(q_raw, turn.item & 1, p.status, nullptr);
     } else if (warp == 0) {
         // ---- score products ----
         if (elect_one()) {
             constexpr uint32_t kIdS = idesc_make(true, 64, 2 * N), kIdP = idesc_bf16(64, 2 * N, false, false);
             const uint32_t q_addr = smem_u32(smem), ring = smem_u32(smem + kPlan.ring_off);
-            uint32_t it = 0, item = 0, st = 0, ph = 0;
+            uint32_t it = 0, item = 0, tb = 0, ph = 0, sl = 0;
             bool ok = true;
-            while (ok && walk.next(p, w)) {
-                if (!(ok = mbar_wait(q_full, item & 1, p.status, abort_flag))) break;
+            while (ok && walk.next(w)) {
+                if (!(ok = wait(q_full, item & 1, p.status, abort_flag))) break;
                 for (int t = w.t0; t < w.t1; ++t, ++it) {
-                    const uint32_t d = tmem + kSCol + (it & 1) * 2 * N, tile = ring + st * kStage;
+                    const uint32_t d = tmem + kSCol + (it & 1) * 2 * N;
                     // the softmax has read the scores before last
-                    if (!(ok = mbar_wait(s_empty + (it & 1), ((it >> 1) & 1) ^ 1, p.status, abort_flag))) break;
-                    if (!(ok = mbar_wait(full + st, ph, p.status, abort_flag))) break;
+                    if (!(ok = wait(s_empty + (it & 1), ((it >> 1) & 1) ^ 1, p.status, abort_flag))) break;
+                    if (!(ok = wait(full + tb, ph, p.status, abort_flag))) break;
                     // records and queries were written by other threads: order
                     // their writes before the tensor core's reads
                     fence_proxy_async_smem();
                     tc_fence_after();
 #pragma unroll
-                    for (int k = 0; k < 16; ++k)
-                        mma_fp8(d, sdesc_sw128(tile + (k >> 2) * kChunk + 32 * (k & 3)),
-                                sdesc_sw128(q_addr + (k >> 2) * 2 * N * 128 + 32 * (k & 3)), kIdS, k != 0);
-#pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        mma_bf16(d, sdesc_sw128(tile + 4 * kChunk + 32 * k), sdesc_sw128(q_addr + 8 * N * 128 + 32 * k), kIdP, 1u);
+                        mma_bf16(d, sdesc_sw128(ring + sl * kChunk + 32 * k), sdesc_sw128(q_addr + 8 * N * 128 + 32 * k), kIdP, k != 0);
+                    mma_commit(empty + sl);
+                    if (++sl == kSlots) sl = 0;
+#pragma unroll 1
+                    for (int m = 0; m < 4; ++m) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            mma_fp8(d, sdesc_sw128(ring + sl * kChunk + 32 * k), sdesc_sw128(q_addr + m * 2 * N * 128 + 32 * k), kIdS, 1u);
+                        if (++sl == kSlots) sl = 0;
+                    }
                     mma_commit(s_full + (it & 1));
                     if (t + 1 == w.t1) mma_commit(q_empty);
-                    if (++st == kStages) st = 0, ph ^= 1;
+                    if (++tb == kTiles) tb = 0, ph ^= 1;
                 }
                 ++item;
             }
             // nothing of this CTA may run on when its shared memory and TMEM go
             mma_commit(drain);
-            mbar_wait(drain, 0, p.status, nullptr);
+            wait(drain, 0, p.status, nullptr);
         }
     } else if (warp == 2) {
         // ---- value products ----
@@ -425,22 +611,23 @@ __global__ void __launch_bounds__(threads_of(N), 1) qattend_kernel(const QParams
             // e4m3 x e5m2, both operands MN-major
             constexpr uint32_t kIdO = idesc_make(true, 128, kOCols) | 1u << 10 | 1u << 15 | 1u << 16;
             const uint32_t ring = smem_u32(smem + kPlan.ring_off), p_addr = smem_u32(smem + kPlan.p_off);
-            uint32_t it = 0, item = 0, st = 0;
+            uint32_t it = 0, item = 0, sl = 0;
             bool ok = true;
-            while (ok && walk.next(p, w)) {
+            while (ok && walk.next(w)) {
                 for (int t = w.t0; t < w.t1; ++t, ++it) {
                     // the weights are there, which the records were before them
-                    if (!(ok = mbar_wait(p_full + (it & 1), (it >> 1) & 1, p.status, abort_flag))) break;
+                    if (!(ok = wait(p_full + (it & 1), (it >> 1) & 1, p.status, abort_flag))) break;
                     // the accumulators of the piece before were read
-                    if (t == w.t0 && !(ok = mbar_wait(o_empty, (item & 1) ^ 1, p.status, abort_flag))) break;
+                    if (t == w.t0 && !(ok = wait(o_empty, (item & 1) ^ 1, p.status, abort_flag))) break;
                     fence_proxy_async_smem();
                     tc_fence_after();
-                    const uint32_t tile = ring + st * kStage, weights = p_addr + (it & 1) * kPlan.p_bytes;
-#pragma unroll
-                    for (int m = 0; m < 4; ++m)
+                    const uint32_t weights = p_addr + (it & 1) * kPlan.p_bytes;
+                    if (++sl == kSlots) sl = 0;
+#pragma unroll 1
+                    for (int m = 0; m < 4; ++m) {
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
-                            const uint64_t a = sdesc_mn_sw128(tile + m * kChunk + 4096 * k, kChunk);
+                            const uint64_t a = sdesc_mn_sw128(ring + sl * kChunk + 4096 * k, kChunk);
                             const uint32_t more = (t != w.t0 || k != 0) ? 1u : 0u;
                             if (kWide) {
 #pragma unroll
@@ -452,14 +639,15 @@ __global__ void __launch_bounds__(threads_of(N), 1) qattend_kernel(const QParams
                                         kIdO, more);
                             }
                         }
-                    mma_commit(empty + st);
+                        mma_commit(empty + sl);
+                        if (++sl == kSlots) sl = 0;
+                    }
                     mma_commit(pv_done + (it & 1));
-                    if (++st == kStages) st = 0;
                 }
                 ++item;
             }
             mma_commit(drain + 1);
-            mbar_wait(drain + 1, 0, p.status, nullptr);
+            wait(drain + 1, 0, p.status, nullptr);
         }
     } else if (warp >= 4) {
         // ---- softmax and epilogue ----
@@ -468,111 +656,169 @@ __global__ void __launch_bounds__(threads_of(N), 1) qattend_kernel(const QParams
         const uint32_t lanes = static_cast<uint32_t>(32 * sw) << 16;
         const int key = 16 * sw + (lane & 15);
         const int hw = half * (N / kHalves), hb = hw + (lane >> 4) * kH;     // this warp's and this thread's first head
-        uint32_t it = 0, item = 0, st = 0, ph = 0;
+        uint32_t it = 0, item = 0, tb = 0, ph = 0;
         bool ok = true;
-        while (ok && walk.next(p, w)) {
-            // maximum and this thread's share of the sum of head hb + i; the
-            // largest scale so far, as a power of two, and what brings it to kTop
-            float mx[kH], sum[kH], top = 0x1p-100f, up = kTop * 0x1p100f;
+        while (ok && walk.next(w)) {
+            // reference and this thread's share of the sum of head hb + i; the
+            // unit of the scales (a power of two) and what brings it to p.room
+            f2 minus_m[kH / 2], sum[kH / 2];
+            float top = kNoScale, up = p.room / kNoScale;
 #pragma unroll
-            for (int i = 0; i < kH; ++i) {
-                mx[i] = kNone;
-                sum[i] = 0.0f;
+            for (int i = 0; i < kH / 2; ++i) {
+                minus_m[i] = f2_pack(-kNone, -kNone);
+                sum[i] = 0;
             }
             const float* factor = factors + item % kFactors * N + hb;
             for (int t = w.t0; t < w.t1; ++t, ++it) {
-                ok = ok && mbar_wait(s_full + (it & 1), (it >> 1) & 1, p.status, abort_flag);
+                ok = ok && wait(s_full + (it & 1), (it >> 1) & 1, p.status, abort_flag);
                 tc_fence_after();
                 uint32_t raw[kH], low[kH];
                 tmem_ld_halves(tmem + lanes + kSCol + (it & 1) * 2 * N + hw, raw);
                 tmem_ld_halves(tmem + lanes + kSCol + (it & 1) * 2 * N + N + hw, low);
                 // (long complete; it is what makes the copied scales visible here)
-                ok = ok && mbar_wait(full + st, ph, p.status, abort_flag);
-                const bool valid = (masks[4 * st + sw] >> (lane & 15)) & 1;
-                const float scale = scales[st * kKeys + key];
-                // x: log2 of the weight, before the maximum goes off
-                float x[kH];
-#pragma unroll
-                for (int i = 0; i < kH; i += 4) *reinterpret_cast<float4*>(x + i) = *reinterpret_cast<const float4*>(factor + i);
+                ok = ok && wait(full + tb, ph, p.status, abort_flag);
+                const bool valid = (masks[4 * tb + sw] >> (lane & 15)) & 1;
+                const float scale = scales[tb * kKeys + key];
+                f2 dot[kH / 2];
                 tmem_wait_halves(raw);
                 tmem_wait_halves(low);
                 tc_fence_before();
                 mbar_arrive(s_empty + (it & 1));
-                bool grow = !ok || (valid && scale > top);
 #pragma unroll
-                for (int i = 0; i < kH; ++i) {
-                    x[i] = valid ? fmaf(__uint_as_float(low[i]), 0.0625f, __uint_as_float(raw[i])) * scale * x[i] : -INFINITY;
-                    grow |= x[i] - mx[i] > kGrow;
-                }
-                if (named_any<1, kSoftThreads>(grow)) {
-                    // a wait that ran out in any thread ends the loop in all
-                    if (named_any<1, kSoftThreads>(!ok)) { ok = false; break; }
-                    // new maxima: over this warp's 16 keys, then over the four warps
-                    float v[kH];
+                for (int i = 0; i < kH / 2; ++i)
+                    dot[i] = f2_fma(f2_pack(__uint_as_float(low[2 * i]), __uint_as_float(low[2 * i + 1])), f2_pack(0.0625f, 0.0625f),
+                                  f2_pack(__uint_as_float(raw[2 * i]), __uint_as_float(raw[2 * i + 1])));
+                // Weights, and times the scale as three e5m2; the vote is on their
+                // size.  Where it moves references they are formed once more (by
+                // the same code: a copy of its own, rarely run, would come from
+                // memory each time).
+                uint32_t part[3][kH / 4];
+                f2 e[kH / 2];
+                bool again = false;
+                uint32_t which[2];          // heads whose reference moved, and by what: lane and lane + 32
+                float factor_of[2];
+#pragma unroll 1
+                for (;; again = true) {
+                    const float by = valid ? scale * up : 0.0f;
+                    if (again || t != w.t0) {       // (a row's first tile sets them)
+                        bool grow = weigh<kH>(dot, factor, scale, minus_m, by, e, part);
+                        grow |= by > kMost * kMostScale && top < kTopUnit;
+                        if (valid && scale < kLeast) {
+                            // such a key's weight has no product to judge it by
 #pragma unroll
-                    for (int i = 0; i < kH; ++i) v[i] = x[i];
-                    const float most = over_keys(v, [](float a, float b) { return fmaxf(a, b); });
-                    if ((lane & 15) < kH) stat[sw * N + hb + (lane & 15)] = most;
+                            for (int i = 0; i < kH / 2; ++i) grow |= fmaxf(f2_unpack(e[i]).x, f2_unpack(e[i]).y) > kMostWeight;
+                        }
+                        if (!valid) {
+                            grow = false;
+#pragma unroll
+                            for (int i = 0; i < kH / 2; ++i) e[i] = 0;
+#pragma unroll
+                            for (int i = 0; i < kH / 4; ++i) part[0][i] = part[1][i] = part[2][i] = 0u;
+                        }
+                        if (again || !named_any<1, kSoftThreads>(grow || !ok)) break;
+                    }
+                    // largest weights times scales, as log2, over this warp's 16
+                    // keys, then over the four warps
                     float s = valid ? scale : 0.0f;
                     for (int d = 8; d > 0; d >>= 1) s = fmaxf(s, __shfl_xor_sync(~0u, s, d));
                     if (half == 0 && lane == 0) stat[5 * N + sw] = s;
-                    named_sync<1, kSoftThreads>();
-                    s = fmaxf(fmaxf(stat[5 * N], stat[5 * N + 1]), fmaxf(stat[5 * N + 2], stat[5 * N + 3]));
-                    // the power of two at or above it
-                    s = __uint_as_float((__float_as_uint(fmaxf(s, top)) + 0x7FFFFFu) & 0x7F800000u);
-                    const float fall = __fdividef(top, s);
-                    top = s;
-                    up = __fdividef(kTop, s);
+                    // (the unit's log2 is taken off below; scales below 2^-32, which
+                    // the format does not have, count as that)
+                    const float shift = __log2f(fmaxf(scale, kLeast));
+                    float v[kH];
 #pragma unroll
                     for (int i = 0; i < kH; ++i) {
-                        const int h = hb + i;
-                        const float m = fmaxf(fmaxf(fmaxf(stat[h], stat[N + h]), fmaxf(stat[2 * N + h], stat[3 * N + h])), mx[i]);
-                        const float f = exp2_fast(mx[i] - m);
-                        mx[i] = m;
-                        sum[i] *= f;
-                        if (sw == 0 && (lane & 15) == 0) stat[4 * N + h] = f * fall;
+                        const float2 x = f2_unpack(dot[i / 2]);
+                        v[i] = valid ? fmaf(i & 1 ? x.y : x.x, scale * factor[i], shift) : -INFINITY;
                     }
-                    named_sync<1, kSoftThreads>();
-                    if (t != w.t0) {
-                        // the accumulators' columns (heads) times their factors,
-                        // half of the dimensions each
-                        ok = mbar_wait(pv_done + ((it - 1) & 1), ((it - 1) >> 1) & 1, p.status, abort_flag);
-                        tc_fence_after();
-                        for (int c = kGroupsM * kOCols * half; c < kGroupsM * kOCols * (half + 1); c += 16) {
-                            uint32_t v[16];
-                            tmem_ld16_nowait(tmem + lanes + c, v);
-                            tmem_wait_ld16(v);
+                    const float most = over_keys(v, [](float a, float b) { return fmaxf(a, b); });
+                    if ((lane & 15) < kH) stat[sw * N + hb + (lane & 15)] = most;
+                    if (sw == 0 && (lane & 15) == 0) {
 #pragma unroll
-                            for (int j = 0; j < 16; ++j)
-                                v[j] = __float_as_uint(__uint_as_float(v[j]) * stat[4 * N + ((c + j) & (N - 1))]);
-                            tmem_st16(tmem + lanes + c, v);
+                        for (int i = 0; i < kH; ++i)
+                            stat[4 * N + hb + i] = -(i & 1 ? f2_unpack(minus_m[i / 2]).y : f2_unpack(minus_m[i / 2]).x);
+                    }
+                    // a wait that ran out in any thread ends the loop in all
+                    if (named_any<1, kSoftThreads>(!ok)) { ok = false; break; }
+                    // a unit for the scales: the tile's largest, where none is set
+                    // or it lies far below.  References are relative to it: the
+                    // accumulators stay as they are, the sums follow.
+                    s = fmaxf(fmaxf(stat[5 * N], stat[5 * N + 1]), fmaxf(stat[5 * N + 2], stat[5 * N + 3]));
+                    float fall = 0.0f;
+                    if (s > top * kMostScale || (top == kNoScale && s > 0.0f)) {
+                        // the power of two at or above it
+                        s = fminf(__uint_as_float((__float_as_uint(s) + 0x7FFFFFu) & 0x7F800000u), kTopUnit);
+                        fall = __log2f(s) - __log2f(top);
+                        top = s;
+                        up = __fdividef(p.room, s);
+                    }
+                    // References before and behind, a lane two heads: the largest of
+                    // the four warps where that lies kNear above the old one.  (Each
+                    // thread for its own heads is shorter in steps and longer in
+                    // code, which comes from memory: it ran 3.2k cycles.)
+                    const float unit = __log2f(top), more = exp2_fast(fall);
+                    float ref[2];
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const int h = (lane + 32 * k) & (N - 1);
+                        const float m = fmaxf(fmaxf(stat[h], stat[N + h]), fmaxf(stat[2 * N + h], stat[3 * N + h])) - unit;
+                        const float old = stat[4 * N + h] - fall;
+                        ref[k] = m - old > kNear ? m : old;
+                        factor_of[k] = exp2_fast(old - ref[k]);
+                        which[k] = __ballot_sync(~0u, factor_of[k] != 1.0f && (N == 64 || (k == 0 && lane < N)));
+                    }
+                    // a half warp's heads begin at lane hb & 31 of one of the two
+                    const float of = half == 1 ? ref[1] : ref[0], f = (half == 1 ? factor_of[1] : factor_of[0]) * more;
+#pragma unroll
+                    for (int i = 0; i < kH / 2; ++i) {
+                        const int l = (hb & 31) + 2 * i;
+                        minus_m[i] = f2_pack(-__shfl_sync(~0u, of, l), -__shfl_sync(~0u, of, l + 1));
+                        sum[i] = f2_mul(sum[i], f2_pack(__shfl_sync(~0u, f, l), __shfl_sync(~0u, f, l + 1)));
+                    }
+                }
+                if (!ok) break;
+                if (again && t != w.t0) {
+                    // the moved heads' columns of the accumulators times their
+                    // factors, half of the dimensions each
+                    ok = wait(pv_done + ((it - 1) & 1), ((it - 1) >> 1) & 1, p.status, abort_flag);
+                    tc_fence_after();
+#pragma unroll 1
+                    while (which[0] | which[1]) {
+                        // kMove heads at once; where there are no more, the first
+                        // again and nothing stored
+                        constexpr int kCols = kGroupsM * (kOCols / N);     // a head's columns of this half
+                        constexpr int kMove = kWide ? 6 : 2;
+                        int h[kMove];
+                        float f[kMove];
+                        bool some[kMove];
+                        uint32_t v[kMove][kCols];
+#pragma unroll
+                        for (int k = 0; k < kMove; ++k) {
+                            const int b = which[0] ? 0 : 1;
+                            const uint32_t set = b ? which[1] : which[0];
+                            const int l = set ? __ffs(set) - 1 : 0;
+                            some[k] = set != 0u;
+                            h[k] = some[k] ? l + 32 * b : h[0];
+                            f[k] = __shfl_sync(~0u, b ? factor_of[1] : factor_of[0], l);
+                            if (b) which[1] &= which[1] - 1; else which[0] &= which[0] - 1;
+#pragma unroll
+                            for (int g = 0; g < kCols; ++g)
+                                tmem_ld1_nowait(tmem + lanes + kGroupsM * half * kOCols + g * N + h[k], v[k][g]);
                         }
-                        tmem_wait_st();
+#pragma unroll
+                        for (int k = 0; k < kMove; ++k) {
+                            tmem_wait_all(v[k]);
+#pragma unroll
+                            for (int g = 0; g < kCols; ++g)
+                                if (some[k]) tmem_st1(tmem + lanes + kGroupsM * half * kOCols + g * N + h[k], __float_as_uint(__uint_as_float(v[k][g]) * f[k]));
+                        }
                     }
+                    tmem_wait_st();
                 }
-                // weights, times the scale, as three e5m2
-                const float by = scale * up;
-                uint32_t part[3][kH / 4];
 #pragma unroll
-                for (int i = 0; i < kH; i += 4) {
-                    float e[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        e[k] = exp2_fast(x[i + k] - mx[i + k]);
-                        sum[i + k] += e[k];
-                        e[k] = valid ? e[k] * by : 0.0f;
-                    }
-                    uint32_t r[2] = {f16x2(e[0], e[1]), f16x2(e[2], e[3])};
-#pragma unroll
-                    for (int k = 0; k < 3; ++k) {
-                        const uint32_t a = to_e5m2(r[0]), b = to_e5m2(r[1]);
-                        part[k][i / 4] = __byte_perm(a, b, 0x7531);
-                        r[0] = sub_f16x2(r[0], a & kUpper);
-                        r[1] = sub_f16x2(r[1], b & kUpper);
-                    }
-                }
+                for (int i = 0; i < kH / 2; ++i) sum[i] = f2_add(sum[i], e[i]);
                 // the weight tile before last was read
-                if (it > 1) ok = mbar_wait(pv_done + (it & 1), ((it >> 1) & 1) ^ 1, p.status, abort_flag) && ok;
+                if (it > 1) ok = wait(pv_done + (it & 1), ((it >> 1) & 1) ^ 1, p.status, abort_flag) && ok;
                 uint8_t* pt = smem + kPlan.p_off + (it & 1) * kPlan.p_bytes;
 #pragma unroll
                 for (int k = 0; k < 3; ++k) {
@@ -591,23 +837,27 @@ __global__ void __launch_bounds__(threads_of(N), 1) qattend_kernel(const QParams
                 fence_proxy_async_smem();
                 tc_fence_before();
                 mbar_arrive(p_full + (it & 1));
-                if (++st == kStages) st = 0, ph ^= 1;
+                if (++tb == kTiles) tb = 0, ph ^= 1;
             }
             // A wait may have run out in some threads alone.  None of them leaves
             // before the vote below, whose barrier counts every thread.
             // sums over the warp's keys, then over the four warps
-            ok = ok && mbar_wait(pv_done + ((it - 1) & 1), ((it - 1) >> 1) & 1, p.status, abort_flag);
+            ok = ok && wait(pv_done + ((it - 1) & 1), ((it - 1) >> 1) & 1, p.status, abort_flag);
             tc_fence_after();
             {
-                const float all = over_keys(sum, [](float a, float b) { return a + b; });
+                float v[kH];
+#pragma unroll
+                for (int i = 0; i < kH; ++i) v[i] = i & 1 ? f2_unpack(sum[i / 2]).y : f2_unpack(sum[i / 2]).x;
+                const float all = over_keys(v, [](float a, float b) { return a + b; });
                 if ((lane & 15) < kH) stat[sw * N + hb + (lane & 15)] = all;
                 if (sw == 0 && (lane & 15) == 0) {
 #pragma unroll
-                    for (int i = 0; i < kH; ++i) stat[4 * N + hb + i] = mx[i];
+                    for (int i = 0; i < kH; ++i)
+                        stat[4 * N + hb + i] = -(i & 1 ? f2_unpack(minus_m[i / 2]).y : f2_unpack(minus_m[i / 2]).x);
                 }
             }
             if (named_any<1, kSoftThreads>(!ok)) { ok = false; break; }
-            const float unit = top * (1.0f / kTop);      // of the accumulators
+            const float unit = top == kNoScale ? 0.0f : __fdividef(top, p.room);      // of the accumulators
             if constexpr (kCl > 1) {
                 // this CTA's share to its own shared memory (everything in front of the
                 // statistics is consumed): statistics, then the accumulators [head][512]
@@ -620,14 +870,10 @@ __global__ void __launch_bounds__(threads_of(N), 1) qattend_kernel(const QParams
                 for (int hc = 0; hc < N; hc += 16) {
 #pragma unroll 1
                     for (int m = 0; m < kGroupsM; ++m) {
+                        uint32_t v[kOCols / N][16];
                         float o[16];
-#pragma unroll
-                        for (int k = 0; k < kOCols / N; ++k) {
-                            float v[16];
-                            tmem_ld16(tmem + lanes + (kGroupsM * half + m) * kOCols + k * N + hc, v);
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) o[j] = k ? o[j] + v[j] : v[j];
-                        }
+                        load_parts<kOCols / N, N>(tmem + lanes + (kGroupsM * half + m) * kOCols + hc, v);
+                        sum_parts<kOCols / N>(v, o);
 #pragma unroll
                         for (int j = 0; j < 16; ++j) share[(hc + j) * IDX_LATENT_DIM + 128 * m] = o[j] * unit;
                     }
@@ -647,41 +893,42 @@ __global__ void __launch_bounds__(threads_of(N), 1) qattend_kernel(const QParams
                 stat[4 * N + tid] = w.slot >= 0 ? unit : l == 0.0f ? 0.0f : __fdiv_rn(unit, l);
             }
             named_sync<1, kSoftThreads>();
-            // lane = latent dimension, column = head: 16 heads at a time
+            // lane = latent dimension, column = head: 16 heads of 128 dimensions at
+            // a time, the next ones' accumulators on their way
+            constexpr int kParts = kOCols / N, kSteps = kGroupsM * (N / 16);
+            auto column = [&](int i) { return tmem + lanes + (kGroupsM * half + i % kGroupsM) * kOCols + i / kGroupsM * 16; };
+            uint32_t v[kParts][16];
+            load_parts<kParts, N>(column(0), v);
 #pragma unroll 1
-            for (int hc = 0; hc < N; hc += 16) {
-                float f[16];
+            for (int i = 0; i < kSteps; ++i) {
+                const int hc = i / kGroupsM * 16, m = i % kGroupsM;
+                float o[16];
+                sum_parts<kParts>(v, o);
+                if (i + 1 < kSteps) load_parts<kParts, N>(column(i + 1), v);
 #pragma unroll
-                for (int j = 0; j < 16; j += 4)
-                    *reinterpret_cast<float4*>(f + j) = *reinterpret_cast<const float4*>(stat + 4 * N + hc + j);
-                const int d0 = 128 * kGroupsM * half + 32 * sw + lane;
+                for (int j = 0; j < 16; j += 4) {
+                    const float4 f = *reinterpret_cast<const float4*>(stat + 4 * N + hc + j);
+                    o[j] *= f.x;
+                    o[j + 1] *= f.y;
+                    o[j + 2] *= f.z;
+                    o[j + 3] *= f.w;
+                }
+                const int d = 128 * (kGroupsM * half + m) + 32 * sw + lane;
+                if (w.slot >= 0) {
+                    float* part = p.part_o + (static_cast<int64_t>(w.slot) * N + hc) * IDX_LATENT_DIM + d;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) part[j * IDX_LATENT_DIM] = o[j];
+                    continue;
+                }
                 // neighbouring lanes swap so that each stores two dimensions of one head
                 const bool odd = lane & 1;
                 const int left = p.heads - h0 - hc - odd;      // heads from this lane's first one on
-                __nv_bfloat16* dst = p.out + (w.row * p.heads + h0 + hc + odd) * IDX_LATENT_DIM + (d0 & ~1);
-                float* part = p.part_o + (static_cast<int64_t>(w.slot) * N + hc) * IDX_LATENT_DIM + d0;
-#pragma unroll 1
-                for (int m = 0; m < kGroupsM; ++m) {
-                    float o[16];
+                __nv_bfloat16* dst = p.out + (w.row * p.heads + h0 + hc + odd) * IDX_LATENT_DIM + (d & ~1);
 #pragma unroll
-                    for (int k = 0; k < kOCols / N; ++k) {
-                        float v[16];
-                        tmem_ld16(tmem + lanes + (kGroupsM * half + m) * kOCols + k * N + hc, v);
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) o[j] = k ? o[j] + v[j] : v[j];
-                    }
-                    if (w.slot >= 0) {
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) part[j * IDX_LATENT_DIM + 128 * m] = o[j] * f[j];
-                        continue;
-                    }
-#pragma unroll
-                    for (int j = 0; j < 16; j += 2) {
-                        const float a = o[j] * f[j], b = o[j + 1] * f[j + 1];
-                        const float c = __shfl_xor_sync(~0u, odd ? a : b, 1);
-                        const uint32_t two = odd ? bf16x2(c, b) : bf16x2(a, c);
-                        if (j < left) *reinterpret_cast<uint32_t*>(dst + j * IDX_LATENT_DIM + 128 * m) = two;
-                    }
+                for (int j = 0; j < 16; j += 2) {
+                    const float c = __shfl_xor_sync(~0u, odd ? o[j] : o[j + 1], 1);
+                    const uint32_t two = odd ? bf16x2(c, o[j + 1]) : bf16x2(o[j], c);
+                    if (j < left) *reinterpret_cast<uint32_t*>(dst + j * IDX_LATENT_DIM) = two;
                 }
             }
             tc_fence_before();
@@ -740,6 +987,16 @@ __global__ void __launch_bounds__(threads_of(N), 1) qattend_kernel(const QParams
     }
 }
 
+// Where references are held, by the keys n a CTA passes of a row: 2^(15 - G), G
+// binades below what a weight may reach, with n 2^-(32 - G) <= 2^-9: what is
+// lost of weights too small for e5m2 stays below half a bf16 step of the
+// largest even if they all are.  The more room, the fewer references move.
+float room_of(int64_t n) {
+    int g = 13;
+    while (g > 8 && n > (int64_t(1) << (23 - g))) --g;
+    return std::exp2(15.0f - g);
+}
+
 // What joining cut rows costs, in tiles.
 constexpr int kJoinTiles = 14;
 
@@ -772,7 +1029,7 @@ Shape shape_of(int64_t rows, int heads, int64_t max_keys, bool paged) {
 }
 
 template <int N, int kCl>
-cudaError_t launch_n(const QParams& p, int ctas, cudaStream_t st) {
+cudaError_t launch_n(const QParams& p, const CUtensorMap& ql, const CUtensorMap& qp, int ctas, cudaStream_t st) {
     static std::atomic<unsigned long long> done{0};
     cudaError_t e = set_smem_once(qattend_kernel<N, kCl>, qplan_of(N).total, done);
     if (e != cudaSuccess) return e;
@@ -791,19 +1048,19 @@ cudaError_t launch_n(const QParams& p, int ctas, cudaStream_t st) {
     cfg.attrs = attr;
     cfg.numAttrs = kCl > 1 ? 2 : 1;
     kt_mark(st);
-    e = cudaLaunchKernelEx(&cfg, qattend_kernel<N, kCl>, p);
+    e = cudaLaunchKernelEx(&cfg, qattend_kernel<N, kCl>, ql, qp, p);
     kt_mark(st);
     if (e != cudaSuccess || p.split != 1) return e;
     return launch_join(p, N, ctas, st);
 }
 
 template <int N>
-cudaError_t launch_cl(const QParams& p, const Shape& s, cudaStream_t st) {
+cudaError_t launch_cl(const QParams& p, const CUtensorMap& ql, const CUtensorMap& qp, const Shape& s, cudaStream_t st) {
     switch (s.cluster) {
-        case 2: return launch_n<N, 2>(p, s.ctas, st);
-        case 4: return launch_n<N, 4>(p, s.ctas, st);
-        case 8: return launch_n<N, 8>(p, s.ctas, st);
-        default: return launch_n<N, 1>(p, s.ctas, st);
+        case 2: return launch_n<N, 2>(p, ql, qp, s.ctas, st);
+        case 4: return launch_n<N, 4>(p, ql, qp, s.ctas, st);
+        case 8: return launch_n<N, 8>(p, ql, qp, s.ctas, st);
+        default: return launch_n<N, 1>(p, ql, qp, s.ctas, st);
     }
 }
 
@@ -817,6 +1074,8 @@ size_t qattend_ws_need(int64_t rows, int heads, int64_t max_keys, bool paged) {
 }
 
 cudaError_t launch_qattend(const AttendArgs& a, int64_t block_bytes, cudaStream_t st) {
+    EncodeTiledFn enc = encode_tiled_fn();
+    if (!enc) return cudaErrorNotSupported;
     const Shape s = shape_of(a.rows, a.heads, a.max_keys, a.block_table != nullptr);
     QParams p{};
     p.slots = a.slots; p.slots_stride = a.slots_stride;
@@ -828,12 +1087,17 @@ cudaError_t launch_qattend(const AttendArgs& a, int64_t block_bytes, cudaStream_
     p.out = static_cast<__nv_bfloat16*>(a.out); p.lse = a.lse; p.status = a.status;
     p.part_o = static_cast<float*>(a.ws);
     p.part_ml = reinterpret_cast<float2*>(p.part_o + static_cast<size_t>(2) * s.ctas * s.N * IDX_LATENT_DIM);
-    p.ql = static_cast<const uint16_t*>(a.ql); p.qp = static_cast<const uint16_t*>(a.qp);
-    p.ql_row = a.ql_row; p.ql_head = a.ql_head; p.qp_row = a.qp_row; p.qp_head = a.qp_head;
     p.block_bytes = block_bytes;
-    if (s.N == 16) return launch_cl<16>(p, s, st);
-    if (s.N == 32) return launch_cl<32>(p, s, st);
-    return launch_cl<64>(p, s, st);
+    const int64_t tiles = a.max_keys > 0 ? (a.max_keys + kKeys - 1) / kKeys : 1;
+    const int64_t run = s.split == 1 ? std::min(tiles, (a.rows * s.hgs * tiles + s.ctas - 1) / s.ctas) : (tiles + s.cluster - 1) / s.cluster;
+    p.room = room_of(run * kKeys);
+    CUtensorMap ql, qp;
+    if (!head_map(&ql, enc, a.ql, IDX_LATENT_DIM, a.ql_row, a.ql_head, a.rows, a.heads, s.N, 1, &p.ql_swap) ||
+        !head_map(&qp, enc, a.qp, IDX_LATENT_PE_DIM, a.qp_row, a.qp_head, a.rows, a.heads, s.N, 1, &p.qp_swap))
+        return cudaErrorInvalidValue;
+    if (s.N == 16) return launch_cl<16>(p, ql, qp, s, st);
+    if (s.N == 32) return launch_cl<32>(p, ql, qp, s, st);
+    return launch_cl<64>(p, ql, qp, s, st);
 }
 
 }  // namespace dsaidx
