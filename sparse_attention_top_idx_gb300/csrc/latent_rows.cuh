@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const RowParams p
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int64_t row = blockIdx.x;
     const int warp = warp_id(), lane = lane_id(), wh = warp % kW;
-    const int head = blockIdx.y * (kJoinWarps / kW) + warp / kW, hg = head / 64, h = head % 64;
+    const int head = blockIdx.y * (kJoinWarps / kW) + warp / kW, hg = head / N, h = head % N;
     const bool live = head < p.heads;
     int64_t a, tt;
     const int nt = tiles_of(row_keys(p, row));

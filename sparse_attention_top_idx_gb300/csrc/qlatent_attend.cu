@@ -179,6 +179,11 @@ __device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
+__device__ __forceinline__ uint32_t max_f16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -217,19 +222,20 @@ __device__ __forceinline__ void copy4_or_zero(uint32_t dst, const void* src, uin
 
 // Combines v[0..kH) over the 16 lanes of a half warp: halves are exchanged, so
 // that lane i is left with element i % kH.
-template <int kH, class Op>
-__device__ __forceinline__ float over_keys(float (&v)[kH], Op op) {
+template <int kH, class T, class Op>
+__device__ __forceinline__ T over_keys(T (&v)[kH], Op op) {
     const int lane = lane_id();
 #pragma unroll
     for (int s = kH / 2; s > 0; s /= 2) {
         const bool up = lane & s;
 #pragma unroll
         for (int i = 0; i < s; ++i) {
-            const float give = up ? v[i] : v[i + s], keep = up ? v[i + s] : v[i];
+            const T give = up ? v[i] : v[i + s], keep = up ? v[i + s] : v[i];
             v[i] = op(keep, __shfl_xor_sync(~0u, give, s));
         }
     }
-    if (kH < 16) v[0] = op(v[0], __shfl_xor_sync(~0u, v[0], 8));
+#pragma unroll
+    for (int s = kH; s < 16; s *= 2) v[0] = op(v[0], __shfl_xor_sync(~0u, v[0], s));
     return v[0];
 }
 
@@ -239,8 +245,10 @@ __device__ __forceinline__ float over_keys(float (&v)[kH], Op op) {
 // its hi and lo rows take: a warp reads a head and writes it back split, 16
 // values a lane.  (Read by plain loads instead, two heads ahead, a head took
 // 500 to 1200 cycles: trips to L2.)
+// One copy for the roles that call it: the kernel's code is larger than the
+// instruction caches.
 template <int N>
-__device__ __forceinline__ void split_heads(uint8_t* q, int first, int n, float scale_log2, float* factor) {
+__device__ __noinline__ void split_heads(uint8_t* q, int first, int n, float scale_log2, float* factor) {
     const int lane = lane_id();
 #pragma unroll 2
     for (int h = first; h < first + n; ++h) {
@@ -328,37 +336,38 @@ struct QueryTurn {
     }
 };
 
-// Weights e = 2^(dot f scale - m) of one key's heads, and their products with
-// `by` as the sum of three e5m2 each: the three leading bits, the next three
-// significant ones and the rest rounded, 2^-9 of the product off at most.
-// True where a product is too large (or not a number).
+// Weights e = 2^(dot f scale - m) of one key's heads and, in fp16, their
+// products with `by`.  True where one is too large (or not a number).
 template <int kH>
 __device__ __forceinline__ bool weigh(const f2 (&dot)[kH / 2], const float* factor, float scale, const f2 (&minus_m)[kH / 2], float by,
-                                      f2 (&e)[kH / 2], uint32_t (&part)[3][kH / 4]) {
+                                      f2 (&e)[kH / 2], uint32_t (&r)[kH / 2]) {
     const f2 scale2 = f2_pack(scale, scale), by2 = f2_pack(by, by);
     uint32_t most = 0;
 #pragma unroll
-    for (int i = 0; i < kH / 4; ++i) {
-        const float4 f = reinterpret_cast<const float4*>(factor)[i];
-        uint32_t r[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const float2 y = f2_unpack(f2_fma(dot[2 * i + k], f2_mul(k ? f2_pack(f.z, f.w) : f2_pack(f.x, f.y), scale2), minus_m[2 * i + k]));
-            e[2 * i + k] = f2_pack(exp2_fast(y.x), exp2_fast(y.y));
-            const float2 w = f2_unpack(f2_mul(e[2 * i + k], by2));
-            r[k] = f16x2(w.x, w.y);
-            most = __vmaxu2(most, r[k]);
-        }
-#pragma unroll
-        for (int k = 0; k < 3; ++k) {
-            const uint32_t a = k == 2 ? r[0] + 0x00800080u : r[0], b = k == 2 ? r[1] + 0x00800080u : r[1];
-            part[k][i] = __byte_perm(a, b, 0x7531);
-            if (k == 2) break;
-            r[0] = sub_f16x2(r[0], a & kUpper);
-            r[1] = sub_f16x2(r[1], b & kUpper);
-        }
+    for (int i = 0; i < kH / 2; ++i) {
+        const float2 y = f2_unpack(f2_fma(dot[i], f2_mul(reinterpret_cast<const f2*>(factor)[i], scale2), minus_m[i]));
+        e[i] = f2_pack(exp2_fast(y.x), exp2_fast(y.y));
+        const float2 w = f2_unpack(f2_mul(e[i], by2));
+        r[i] = f16x2(w.x, w.y);
+        most = __vmaxu2(most, r[i]);
     }
     return max(most & 0xFFFFu, most >> 16) > kMost16;
+}
+// The products as the sum of three e5m2 each: the three leading bits, the next
+// three significant ones and the rest rounded, 2^-9 of a product off at most.
+template <int kH>
+__device__ __forceinline__ void in_parts(uint32_t (&r)[kH / 2], uint32_t (&part)[3][kH / 4]) {
+#pragma unroll
+    for (int i = 0; i < kH / 4; ++i) {
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            const uint32_t a = k == 2 ? r[2 * i] + 0x00800080u : r[2 * i], b = k == 2 ? r[2 * i + 1] + 0x00800080u : r[2 * i + 1];
+            part[k][i] = __byte_perm(a, b, 0x7531);
+            if (k == 2) break;
+            r[2 * i] = sub_f16x2(r[2 * i], a & kUpper);
+            r[2 * i + 1] = sub_f16x2(r[2 * i + 1], b & kUpper);
+        }
+    }
 }
 
 template <int N, int kCl>
@@ -372,8 +381,12 @@ __global__ void __launch_bounds__(threads_of(N), 1)
     constexpr int kOCols = kWide ? N : 3 * N;  // accumulator columns of 128 dimensions
     constexpr int kSCol = 4 * kOCols;          // first column behind the accumulators
     constexpr int kH = N / kHalves / 2;        // heads a softmax thread
-    // heads a warp splits: of the four that gather, of the two that do nothing else
+    // heads a warp splits: of the four that gather, of the two that do nothing
+    // else; of a CTA's first row, when the softmax's warps are idle, of those too
     constexpr int kSplit = N == 64 ? 14 : N / 8, kSplitAux = (N - 4 * kSplit) / 2;
+    constexpr int kFirst = N == 16 ? 1 : 2, kFirstAux = N == 16 ? 2 : 4;
+    constexpr int kFirstSoft = (N - 4 * kFirst - 2 * kFirstAux) / (kSoftThreads / 32);
+    static_assert(4 * kFirst + 2 * kFirstAux + kSoftThreads / 32 * kFirstSoft == N, "every head once");
     extern __shared__ __align__(1024) uint8_t smem[];
     uint64_t* bar = reinterpret_cast<uint64_t*>(smem + kPlan.bar_off);
     uint64_t* full = bar;                        // [tiles]
@@ -406,7 +419,7 @@ __global__ void __launch_bounds__(threads_of(N), 1)
             mbar_init(pv_done + i, 1);
             mbar_init(drain + i, 1);
         }
-        mbar_init(q_full, kGatherThreads + 64);
+        mbar_init(q_full, kGatherThreads + 64 + kSoftThreads);
         mbar_init(q_empty, 1);
         mbar_init(q_raw, 1);
         mbar_init(o_empty, kSoftThreads);
@@ -532,7 +545,8 @@ __global__ void __launch_bounds__(threads_of(N), 1)
                     if (t0 + i == split_at) {
                         if (!(ok = turn.wait(q_empty, p_full, p.status, abort_flag))) break;
                         if (!(ok = __all_sync(~0u, wait(q_raw, turn.item & 1, p.status, abort_flag)))) break;
-                        split_heads<N>(smem, wq * kSplit, kSplit, p.scale_log2, factors + turn.item % kFactors * N);
+                        split_heads<N>(smem, wq * (turn.item ? kSplit : kFirst), turn.item ? kSplit : kFirst, p.scale_log2,
+                                       factors + turn.item % kFactors * N);
                         fence_proxy_async_smem();
                         mbar_arrive(q_full);
                         turn.next(w);
@@ -543,7 +557,6 @@ __global__ void __launch_bounds__(threads_of(N), 1)
         copy_wait_all();
     } else if (warp == 1 || warp == 3) {
         // ---- queries: their copies, and the other heads ----
-        const int h0 = 4 * kSplit + (warp >> 1) * kSplitAux;
         QueryTurn turn;
         bool ok = true;
         while (ok && walk.next(w)) {
@@ -551,14 +564,15 @@ __global__ void __launch_bounds__(threads_of(N), 1)
             if (warp == 1 && elect_one()) {
                 mbar_arrive_expect_tx(q_raw, 9 * N * 128);
                 const uint32_t q_addr = smem_u32(smem);
-                const int h = w.hg * 64, row = static_cast<int>(w.row);
+                const int h = w.hg * N, row = static_cast<int>(w.row);
                 for (int c = 0; c < 8; ++c)
                     tma_tile_3d(q_addr + c * N * 128, &ql_map, q_raw, 64 * c, p.ql_swap ? row : h, p.ql_swap ? h : row);
                 tma_tile_3d(q_addr + 8 * N * 128, &qp_map, q_raw, 0, p.qp_swap ? row : h, p.qp_swap ? h : row);
             }
             __syncwarp();
             if (!(ok = __all_sync(~0u, wait(q_raw, turn.item & 1, p.status, abort_flag)))) break;
-            split_heads<N>(smem, h0, kSplitAux, p.scale_log2, factors + turn.item % kFactors * N);
+            const int n = turn.item ? kSplitAux : kFirstAux;
+            split_heads<N>(smem, 4 * (turn.item ? kSplit : kFirst) + (warp >> 1) * n, n, p.scale_log2, factors + turn.item % kFactors * N);
             fence_proxy_async_smem();
             mbar_arrive(q_full);
             turn.next(w);
@@ -658,11 +672,19 @@ __global__ void __launch_bounds__(threads_of(N), 1)
         const int hw = half * (N / kHalves), hb = hw + (lane >> 4) * kH;     // this warp's and this thread's first head
         uint32_t it = 0, item = 0, tb = 0, ph = 0;
         bool ok = true;
-        while (ok && walk.next(w)) {
+        if (sh_run[0] < sh_run[1]) {
+            ok = wait(q_raw, 0, p.status, abort_flag);
+            if (__all_sync(~0u, ok))
+                split_heads<N>(smem, 4 * kFirst + 2 * kFirstAux + (tid >> 5) * kFirstSoft, kFirstSoft, p.scale_log2, factors);
+            fence_proxy_async_smem();
+            mbar_arrive(q_full);
+        }
+        while (walk.next(w)) {
             // reference and this thread's share of the sum of head hb + i; the
             // unit of the scales (a power of two) and what brings it to p.room
             f2 minus_m[kH / 2], sum[kH / 2];
             float top = kNoScale, up = p.room / kNoScale;
+            float ref[2] = {kNone, kNone};      // the references again: of heads lane and lane + 32
 #pragma unroll
             for (int i = 0; i < kH / 2; ++i) {
                 minus_m[i] = f2_pack(-kNone, -kNone);
@@ -672,6 +694,7 @@ __global__ void __launch_bounds__(threads_of(N), 1)
             for (int t = w.t0; t < w.t1; ++t, ++it) {
                 ok = ok && wait(s_full + (it & 1), (it >> 1) & 1, p.status, abort_flag);
                 tc_fence_after();
+                if (t == w.t0) mbar_arrive(q_full);      // this role has no part in the next row's queries
                 uint32_t raw[kH], low[kH];
                 tmem_ld_halves(tmem + lanes + kSCol + (it & 1) * 2 * N + hw, raw);
                 tmem_ld_halves(tmem + lanes + kSCol + (it & 1) * 2 * N + N + hw, low);
@@ -688,12 +711,12 @@ __global__ void __launch_bounds__(threads_of(N), 1)
                 for (int i = 0; i < kH / 2; ++i)
                     dot[i] = f2_fma(f2_pack(__uint_as_float(low[2 * i]), __uint_as_float(low[2 * i + 1])), f2_pack(0.0625f, 0.0625f),
                                   f2_pack(__uint_as_float(raw[2 * i]), __uint_as_float(raw[2 * i + 1])));
-                // Weights, and times the scale as three e5m2; the vote is on their
+                // Weights, and their products with the scale; the vote is on their
                 // size.  Where it moves references they are formed once more (by
                 // the same code: a copy of its own, rarely run, would come from
                 // memory each time).
-                uint32_t part[3][kH / 4];
                 f2 e[kH / 2];
+                uint32_t r[kH / 2];
                 bool again = false;
                 uint32_t which[2];          // heads whose reference moved, and by what: lane and lane + 32
                 float factor_of[2];
@@ -701,7 +724,7 @@ __global__ void __launch_bounds__(threads_of(N), 1)
                 for (;; again = true) {
                     const float by = valid ? scale * up : 0.0f;
                     if (again || t != w.t0) {       // (a row's first tile sets them)
-                        bool grow = weigh<kH>(dot, factor, scale, minus_m, by, e, part);
+                        bool grow = weigh<kH>(dot, factor, scale, minus_m, by, e, r);
                         grow |= by > kMost * kMostScale && top < kTopUnit;
                         if (valid && scale < kLeast) {
                             // such a key's weight has no product to judge it by
@@ -711,9 +734,7 @@ __global__ void __launch_bounds__(threads_of(N), 1)
                         if (!valid) {
                             grow = false;
 #pragma unroll
-                            for (int i = 0; i < kH / 2; ++i) e[i] = 0;
-#pragma unroll
-                            for (int i = 0; i < kH / 4; ++i) part[0][i] = part[1][i] = part[2][i] = 0u;
+                            for (int i = 0; i < kH / 2; ++i) e[i] = r[i] = 0;
                         }
                         if (again || !named_any<1, kSoftThreads>(grow || !ok)) break;
                     }
@@ -725,18 +746,18 @@ __global__ void __launch_bounds__(threads_of(N), 1)
                     // (the unit's log2 is taken off below; scales below 2^-32, which
                     // the format does not have, count as that)
                     const float shift = __log2f(fmaxf(scale, kLeast));
-                    float v[kH];
+                    // (in fp16: a reference need not be the largest to the last bit)
+                    uint32_t v[kH / 2];
+                    const f2 scale2 = f2_pack(scale, scale), shift2 = f2_pack(shift, shift);
 #pragma unroll
-                    for (int i = 0; i < kH; ++i) {
-                        const float2 x = f2_unpack(dot[i / 2]);
-                        v[i] = valid ? fmaf(i & 1 ? x.y : x.x, scale * factor[i], shift) : -INFINITY;
+                    for (int i = 0; i < kH / 2; ++i) {
+                        const float2 x = f2_unpack(f2_fma(dot[i], f2_mul(reinterpret_cast<const f2*>(factor)[i], scale2), shift2));
+                        v[i] = valid ? f16x2(x.x, x.y) : 0xFC00FC00u;
                     }
-                    const float most = over_keys(v, [](float a, float b) { return fmaxf(a, b); });
-                    if ((lane & 15) < kH) stat[sw * N + hb + (lane & 15)] = most;
-                    if (sw == 0 && (lane & 15) == 0) {
-#pragma unroll
-                        for (int i = 0; i < kH; ++i)
-                            stat[4 * N + hb + i] = -(i & 1 ? f2_unpack(minus_m[i / 2]).y : f2_unpack(minus_m[i / 2]).x);
+                    const uint32_t most = over_keys(v, [](uint32_t a, uint32_t b) { return max_f16x2(a, b); });
+                    if ((lane & 15) < kH / 2) {
+                        const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&most));
+                        *reinterpret_cast<float2*>(stat + sw * N + hb + 2 * (lane & (kH / 2 - 1))) = x;
                     }
                     // a wait that ran out in any thread ends the loop in all
                     if (named_any<1, kSoftThreads>(!ok)) { ok = false; break; }
@@ -757,12 +778,11 @@ __global__ void __launch_bounds__(threads_of(N), 1)
                     // thread for its own heads is shorter in steps and longer in
                     // code, which comes from memory: it ran 3.2k cycles.)
                     const float unit = __log2f(top), more = exp2_fast(fall);
-                    float ref[2];
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         const int h = (lane + 32 * k) & (N - 1);
                         const float m = fmaxf(fmaxf(stat[h], stat[N + h]), fmaxf(stat[2 * N + h], stat[3 * N + h])) - unit;
-                        const float old = stat[4 * N + h] - fall;
+                        const float old = ref[k] - fall;
                         ref[k] = m - old > kNear ? m : old;
                         factor_of[k] = exp2_fast(old - ref[k]);
                         which[k] = __ballot_sync(~0u, factor_of[k] != 1.0f && (N == 64 || (k == 0 && lane < N)));
@@ -817,6 +837,8 @@ __global__ void __launch_bounds__(threads_of(N), 1)
                 }
 #pragma unroll
                 for (int i = 0; i < kH / 2; ++i) sum[i] = f2_add(sum[i], e[i]);
+                uint32_t part[3][kH / 4];
+                in_parts<kH>(r, part);
                 // the weight tile before last was read
                 if (it > 1) ok = wait(pv_done + (it & 1), ((it >> 1) & 1) ^ 1, p.status, abort_flag) && ok;
                 uint8_t* pt = smem + kPlan.p_off + (it & 1) * kPlan.p_bytes;
@@ -850,10 +872,9 @@ __global__ void __launch_bounds__(threads_of(N), 1)
                 for (int i = 0; i < kH; ++i) v[i] = i & 1 ? f2_unpack(sum[i / 2]).y : f2_unpack(sum[i / 2]).x;
                 const float all = over_keys(v, [](float a, float b) { return a + b; });
                 if ((lane & 15) < kH) stat[sw * N + hb + (lane & 15)] = all;
-                if (sw == 0 && (lane & 15) == 0) {
-#pragma unroll
-                    for (int i = 0; i < kH; ++i)
-                        stat[4 * N + hb + i] = -(i & 1 ? f2_unpack(minus_m[i / 2]).y : f2_unpack(minus_m[i / 2]).x);
+                if (tid < 32) {
+                    if (lane < N) stat[4 * N + lane] = ref[0];
+                    if (N == 64) stat[4 * N + 32 + lane] = ref[1];
                 }
             }
             if (named_any<1, kSoftThreads>(!ok)) { ok = false; break; }
@@ -880,7 +901,7 @@ __global__ void __launch_bounds__(threads_of(N), 1)
                 }
                 break;      // a cluster's CTA has one piece
             }
-            const int h0 = w.hg * 64;
+            const int h0 = w.hg * N;
             if (tid < N) {
                 const float l = stat[tid] + stat[N + tid] + stat[2 * N + tid] + stat[3 * N + tid];
                 const float m = stat[4 * N + tid];
@@ -950,36 +971,64 @@ __global__ void __launch_bounds__(threads_of(N), 1)
         cluster_arrive();
         cluster_wait();
         const int64_t row = sh_run[2];
-        const int h0 = static_cast<int>(sh_run[3]) * 64;
-        for (int i = threadIdx.x; i < kShare * (IDX_LATENT_DIM / 4); i += threads_of(N)) {
-            const int h = rank * kShare + i / (IDX_LATENT_DIM / 4), d = 4 * (i % (IDX_LATENT_DIM / 4));
-            if (h0 + h >= p.heads) continue;
+        const int h0 = static_cast<int>(sh_run[3]) * N;
+        // Factors of each CTA's sums by head, then the sums, four quadruples a
+        // thread on their way: little code, as all of it comes from memory.  (Every
+        // thread for itself, each of its heads: 9.4k cycles instead of 4k.)
+        float* weight = reinterpret_cast<float*>(smem + N * IDX_LATENT_DIM * 4);     // [kCl][kShare], behind the share
+        if (threadIdx.x < kShare) {
+            const int h = rank * kShare + threadIdx.x;
             float2 ml[kCl];
-            float4 v[kCl];
             float m = kNone, l = 0.0f;
 #pragma unroll
             for (int r = 0; r < kCl; ++r) {
-                const uint2 b = dsmem_ld_v2(dsmem_addr(stat + 2 * h, r));
-                ml[r] = make_float2(__uint_as_float(b.x), __uint_as_float(b.y));
-                v[r] = dsmem_ld_f4(dsmem_addr(smem + (h * IDX_LATENT_DIM + d) * 4, r));
+                const uint2 u = dsmem_ld_v2(dsmem_addr(stat + 2 * h, r));
+                ml[r] = make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
                 if (ml[r].y != 0.0f) m = fmaxf(m, ml[r].x);
             }
-            float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
             for (int r = 0; r < kCl; ++r) {
-                if (ml[r].y == 0.0f) continue;      // nothing there: neither are its sums
-                const float f = exp2_fast(ml[r].x - m);
-                l += ml[r].y * f;
-                o.x += v[r].x * f;
-                o.y += v[r].y * f;
-                o.z += v[r].z * f;
-                o.w += v[r].w * f;
+                ml[r].x = ml[r].y != 0.0f ? exp2_fast(ml[r].x - m) : 0.0f;
+                if (ml[r].y != 0.0f) l += ml[r].y * ml[r].x;
             }
             const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
-            const int64_t at = row * p.heads + h0 + h;
-            *reinterpret_cast<uint2*>(p.out + at * IDX_LATENT_DIM + d) =
-                make_uint2(bf16x2(o.x * inv, o.y * inv), bf16x2(o.z * inv, o.w * inv));
-            if (d == 0 && p.lse != nullptr) p.lse[at] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+#pragma unroll
+            for (int r = 0; r < kCl; ++r) weight[r * kShare + threadIdx.x] = ml[r].x * inv;
+            if (p.lse != nullptr && h0 + h < p.heads)
+                p.lse[row * p.heads + h0 + h] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+        }
+        __syncthreads();
+        // threads a head: 128, four dimensions each
+        const int d = 4 * (threadIdx.x & 127);
+        constexpr int kStep = threads_of(N) / 128, kBatch = kShare / kStep < 1 ? 1 : kShare / kStep < 4 ? kShare / kStep : 4;
+#pragma unroll 1
+        for (int k0 = threadIdx.x >> 7; k0 < kShare; k0 += kStep * kBatch) {
+            float4 o[kBatch];
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b) o[b] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 1
+            for (int r = 0; r < kCl; ++r) {
+                const uint32_t from = dsmem_addr(smem, r) + (rank * kShare * IDX_LATENT_DIM + d) * 4;
+                float4 v[kBatch];
+#pragma unroll
+                for (int b = 0; b < kBatch; ++b) v[b] = dsmem_ld_f4(from + min(k0 + b * kStep, kShare - 1) * (IDX_LATENT_DIM * 4));
+#pragma unroll
+                for (int b = 0; b < kBatch; ++b) {
+                    const float f = weight[r * kShare + min(k0 + b * kStep, kShare - 1)];
+                    if (f == 0.0f) continue;      // nothing there: neither are its sums
+                    o[b].x += v[b].x * f;
+                    o[b].y += v[b].y * f;
+                    o[b].z += v[b].z * f;
+                    o[b].w += v[b].w * f;
+                }
+            }
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b) {
+                const int h = rank * kShare + k0 + b * kStep;
+                if (k0 + b * kStep < kShare && h0 + h < p.heads)
+                    *reinterpret_cast<uint2*>(p.out + (row * p.heads + h0 + h) * IDX_LATENT_DIM + d) =
+                        make_uint2(bf16x2(o[b].x, o[b].y), bf16x2(o[b].z, o[b].w));
+            }
         }
         // nobody leaves while another still reads its share
         cluster_arrive();
@@ -988,22 +1037,23 @@ __global__ void __launch_bounds__(threads_of(N), 1)
 }
 
 // Where references are held, by the keys n a CTA passes of a row: 2^(15 - G), G
-// binades below what a weight may reach, with n 2^-(32 - G) <= 2^-9: what is
-// lost of weights too small for e5m2 stays below half a bf16 step of the
-// largest even if they all are.  The more room, the fewer references move.
+// binades below what a weight may reach, with n 2^-(32 - G) <= 2^-8: what is
+// lost of weights too small for e5m2 stays below a bf16 step of the largest
+// even if they all are.  The more room, the fewer references move.
 float room_of(int64_t n) {
-    int g = 13;
-    while (g > 8 && n > (int64_t(1) << (23 - g))) --g;
+    int g = 16;
+    while (g > 8 && n > (int64_t(1) << (24 - g))) --g;
     return std::exp2(15.0f - g);
 }
 
 // What joining cut rows costs, in tiles.
 constexpr int kJoinTiles = 14;
 
-Shape shape_of(int64_t rows, int heads, int64_t max_keys, bool paged) {
+// Rows of N heads each over CTAs; *cost in ns.
+Shape shape_n(int64_t rows, int heads, int N, int64_t max_keys, bool paged, int64_t* cost) {
     Shape s{};
-    s.N = width_of(heads);
-    s.hgs = (heads + 63) / 64;
+    s.N = N;
+    s.hgs = (heads + N - 1) / N;
     s.cluster = 1;
     const int64_t g = kMaxCtas;
     const int64_t items = rows * s.hgs, nt = max_keys > 0 ? (max_keys + kKeys - 1) / kKeys : 1;
@@ -1020,10 +1070,27 @@ Shape shape_of(int64_t rows, int heads, int64_t max_keys, bool paged) {
     }
     const int64_t cut = (items * nt + g - 1) / g + kJoinTiles;
     if (cut < best) {
+        best = cut;
         s.split = 1;
         s.cluster = 1;
         const int64_t n = (items * nt + kMinRun - 1) / kMinRun;
         s.ctas = static_cast<int>(n < g ? n : g);
+    }
+    *cost = best * (N == 64 ? 20 : N == 32 ? 13 : 10);
+    return s;
+}
+
+// Fewer heads a CTA where that spreads the rows over more of them.
+Shape shape_of(int64_t rows, int heads, int64_t max_keys, bool paged) {
+    const int widest = width_of(heads);
+    int64_t best, cost;
+    Shape s = shape_n(rows, heads, widest, max_keys, paged, &best);
+    for (int N = widest / 2; N >= 16; N /= 2) {
+        const Shape t = shape_n(rows, heads, N, max_keys, paged, &cost);
+        if (cost < best) {
+            best = cost;
+            s = t;
+        }
     }
     return s;
 }

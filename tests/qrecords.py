@@ -91,10 +91,10 @@ def attend64(q, rec, s, scale):
     * A score sums 2 * 576 products in fp32 (the query is held as two numbers), each exact: terms * 2^-23 of the sum of
       magnitudes; a query element is off by 2^-22 of its head's largest.  Together delta; a weight changes by exp(delta).
     * Weights are held in 9 significant bits and rounded once before, 2^-9 + 2^-11 < 2^-8 of sum p |c|.  The smallest
-      e5m2 is 2^-16, so that a weight times its scale is never closer than 2^-17, and the largest of a head's is held at
-      2^2 or more: 2^-19 of the largest p s for every code.  Where a row is worked on in pieces of n keys, each relative
-      to its own largest, that is held at 2^(15 - G), n 2^-(32 - G) <= 2^-9: the pieces together lose no more than 2^-9
-      of sum p s times the largest code.
+      e5m2 is 2^-16, so that a weight times its scale is never closer than 2^-17.  The largest of a head's over n keys
+      worked on together is held at 2^(15 - G) or more, G <= 16 and n 2^-(32 - G) <= 2^-8: 2^-16 of the largest p s for
+      every code, and together no more than 2^-8 of it times the largest code.  Where a row is worked on in pieces, each
+      relative to its own largest, the latter is no more than 2^-8 of sum p s.
     * The result is rounded to bf16: 2^-8.
     """
     H = q.shape[0]
@@ -109,7 +109,7 @@ def attend64(q, rec, s, scale):
     v = rec[:, :LAT]
     o = p @ v
     codes = v.abs() / torch.where(s > 0, s, 1.0)[:, None]
-    floor = torch.minimum(2.0 ** -19 * (p * s).amax(1, keepdim=True) * codes.sum(0), 2.0 ** -9 * (p @ s)[:, None] * codes.amax(0))
+    floor = torch.minimum(2.0 ** -16 * (p * s).amax(1, keepdim=True) * codes.sum(0), 2.0 ** -8 * (p @ s)[:, None] * codes.amax(0))
     tol = (2.0 ** -8 + 2 * (2 * delta).expm1())[:, None] * (p @ v.abs()) + floor + 2.0 ** -8 * o.abs() + 1e-30
     return o, lse, tol, delta + lse.abs() * 2.0 ** -22 + 2.0 ** -19
 
