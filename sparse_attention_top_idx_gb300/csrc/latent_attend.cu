@@ -60,6 +60,7 @@ namespace dsaidx {
 
 namespace {
 
+constexpr int kKeys = 64;                  // keys a tile
 constexpr int kChunk = kKeys * 128;        // bytes of a chunk: 64 keys x 64 values
 constexpr int kPair = 2 * kChunk;
 // Softmax warpgroups: two at 64 heads (4096 rows of 1024 keys, 128 heads, 1.43
@@ -160,7 +161,7 @@ __global__ void __launch_bounds__(threads_of(N), 1)
             const int item = blockIdx.x / kCl, rank = blockIdx.x % kCl;
             row = item / p.hgs;
             base = item % p.hgs;
-            const int64_t nt = tiles_of(row_keys(p, row));
+            const int64_t nt = tiles_of<kKeys>(row_keys(p, row));
             start = rank * nt / kCl;
             end = (rank + 1) * nt / kCl;
         } else if (!p.split) {
@@ -169,14 +170,14 @@ __global__ void __launch_bounds__(threads_of(N), 1)
         } else {
             int64_t tt;
             if (p.block_table == nullptr) {
-                tt = p.rows * p.hgs * tiles_of(p.max_keys);
+                tt = p.rows * p.hgs * tiles_of<kKeys>(p.max_keys);
             } else {
                 int64_t none;
-                find_row(p, -1, none, tt);
+                find_row<kKeys>(p, -1, none, tt);
             }
             start = run_start(blockIdx.x, gridDim.x, tt);
             end = run_start(blockIdx.x + 1, gridDim.x, tt);
-            if (p.block_table != nullptr && start < end) find_row(p, start, row, base);
+            if (p.block_table != nullptr && start < end) find_row<kKeys>(p, start, row, base);
         }
         if (lane == 0) {
             sh_run[0] = start;
@@ -190,7 +191,7 @@ __global__ void __launch_bounds__(threads_of(N), 1)
     tc_fence_after();
     const uint32_t tmem = *sh_tmem;
     volatile int* abort_flag = sh_abort;
-    Walk walk(p, sh_run[0], sh_run[1], sh_run[2], sh_run[3]);
+    Walk<kKeys> walk(p, sh_run[0], sh_run[1], sh_run[2], sh_run[3]);
     Work w;
 
     if (warp >= 8 && warp < 12) {
@@ -676,7 +677,7 @@ cudaError_t launch_n(const Params& p, const CUtensorMap& ql, const CUtensorMap& 
     e = cudaLaunchKernelEx(&cfg, attend_kernel<N, kCl>, ql, qp, p);
     kt_mark(st);
     if (e != cudaSuccess || p.split != 1) return e;
-    return launch_join(p, N, ctas, st);
+    return launch_join<kKeys>(p, N, ctas, st);
 }
 
 template <int N>

@@ -13,7 +13,6 @@ namespace dsaidx {
 
 namespace {
 
-constexpr int kKeys = 64;                  // keys a tile
 constexpr int kMaxCtas = 152;              // one an SM; CTAs of different clusters never wait on one another
 constexpr int kMinRun = 2;                 // tiles a CTA, at least, where rows are cut
 constexpr float kNone = -3.0e38f;          // maximum of a head without a key so far
@@ -43,8 +42,9 @@ __device__ __forceinline__ int row_keys(const RowParams& p, int64_t row) {
     if (n < 0 || n > p.max_keys || n > static_cast<int64_t>(p.mbps) * p.block_size) return 0;
     return n;
 }
-// Tiles of a row; one for an empty row, which still writes its result.
-__device__ __forceinline__ int tiles_of(int keys) { return keys > 0 ? (keys - 1) / kKeys + 1 : 1; }
+// Tiles (of kTile keys) of a row; one for an empty row, which still writes its result.
+template <int kTile>
+__device__ __forceinline__ int tiles_of(int keys) { return keys > 0 ? (keys - 1) / kTile + 1 : 1; }
 
 // Where the run of CTA c of g begins in the line of tt tiles.
 __device__ __forceinline__ int64_t run_start(int64_t c, int64_t g, int64_t tt) { return c * tt / g; }
@@ -52,12 +52,13 @@ __device__ __forceinline__ int64_t run_start(int64_t c, int64_t g, int64_t tt) {
 // Row in whose tiles position x of the line lies, and where the row begins
 // (both scaled by the head groups); with x < 0 the length of the line.
 // Executed by a whole warp; paged contexts only.
+template <int kTile>
 __device__ __forceinline__ void find_row(const RowParams& p, int64_t x, int64_t& row, int64_t& base) {
     const int lane = lane_id();
     int64_t acc = 0;
     for (int64_t r0 = 0; r0 < p.rows; r0 += 32) {
         const int64_t r = r0 + lane;
-        int64_t v = r < p.rows ? static_cast<int64_t>(tiles_of(row_keys(p, r))) * p.hgs : 0;
+        int64_t v = r < p.rows ? static_cast<int64_t>(tiles_of<kTile>(row_keys(p, r))) * p.hgs : 0;
         for (int d = 1; d < 32; d <<= 1) {
             const int64_t u = __shfl_up_sync(~0u, v, d);
             if (lane >= d) v += u;
@@ -84,6 +85,7 @@ struct Work {
 };
 
 // The pieces of this CTA, in order; every role walks them by itself.
+template <int kTile>
 struct Walk {
     int64_t pos, end;        // split: the run left; whole: item and number of items
     int64_t row, base;       // split, paged: current row and where it begins; cluster: row and head group
@@ -107,7 +109,7 @@ struct Walk {
             w.hg = static_cast<int>(pos - w.row * p.hgs);
             w.keys = row_keys(p, w.row);
             w.t0 = 0;
-            w.t1 = tiles_of(w.keys);
+            w.t1 = tiles_of<kTile>(w.keys);
             w.slot = -1;
             pos += gridDim.x;
             return true;
@@ -116,19 +118,19 @@ struct Walk {
         int nt;
         if (p.block_table == nullptr) {
             w.keys = p.max_keys;
-            nt = tiles_of(w.keys);
+            nt = tiles_of<kTile>(w.keys);
             const int64_t item = pos / nt;
             w.row = item / p.hgs;
             w.hg = static_cast<int>(item - w.row * p.hgs);
             in = pos - item * nt;
         } else {
             w.keys = row_keys(p, row);
-            nt = tiles_of(w.keys);
+            nt = tiles_of<kTile>(w.keys);
             if (pos - base >= static_cast<int64_t>(nt) * p.hgs) {
                 base += static_cast<int64_t>(nt) * p.hgs;
                 ++row;
                 w.keys = row_keys(p, row);
-                nt = tiles_of(w.keys);
+                nt = tiles_of<kTile>(w.keys);
             }
             w.row = row;
             w.hg = static_cast<int>((pos - base) / nt);
@@ -173,7 +175,7 @@ __device__ __forceinline__ int key_slot(const RowParams& p, int keys, int j, int
 // dimensions; the warps' sums are added in order.  A CTA has eight warps.
 constexpr int kJoinWarps = 8;
 
-template <int kW>
+template <int kW, int kTile>
 __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const RowParams p, int N, int ctas) {
     __shared__ float acc[kW > 1 ? kJoinWarps : 1][IDX_LATENT_DIM];
     __shared__ float factor[kJoinWarps][kMaxCtas];     // of each piece, 0 where there is nothing
@@ -185,14 +187,14 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const RowParams p
     const int head = blockIdx.y * (kJoinWarps / kW) + warp / kW, hg = head / N, h = head % N;
     const bool live = head < p.heads;
     int64_t a, tt;
-    const int nt = tiles_of(row_keys(p, row));
+    const int nt = tiles_of<kTile>(row_keys(p, row));
     if (p.block_table == nullptr) {
         tt = p.rows * p.hgs * nt;
         a = row * p.hgs * nt;
     } else {
         int64_t before = 0, all = 0;
         for (int64_t r = lane; r < p.rows; r += 32) {
-            const int64_t t = static_cast<int64_t>(tiles_of(row_keys(p, r))) * p.hgs;
+            const int64_t t = static_cast<int64_t>(tiles_of<kTile>(row_keys(p, r))) * p.hgs;
             all += t;
             if (r < row) before += t;
         }
@@ -293,7 +295,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const RowParams p
 }
 
 // Launches the join of a call that was cut over `ctas` CTAs.
-inline cudaError_t launch_join(const RowParams& p, int N, int ctas, cudaStream_t st) {
+template <int kTile>
+cudaError_t launch_join(const RowParams& p, int N, int ctas, cudaStream_t st) {
     // warps a (row, head): eight where rows have many pieces, else as many as
     // there is parallelism for.  Measured: 9 rows to 75 pieces, 16 heads, whole
     // call 403 us with one warp, 369 with eight; 32 rows of 3.4 pieces, 128
@@ -311,7 +314,7 @@ inline cudaError_t launch_join(const RowParams& p, int N, int ctas, cudaStream_t
     cfg.numAttrs = 1;
     kt_mark(st);
     const cudaError_t e =
-        cudaLaunchKernelEx(&cfg, warps == 8 ? join_kernel<8> : warps == 4 ? join_kernel<4> : join_kernel<1>, p, N, ctas);
+        cudaLaunchKernelEx(&cfg, warps == 8 ? join_kernel<8, kTile> : warps == 4 ? join_kernel<4, kTile> : join_kernel<1, kTile>, p, N, ctas);
     kt_mark(st);
     return e;
 }

@@ -50,10 +50,13 @@ namespace dsaidx {
 
 namespace {
 
-constexpr int kChunk = kKeys * 128;        // bytes of a chunk: 128 codes or 64 bf16 of 64 keys
+// Keys a tile: as many as the tensor core's 128 rows where shared memory and
+// registers hold them.  A tile costs the softmax about as much whichever it is.
+constexpr int keys_of(int N) { return N == 64 ? 64 : 128; }
+constexpr int chunk_of(int N) { return keys_of(N) * 128; }      // bytes of a chunk: 128 codes or 64 bf16 of each key
 constexpr int kTileChunks = 5;             // a tile: one chunk of position parts, four of codes
 constexpr int kFactors = 2;                // rows whose heads' factors are held
-constexpr int halves_of(int N) { return N == 64 ? 2 : 1; }      // softmax warpgroups
+constexpr int halves_of(int N) { return N == 16 ? 1 : 2; }      // softmax warpgroups
 constexpr int threads_of(int N) { return 256 + 128 * halves_of(N); }
 constexpr int kGatherThreads = 128;
 // A head's weights times scales are held relative to a reference, at 2^7 where
@@ -75,18 +78,18 @@ struct QPlan {
 };
 __host__ __device__ constexpr QPlan qplan_of(int N) {
     QPlan p{};
-    p.slots = N == 64 ? 15 : N == 32 ? 21 : 24;
+    p.slots = N == 64 ? 15 : N == 32 ? 9 : 11;
     // scales and masks of a tile are written when its last chunk's slot is
     // free, so that many tiles' are held at once
     p.tiles = (p.slots + kTileChunks - 1) / kTileChunks;
-    p.p_bytes = N == 16 ? 4096 : N == 32 ? 8192 : 3 * 4096;
+    p.p_bytes = keys_of(N) * (N == 16 ? 64 : N == 32 ? 128 : 3 * 64);
     int o = 5 * 2 * N * 128;
     p.p_off = o;      o += 2 * p.p_bytes;
-    p.ring_off = o;   o += p.slots * kChunk;
-    p.scale_off = o;  o += p.tiles * kKeys * 4;
+    p.ring_off = o;   o += p.slots * chunk_of(N);
+    p.scale_off = o;  o += p.tiles * keys_of(N) * 4;
     p.factor_off = o; o += kFactors * N * 4;
     p.stat_off = o;   o += 5 * N * 4 + 16;     // four warps' values and one for all; the warps' largest scales
-    p.mask_off = o;   o += p.tiles * 8;
+    p.mask_off = o;   o += p.tiles * 16;
     p.bar_off = o;    o += (p.tiles + p.slots + 19) * 8;
     p.total = o;
     return p;
@@ -97,10 +100,16 @@ static_assert(qplan_of(64).ring_off % 1024 == 0 && qplan_of(32).ring_off % 1024 
               "the swizzle's period");
 
 struct QParams : RowParams {
-    int64_t block_bytes;
+    int64_t block_bytes, num_blocks;
+    uint32_t div_mul;          // n / block_size = n div_mul >> div_shift for n < 2^31
+    int div_shift;
     int ql_swap, qp_swap;      // the map's middle dimension is the row
     float room;        // where a reference is held
 };
+
+__device__ __forceinline__ uint32_t block_of(const QParams& p, uint32_t n) {
+    return static_cast<uint32_t>((static_cast<uint64_t>(n) * p.div_mul) >> p.div_shift);
+}
 
 // MN-major operand of 64-byte rows with the 64-byte swizzle: rows are the K
 // index, 8-row groups 512 bytes apart.
@@ -114,8 +123,8 @@ __device__ __forceinline__ uint64_t sdesc_mn_sw64(uint32_t saddr) {
     return d;
 }
 
-// kH columns of 16 rows a warp: lanes 0-15 read columns [c, c + kH), lanes
-// 16-31 those kH further on, of row lane % 16.
+// 32 columns of 16 rows a warp: lanes 0-15 read columns [c, c + 16), lanes
+// 16-31 those 16 further on, of row lane % 16.
 __device__ __forceinline__ void tmem_ld_halves(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.16x32bx2.x16.b32 "
@@ -125,21 +134,6 @@ __device__ __forceinline__ void tmem_ld_halves(uint32_t taddr, uint32_t (&r)[16]
         : "r"(taddr)
         : "memory");
 }
-__device__ __forceinline__ void tmem_ld_halves(uint32_t taddr, uint32_t (&r)[8]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x32bx2.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8], 8;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-        : "r"(taddr)
-        : "memory");
-}
-__device__ __forceinline__ void tmem_wait_halves(uint32_t (&r)[16]) { tmem_wait_ld16(r); }
-__device__ __forceinline__ void tmem_wait_halves(uint32_t (&r)[8]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
-                 :
-                 : "memory");
-}
-
 // One column of this thread's lane.
 __device__ __forceinline__ void tmem_ld1_nowait(uint32_t taddr, uint32_t& r) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr) : "memory");
@@ -220,9 +214,9 @@ __device__ __forceinline__ void copy4_or_zero(uint32_t dst, const void* src, uin
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
-// Combines v[0..kH) over the 16 lanes of a half warp: halves are exchanged, so
-// that lane i is left with element i % kH.
-template <int kH, class T, class Op>
+// Combines v[0..kH) over kLanes lanes (a warp, or each half of one): halves are
+// exchanged, so that lane i is left with element i % kH.
+template <int kLanes, int kH, class T, class Op>
 __device__ __forceinline__ T over_keys(T (&v)[kH], Op op) {
     const int lane = lane_id();
 #pragma unroll
@@ -235,7 +229,7 @@ __device__ __forceinline__ T over_keys(T (&v)[kH], Op op) {
         }
     }
 #pragma unroll
-    for (int s = kH; s < 16; s *= 2) v[0] = op(v[0], __shfl_xor_sync(~0u, v[0], s));
+    for (int s = kH; s < kLanes; s *= 2) v[0] = op(v[0], __shfl_xor_sync(~0u, v[0], s));
     return v[0];
 }
 
@@ -301,10 +295,12 @@ __device__ __noinline__ bool wait_longer(uint64_t* bar, uint32_t parity, int32_t
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int32_t* status, volatile int* abort_flag) {
     return mbar_try_wait(bar, parity) || wait_longer(bar, parity, status, abort_flag);
 }
-__device__ __noinline__ bool next_piece(const QParams* p, Walk* walk, Work* w) { return walk->next(*p, *w); }
+template <int kTile>
+__device__ __noinline__ bool next_piece(const QParams* p, Walk<kTile>* walk, Work* w) { return walk->next(*p, *w); }
+template <int kTile>
 struct Pieces {
     const QParams* p;
-    Walk walk;
+    Walk<kTile> walk;
     __device__ __forceinline__ bool next(Work& w) {
         Work got;
         const bool more = next_piece(p, &walk, &got);
@@ -376,11 +372,13 @@ __global__ void __launch_bounds__(threads_of(N), 1)
                    const __grid_constant__ QParams p) {
     constexpr QPlan kPlan = qplan_of(N);
     constexpr int kSlots = kPlan.slots, kTiles = kPlan.tiles;
-    constexpr int kHalves = halves_of(N), kSoftThreads = 128 * kHalves, kGroupsM = 4 / kHalves;
+    constexpr int kKeys = keys_of(N), kChunk = chunk_of(N), kHalves = halves_of(N), kSoftThreads = 128 * kHalves, kGroupsM = 4 / kHalves;
     constexpr bool kWide = N == 64;            // the weights' parts share the accumulators
     constexpr int kOCols = kWide ? N : 3 * N;  // accumulator columns of 128 dimensions
     constexpr int kSCol = 4 * kOCols;          // first column behind the accumulators
-    constexpr int kH = N / kHalves / 2;        // heads a softmax thread
+    constexpr int kWarpKeys = kKeys / 4;       // keys of a tile that a gather warp copies and a softmax warp weighs
+    constexpr int kH = kWide ? 16 : N / kHalves;       // heads a softmax thread
+    static_assert(kH == 16, "of half a warp where that has 16 keys");
     // heads a warp splits: of the four that gather, of the two that do nothing
     // else; of a CTA's first row, when the softmax's warps are idle, of those too
     constexpr int kSplit = N == 64 ? 14 : N / 8, kSplitAux = (N - 4 * kSplit) / 2;
@@ -403,8 +401,8 @@ __global__ void __launch_bounds__(threads_of(N), 1)
     int64_t* sh_run = reinterpret_cast<int64_t*>(s_full + 14);   // start, end, row, base
     uint32_t* sh_tmem = reinterpret_cast<uint32_t*>(s_full + 18);
     int* sh_abort = reinterpret_cast<int*>(sh_tmem + 1);
-    uint16_t* masks = reinterpret_cast<uint16_t*>(smem + kPlan.mask_off);   // [tiles][4]: 16 keys each
-    float* scales = reinterpret_cast<float*>(smem + kPlan.scale_off);       // [tiles][64]
+    uint32_t* masks = reinterpret_cast<uint32_t*>(smem + kPlan.mask_off);   // [tiles][4]: a warp's keys each
+    float* scales = reinterpret_cast<float*>(smem + kPlan.scale_off);       // [tiles][kKeys]
     float* factors = reinterpret_cast<float*>(smem + kPlan.factor_off);     // [kFactors][N]
     float* stat = reinterpret_cast<float*>(smem + kPlan.stat_off);          // [5][N], [4]
     const int warp = warp_id(), lane = lane_id();
@@ -442,7 +440,7 @@ __global__ void __launch_bounds__(threads_of(N), 1)
             const int item = blockIdx.x / kCl, rank = blockIdx.x % kCl;
             row = item / p.hgs;
             base = item % p.hgs;
-            const int64_t nt = tiles_of(row_keys(p, row));
+            const int64_t nt = tiles_of<kKeys>(row_keys(p, row));
             start = rank * nt / kCl;
             end = (rank + 1) * nt / kCl;
         } else if (!p.split) {
@@ -451,14 +449,14 @@ __global__ void __launch_bounds__(threads_of(N), 1)
         } else {
             int64_t tt;
             if (p.block_table == nullptr) {
-                tt = p.rows * p.hgs * tiles_of(p.max_keys);
+                tt = p.rows * p.hgs * tiles_of<kKeys>(p.max_keys);
             } else {
                 int64_t none;
-                find_row(p, -1, none, tt);
+                find_row<kKeys>(p, -1, none, tt);
             }
             start = run_start(blockIdx.x, gridDim.x, tt);
             end = run_start(blockIdx.x + 1, gridDim.x, tt);
-            if (p.block_table != nullptr && start < end) find_row(p, start, row, base);
+            if (p.block_table != nullptr && start < end) find_row<kKeys>(p, start, row, base);
         }
         if (lane == 0) {
             sh_run[0] = start;
@@ -472,7 +470,7 @@ __global__ void __launch_bounds__(threads_of(N), 1)
     tc_fence_after();
     const uint32_t tmem = *sh_tmem;
     volatile int* abort_flag = sh_abort;
-    Pieces walk{&p, Walk(p, sh_run[0], sh_run[1], sh_run[2], sh_run[3])};
+    Pieces<kKeys> walk{&p, Walk<kKeys>(p, sh_run[0], sh_run[1], sh_run[2], sh_run[3])};
     Work w;
 
     if (warp >= 8 && warp < 12) {
@@ -480,9 +478,9 @@ __global__ void __launch_bounds__(threads_of(N), 1)
         // A copy instruction moves 128 bytes of four keys: lane / 8 is the key
         // among them, lane % 8 the 16-byte piece.
         const int wq = warp - 8, sub = lane >> 3, piece = lane & 7;
-        const uint32_t even = wq * 2048 + sub * 128 + ((piece ^ sub) << 4), odd = even ^ 64u;   // keys 4 k + sub by k
+        const uint32_t even = wq * kWarpKeys * 128 + sub * 128 + ((piece ^ sub) << 4), odd = even ^ 64u;   // keys 4 k + sub by k
         const uint32_t ring = smem_u32(smem + kPlan.ring_off), sc_addr = smem_u32(scales);
-        const int none = static_cast<int>(p.num_slots), j = 16 * wq + (lane & 15);
+        const int j = kWarpKeys * wq + (lane & (kWarpKeys - 1));
         const uint32_t block_units = static_cast<uint32_t>(p.block_bytes / 128);
         uint32_t tb = 0;                              // the tile's buffer of scales and masks
         uint32_t sl = 0, ph = 1;                      // ring slot and the parity that frees it
@@ -491,54 +489,85 @@ __global__ void __launch_bounds__(threads_of(N), 1)
         while (ok && walk.next(w)) {
             if (p.block_table != nullptr && w.keys == 0 && lane == 0 && __ldg(p.seq_lens + w.row) != 0)
                 set_status(p.status, IDX_ERR_DEVICE_CHECK);
-            // Keys are looked up for two tiles at once, lanes 0-15 for the first.
-            // What names them is read two and four tiles ahead: a trip to memory
-            // takes longer than a tile, and a register that a load has yet to
-            // fill cannot be moved either.
-            const int two = lane >> 4;
-            auto entry_of = [&](int t) { return t < w.t1 ? key_entry(p, w.row, w.keys, t * kKeys + j) : int64_t(-1); };
-            int64_t entry = entry_of(w.t0 + two), next = entry_of(w.t0 + 2 + two);
-            // the queries are written behind the copies of the second tile
-            const int split_at = min(w.t0 + 1, w.t1 - 1);
-            for (int t0 = w.t0; ok && t0 < w.t1; t0 += 2) {
-                const int slot = t0 + two < w.t1 ? key_slot(p, w.keys, (t0 + two) * kKeys + j, entry) : none;
+            // Keys are looked up for a whole warp's lanes, of two tiles at once where
+            // it has 16 keys of one.  What names them is read one and two of these
+            // steps ahead: a trip to memory takes longer than a tile, and a
+            // register that a load has yet to fill cannot be moved either.
+            constexpr int kPer = 32 / kWarpKeys;
+            const int two = kPer == 2 ? lane >> 4 : 0;
+            // (the entry of the slot list, or of the block table)
+            auto entry_of = [&](int t) {
+                const int key = t * kKeys + j;
+                if (t >= w.t1 || key >= w.keys) return int64_t(-1);
+                return p.block_table == nullptr
+                           ? __ldg(p.slots + w.row * p.slots_stride + key)
+                           : static_cast<int64_t>(__ldg(p.block_table + w.row * p.mbps + block_of(p, key)));
+            };
+            int64_t entry = entry_of(w.t0 + two), next = entry_of(w.t0 + kPer + two);
+            // the queries are written behind the copies of the second tile, or of
+            // the first where the ring does not hold two: its slots come free by
+            // products with these queries
+            const int split_at = kSlots >= 2 * kTileChunks ? min(w.t0 + 1, w.t1 - 1) : w.t0;
+            for (int t0 = w.t0; ok && t0 < w.t1; t0 += kPer) {
+                // block and place of this lane's key
+                const int key = (t0 + two) * kKeys + j;
+                const bool there = t0 + two < w.t1 && key < w.keys;
+                bool named = there && entry >= 0;
+                if (p.block_table == nullptr ? entry >= p.num_slots : there && (entry < 0 || entry >= p.num_blocks)) {
+                    if (there) set_status(p.status, IDX_ERR_DEVICE_CHECK);
+                    named = false;
+                }
+                const uint32_t what = named ? static_cast<uint32_t>(entry) : 0u;
+                uint32_t block = what, at = 0u;
+                if (p.block_table == nullptr) {
+                    block = block_of(p, what);
+                    at = what - block * p.block_size;
+                } else if (named) {
+                    at = key - block_of(p, key) * p.block_size;
+                }
                 entry = next;
-                next = entry_of(t0 + 4 + two);
-                const uint32_t both = __ballot_sync(~0u, slot != none);
+                next = entry_of(t0 + 2 * kPer + two);
+                const uint32_t both = __ballot_sync(~0u, named);
                 // a record begins a multiple of 128 bytes into the pool
-                const uint32_t own = slot == none ? 0u : static_cast<uint32_t>(slot);
-                const uint32_t block = own / static_cast<uint32_t>(p.block_size), at = own - block * p.block_size;
                 const uint32_t unit = block * block_units + at * (kQRow / 128);
                 const uint8_t* sc = p.pool + block * p.block_bytes + static_cast<int64_t>(p.block_size) * kQRow + 4 * at;
 #pragma unroll 1
-                for (int i = 0; i < 2 && t0 + i < w.t1; ++i) {
-                    const uint32_t valid = (both >> (16 * i)) & 0xFFFFu;
-                    const uint8_t* src[4];
+                for (int i = 0; i < kPer && t0 + i < w.t1; ++i) {
+                    constexpr uint32_t kAll = kPer == 2 ? 0xFFFFu : ~0u;
+                    const uint32_t valid = (both >> (16 * i)) & kAll;
+                    const uint8_t* src[kWarpKeys / 4];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
+                    for (int k = 0; k < kWarpKeys / 4; ++k)
                         src[k] = p.pool + static_cast<int64_t>(__shfl_sync(~0u, unit, 16 * i + 4 * k + sub)) * 128 + 16 * piece;
-                    // the tile's slots, a lane each
-                    const bool wraps = sl + lane >= kSlots;
-                    ok = lane >= kTileChunks || wait(empty + (wraps ? sl + lane - kSlots : sl + lane), ph ^ wraps, p.status, abort_flag);
-                    if (!(ok = __all_sync(~0u, ok))) break;
-                    // the position parts first: they are freed first
-                    int c = 4 * 128;
-#pragma unroll 1
-                    for (int m = 0; m < kTileChunks; ++m) {
-                        const uint32_t dst = ring + sl * kChunk;
-                        if (valid == 0xFFFFu) {
+                    // The position parts first, as they are freed first.  A wait that
+                    // ran out ends the loop below; copies may then meet products, but
+                    // the call has failed.
+                    if (valid == kAll) {
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) copy16(dst + ((k & 1) ? odd : even) + 512 * k, src[k] + c);
-                        } else {
+                        for (int m = 0; m < kTileChunks; ++m) {
+                            ok = wait(empty + sl, ph, p.status, abort_flag) && ok;
+                            const uint32_t dst = ring + sl * kChunk;
 #pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                copy16_or_zero(dst + ((k & 1) ? odd : even) + 512 * k, src[k] + c, (valid >> (4 * k + sub)) & 1 ? 16 : 0);
+                            for (int k = 0; k < kWarpKeys / 4; ++k)
+                                copy16(dst + ((k & 1) ? odd : even) + 512 * k, src[k] + 128 * (m == 0 ? 4 : m - 1));
+                            if (++sl == kSlots) sl = 0, ph ^= 1;
                         }
-                        c = m * 128;
-                        if (++sl == kSlots) sl = 0, ph ^= 1;
+                    } else {
+                        int c = 4 * 128;
+#pragma unroll 1
+                        for (int m = 0; m < kTileChunks; ++m) {
+                            ok = wait(empty + sl, ph, p.status, abort_flag) && ok;
+                            const uint32_t dst = ring + sl * kChunk;
+#pragma unroll
+                            for (int k = 0; k < kWarpKeys / 4; ++k)
+                                copy16_or_zero(dst + ((k & 1) ? odd : even) + 512 * k, src[k] + c, (valid >> (4 * k + sub)) & 1 ? 16 : 0);
+                            c = m * 128;
+                            if (++sl == kSlots) sl = 0, ph ^= 1;
+                        }
                     }
-                    if (two == i) copy4_or_zero(sc_addr + (tb * kKeys + j) * 4, sc, slot == none ? 0 : 4);
-                    if (lane == 0) masks[4 * tb + wq] = static_cast<uint16_t>(valid);
+                    if (!(ok = __all_sync(~0u, ok))) break;
+                    if (two == i) copy4_or_zero(sc_addr + (tb * kKeys + j) * 4, sc, named ? 4 : 0);
+                    if (lane == 0) masks[4 * tb + wq] = valid;
                     copy_arrive(full + tb);
                     if (lane == 0) mbar_arrive(full + tb);
                     if (++tb == kTiles) tb = 0;
@@ -582,7 +611,7 @@ __global__ void __launch_bounds__(threads_of(N), 1)
     } else if (warp == 0) {
         // ---- score products ----
         if (elect_one()) {
-            constexpr uint32_t kIdS = idesc_make(true, 64, 2 * N), kIdP = idesc_bf16(64, 2 * N, false, false);
+            constexpr uint32_t kIdS = idesc_make(true, kKeys, 2 * N), kIdP = idesc_bf16(kKeys, 2 * N, false, false);
             const uint32_t q_addr = smem_u32(smem), ring = smem_u32(smem + kPlan.ring_off);
             uint32_t it = 0, item = 0, tb = 0, ph = 0, sl = 0;
             bool ok = true;
@@ -640,7 +669,7 @@ __global__ void __launch_bounds__(threads_of(N), 1)
 #pragma unroll 1
                     for (int m = 0; m < 4; ++m) {
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) {
+                        for (int k = 0; k < kKeys / 32; ++k) {
                             const uint64_t a = sdesc_mn_sw128(ring + sl * kChunk + 4096 * k, kChunk);
                             const uint32_t more = (t != w.t0 || k != 0) ? 1u : 0u;
                             if (kWide) {
@@ -668,8 +697,8 @@ __global__ void __launch_bounds__(threads_of(N), 1)
         const int sw = warp & 3, half = warp >> 3;      // lane quadrant; which half (one: all) of the heads
         const int tid = 128 * half + (threadIdx.x & 127);
         const uint32_t lanes = static_cast<uint32_t>(32 * sw) << 16;
-        const int key = 16 * sw + (lane & 15);
-        const int hw = half * (N / kHalves), hb = hw + (lane >> 4) * kH;     // this warp's and this thread's first head
+        const int own = lane & (kWarpKeys - 1), key = kWarpKeys * sw + own;
+        const int hw = half * (N / kHalves), hb = hw + (kWide ? lane >> 4 : 0) * kH;     // this warp's and this thread's first head
         uint32_t it = 0, item = 0, tb = 0, ph = 0;
         bool ok = true;
         if (sh_run[0] < sh_run[1]) {
@@ -696,15 +725,21 @@ __global__ void __launch_bounds__(threads_of(N), 1)
                 tc_fence_after();
                 if (t == w.t0) mbar_arrive(q_full);      // this role has no part in the next row's queries
                 uint32_t raw[kH], low[kH];
-                tmem_ld_halves(tmem + lanes + kSCol + (it & 1) * 2 * N + hw, raw);
-                tmem_ld_halves(tmem + lanes + kSCol + (it & 1) * 2 * N + N + hw, low);
+                const uint32_t scores = tmem + lanes + kSCol + (it & 1) * 2 * N + hw;
+                if constexpr (kWide) {
+                    tmem_ld_halves(scores, raw);
+                    tmem_ld_halves(scores + N, low);
+                } else {
+                    tmem_ld16_nowait(scores, raw);
+                    tmem_ld16_nowait(scores + N, low);
+                }
                 // (long complete; it is what makes the copied scales visible here)
                 ok = ok && wait(full + tb, ph, p.status, abort_flag);
-                const bool valid = (masks[4 * tb + sw] >> (lane & 15)) & 1;
+                const bool valid = (masks[4 * tb + sw] >> own) & 1;
                 const float scale = scales[tb * kKeys + key];
                 f2 dot[kH / 2];
-                tmem_wait_halves(raw);
-                tmem_wait_halves(low);
+                tmem_wait_ld16(raw);
+                tmem_wait_ld16(low);
                 tc_fence_before();
                 mbar_arrive(s_empty + (it & 1));
 #pragma unroll
@@ -741,7 +776,7 @@ __global__ void __launch_bounds__(threads_of(N), 1)
                     // largest weights times scales, as log2, over this warp's 16
                     // keys, then over the four warps
                     float s = valid ? scale : 0.0f;
-                    for (int d = 8; d > 0; d >>= 1) s = fmaxf(s, __shfl_xor_sync(~0u, s, d));
+                    for (int d = kWarpKeys / 2; d > 0; d >>= 1) s = fmaxf(s, __shfl_xor_sync(~0u, s, d));
                     if (half == 0 && lane == 0) stat[5 * N + sw] = s;
                     // (the unit's log2 is taken off below; scales below 2^-32, which
                     // the format does not have, count as that)
@@ -754,10 +789,10 @@ __global__ void __launch_bounds__(threads_of(N), 1)
                         const float2 x = f2_unpack(f2_fma(dot[i], f2_mul(reinterpret_cast<const f2*>(factor)[i], scale2), shift2));
                         v[i] = valid ? f16x2(x.x, x.y) : 0xFC00FC00u;
                     }
-                    const uint32_t most = over_keys(v, [](uint32_t a, uint32_t b) { return max_f16x2(a, b); });
-                    if ((lane & 15) < kH / 2) {
+                    const uint32_t most = over_keys<kWarpKeys>(v, [](uint32_t a, uint32_t b) { return max_f16x2(a, b); });
+                    if (own < kH / 2) {
                         const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&most));
-                        *reinterpret_cast<float2*>(stat + sw * N + hb + 2 * (lane & (kH / 2 - 1))) = x;
+                        *reinterpret_cast<float2*>(stat + sw * N + hb + 2 * own) = x;
                     }
                     // a wait that ran out in any thread ends the loop in all
                     if (named_any<1, kSoftThreads>(!ok)) { ok = false; break; }
@@ -787,8 +822,8 @@ __global__ void __launch_bounds__(threads_of(N), 1)
                         factor_of[k] = exp2_fast(old - ref[k]);
                         which[k] = __ballot_sync(~0u, factor_of[k] != 1.0f && (N == 64 || (k == 0 && lane < N)));
                     }
-                    // a half warp's heads begin at lane hb & 31 of one of the two
-                    const float of = half == 1 ? ref[1] : ref[0], f = (half == 1 ? factor_of[1] : factor_of[0]) * more;
+                    // a thread's heads begin at lane hb & 31 of one of the two
+                    const float of = hb >= 32 ? ref[1] : ref[0], f = (hb >= 32 ? factor_of[1] : factor_of[0]) * more;
 #pragma unroll
                     for (int i = 0; i < kH / 2; ++i) {
                         const int l = (hb & 31) + 2 * i;
@@ -852,8 +887,8 @@ __global__ void __launch_bounds__(threads_of(N), 1)
                         *reinterpret_cast<uint4*>(pt + key * 128 + (((2 * k + (hb >> 4)) ^ (key & 7)) << 4)) =
                             *reinterpret_cast<const uint4*>(part[k]);
                     } else {
-                        *reinterpret_cast<uint2*>(pt + key * 64 + ((k ^ ((key >> 1) & 3)) << 4) + hb) =
-                            *reinterpret_cast<const uint2*>(part[k]);
+                        *reinterpret_cast<uint4*>(pt + key * 64 + ((k ^ ((key >> 1) & 3)) << 4)) =
+                            *reinterpret_cast<const uint4*>(part[k]);
                     }
                 }
                 fence_proxy_async_smem();
@@ -870,8 +905,8 @@ __global__ void __launch_bounds__(threads_of(N), 1)
                 float v[kH];
 #pragma unroll
                 for (int i = 0; i < kH; ++i) v[i] = i & 1 ? f2_unpack(sum[i / 2]).y : f2_unpack(sum[i / 2]).x;
-                const float all = over_keys(v, [](float a, float b) { return a + b; });
-                if ((lane & 15) < kH) stat[sw * N + hb + (lane & 15)] = all;
+                const float all = over_keys<kWarpKeys>(v, [](float a, float b) { return a + b; });
+                if (own < kH) stat[sw * N + hb + own] = all;
                 if (tid < 32) {
                     if (lane < N) stat[4 * N + lane] = ref[0];
                     if (N == 64) stat[4 * N + 32 + lane] = ref[1];
@@ -1056,6 +1091,7 @@ Shape shape_n(int64_t rows, int heads, int N, int64_t max_keys, bool paged, int6
     s.hgs = (heads + N - 1) / N;
     s.cluster = 1;
     const int64_t g = kMaxCtas;
+    const int kKeys = keys_of(N);
     const int64_t items = rows * s.hgs, nt = max_keys > 0 ? (max_keys + kKeys - 1) / kKeys : 1;
     int64_t best = (items + g - 1) / g * nt;
     s.ctas = static_cast<int>(items < g ? items : g);
@@ -1076,7 +1112,7 @@ Shape shape_n(int64_t rows, int heads, int N, int64_t max_keys, bool paged, int6
         const int64_t n = (items * nt + kMinRun - 1) / kMinRun;
         s.ctas = static_cast<int>(n < g ? n : g);
     }
-    *cost = best * (N == 64 ? 20 : N == 32 ? 13 : 10);
+    *cost = best * (N == 64 ? 20 : N == 32 ? 22 : 17);
     return s;
 }
 
@@ -1118,7 +1154,7 @@ cudaError_t launch_n(const QParams& p, const CUtensorMap& ql, const CUtensorMap&
     e = cudaLaunchKernelEx(&cfg, qattend_kernel<N, kCl>, ql, qp, p);
     kt_mark(st);
     if (e != cudaSuccess || p.split != 1) return e;
-    return launch_join(p, N, ctas, st);
+    return launch_join<keys_of(N)>(p, N, ctas, st);
 }
 
 template <int N>
@@ -1155,6 +1191,14 @@ cudaError_t launch_qattend(const AttendArgs& a, int64_t block_bytes, cudaStream_
     p.part_o = static_cast<float*>(a.ws);
     p.part_ml = reinterpret_cast<float2*>(p.part_o + static_cast<size_t>(2) * s.ctas * s.N * IDX_LATENT_DIM);
     p.block_bytes = block_bytes;
+    p.num_blocks = a.num_slots / a.block_size;
+    // ceil(2^(31 + l) / d) with d <= 2^l: n times it is off from n 2^(31 + l) / d
+    // by less than n 2^l / d, which for n < 2^31 no quotient notices
+    int l = 0;
+    while ((1 << l) < a.block_size) ++l;
+    p.div_shift = 31 + l;
+    p.div_mul = static_cast<uint32_t>(((uint64_t(1) << p.div_shift) + a.block_size - 1) / a.block_size);
+    const int kKeys = keys_of(s.N);
     const int64_t tiles = a.max_keys > 0 ? (a.max_keys + kKeys - 1) / kKeys : 1;
     const int64_t run = s.split == 1 ? std::min(tiles, (a.rows * s.hgs * tiles + s.ctas - 1) / s.ctas) : (tiles + s.cluster - 1) / s.cluster;
     p.room = room_of(run * kKeys);
