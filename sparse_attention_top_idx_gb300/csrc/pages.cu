@@ -1,13 +1,16 @@
 // pages.cu -- idx_pages_*: counts, block tables and contents of the pages that
 // the paged caches share (declared in include/dsaidx_pages.h).
 //
-// Fork and extend are two kernels.  take_kernel lists the free pages in the
-// order of their ids (one cluster: each CTA counts its share of the counts,
-// the shares are added up through distributed shared memory, then each lists
-// its own) and, beside it, how many pages the rows before each row need.  The
-// second kernel reads both: row i's pages are entries [before_i, before_i +
+// take_kernel lists the free pages in the order of their ids (one cluster: each
+// CTA counts its share of the counts, the CTAs' sums meet through distributed
+// shared memory, then each lists its own) and, beside them, how many pages the
+// rows before each row need.  Row i's pages are entries [before_i, before_i +
 // need_i) of the list, so that who gets what depends on nothing but the counts
-// and the rows.  Compaction ranks pages in the same way.
+// and the rows.  The same kernel writes the rows where they are few enough for
+// eight CTAs, else a second one does.  Compaction ranks pages in the same way.
+//
+// All of these are short chains of trips to L2 and cluster barriers (6 to 9 us
+// a kernel alone, about 4 behind others); the contents' copy is bound by memory.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -23,6 +26,9 @@ constexpr int kScanCtas = 8;          // CTAs of the cluster that looks the coun
 constexpr int kScanThreads = 1024;
 constexpr int kScanWarps = kScanThreads / 32;
 constexpr int kRowThreads = 256;      // table kernels: columns a CTA
+// Table entries that the cluster's eight CTAs write themselves: at eight a
+// thread that takes as long as another kernel's start.
+constexpr int64_t kFewCells = 8 * kScanCtas * kScanThreads;
 constexpr int kCopyThreads = 256;
 constexpr int kCopyVecs = 4;          // 16-byte vectors a thread has in flight
 constexpr int kSlice = kCopyThreads * kCopyVecs * 16;
@@ -51,6 +57,7 @@ struct Rows {
     int32_t* status;
     int num_blocks, block_size, old_rows, mbps, rows, new_mbps;
     int cap;                   // entries of the list that can be asked for
+    int finish;                // the rows are written behind the list, by the same kernel
     Taken taken;
 };
 
@@ -81,47 +88,53 @@ __device__ __forceinline__ bool row_need(const Rows& a, int i, RowNeed& r) {
     return true;
 }
 
-// Sum over the block and, per thread, the sum of the threads before it.
-__device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total) {
-    const int lane = lane_id(), warp = warp_id();
-    int x = v;
+// Two sums at once, one in each half of 64 bits (neither passes 2^31).
+typedef unsigned long long u64;
+__device__ __forceinline__ u64 two(int a, int b) { return static_cast<u64>(static_cast<uint32_t>(b)) << 32 | static_cast<uint32_t>(a); }
+__device__ __forceinline__ int first_of(u64 v) { return static_cast<int>(static_cast<uint32_t>(v)); }
+__device__ __forceinline__ int second_of(u64 v) { return static_cast<int>(v >> 32); }
+
+// Shared memory of the scans: the warps' sums, and the CTAs' by scan.
+struct ScanMemory {
+    u64 warps[32];
+    u64 ctas[2][kScanCtas];
+};
+// Sum of v over the threads before this one in the cluster; *total over all.
+// One cluster barrier: every CTA writes its sum into the others' memory first.
+// `scan` is 0 for a kernel's first call, 1 for its second.
+__device__ __forceinline__ u64 cluster_before(u64 v, int scan, ScanMemory& m, u64* total) {
+    const int lane = lane_id(), warp = warp_id(), rank = static_cast<int>(cluster_rank());
+    u64 x = v;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const int u = __shfl_up_sync(~0u, x, d);
+        const u64 u = __shfl_up_sync(~0u, x, d);
         if (lane >= d) x += u;
     }
     __syncthreads();       // the sums of a scan before are read
-    if (lane == 31) warp_sums[warp] = x;
+    if (lane == 31) m.warps[warp] = x;
     __syncthreads();
-    int w = warp_sums[lane & (kScanWarps - 1)];
+    u64 w = m.warps[lane];
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const int u = __shfl_up_sync(~0u, w, d);
+        const u64 u = __shfl_up_sync(~0u, w, d);
         if (lane >= d) w += u;
     }
-    total = __shfl_sync(~0u, w, 31);
-    const int before = __shfl_sync(~0u, w, warp > 0 ? warp - 1 : 0);
-    return x - v + (warp > 0 ? before : 0);
-}
-
-// Sum of `mine` over the CTAs of the cluster before this one, and over all.
-__device__ __forceinline__ int cluster_scan(int mine, int* slot, int& total) {
-    __syncthreads();
-    if (threadIdx.x == 0) *slot = mine;
+    const u64 cta = __shfl_sync(~0u, w, 31);
+    u64 before = x - v;
+    const u64 warps = __shfl_sync(~0u, w, warp > 0 ? warp - 1 : 0);
+    if (warp > 0) before += warps;
+    if (scan == 0) cluster_wait();     // all of them have started (their kernels arrive first of all)
+    if (threadIdx.x < kScanCtas) dsmem_st_u64(dsmem_addr(&m.ctas[scan][rank], threadIdx.x), cta);
     cluster_arrive();
     cluster_wait();
-    const int rank = static_cast<int>(cluster_rank());
-    int before = 0;
-    total = 0;
+    u64 all = 0;
 #pragma unroll
     for (int r = 0; r < kScanCtas; ++r) {
-        const int v = static_cast<int>(dsmem_ld_u32(dsmem_addr(slot, r)));
-        if (r < rank) before += v;
-        total += v;
+        const u64 c = m.ctas[scan][r];
+        if (r < rank) before += c;
+        all += c;
     }
-    // read by all before anyone writes it again or leaves
-    cluster_arrive();
-    cluster_wait();
+    *total = all;
     return before;
 }
 
@@ -156,44 +169,103 @@ __device__ __forceinline__ int warp_before(int v, int& total) {
     return x - v;
 }
 
-__global__ void __launch_bounds__(kScanThreads, 1) take_kernel(const Rows a) {
-    __shared__ int warp_sums[32];
-    __shared__ int slot;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (blockIdx.x >= kScanCtas) {
-        // the other cluster: what the rows before each row need
-        if (blockIdx.x > kScanCtas) return;
-        int before = 0;
-        for (int i0 = 0; i0 < a.rows; i0 += kScanThreads) {
-            const int i = i0 + threadIdx.x;
-            RowNeed r{0, 0, 0, 0};
-            if (i < a.rows && !row_need(a, i, r)) r.need = 0;
-            int total;
-            const int at = block_scan(r.need, warp_sums, total);
-            // no more than the pool has are ever given, so sums stop there
-            if (i < a.rows) a.taken.before[i] = before + at;
-            before = min(before + total, a.num_blocks + 1);
+__device__ __forceinline__ int free_in(const int4& v) { return (v.x == 0) + (v.y == 0) + (v.z == 0) + (v.w == 0); }
+
+// Columns j0 + step k < end, k < kCols, of a forked row, whose loads are in
+// flight together; the thread with column 0 writes what the row is.
+constexpr int kCols = 4;
+__device__ __forceinline__ void fork_cols(const Rows& a, int i, int before, int found, int j0, int step, int end) {
+    RowNeed r;
+    bool ok = row_need(a, i, r);
+    if (ok && r.need > 0) ok = before < found;
+    if (!ok) r.length = r.need = 0;
+    const int full = r.length / a.block_size;
+    const int32_t* old = a.table + static_cast<int64_t>(r.length > 0 ? r.parent : 0) * a.mbps;
+    int32_t* row = a.new_table + static_cast<int64_t>(i) * a.new_mbps;
+    const int fresh = r.need > 0 ? __ldcg(a.taken.list + before) : -1;
+    int page[kCols];
+#pragma unroll
+    for (int k = 0; k < kCols; ++k) page[k] = j0 + k * step < min(full, end) ? old[j0 + k * step] : -1;
+    const int from = j0 == 0 && r.need > 0 ? old[full] : -1;
+#pragma unroll
+    for (int k = 0; k < kCols; ++k) {
+        const int j = j0 + k * step;
+        if (j >= end) break;
+        int v = page[k];
+        if (j < full) {
+            if (v < 0 || v >= a.num_blocks) {
+                set_status(a.status, IDX_ERR_DEVICE_CHECK);
+                v = -1;
+            } else {
+                atomicAdd(a.refs + v, 1);
+            }
+        } else if (j == full && r.need > 0) {
+            v = fresh;
+            a.refs[v] = 1;
         }
+        row[j] = v;
+    }
+    if (j0 == 0) {
+        const bool there = r.need > 0 && from >= 0 && from < a.num_blocks;
+        if (!ok || (r.need > 0 && !there)) set_status(a.status, IDX_ERR_DEVICE_CHECK);
+        a.new_lens[i] = r.length;
+        a.pairs[2 * i] = there ? from : -1;
+        a.pairs[2 * i + 1] = there ? fresh : -1;
+    }
+}
+
+// A whole warp.
+__device__ __forceinline__ void extend_row(const Rows& a, int i, int before, int found) {
+    const int lane = lane_id();
+    RowNeed r;
+    bool ok = row_need(a, i, r);
+    if (ok && r.need > 0) ok = before + r.need <= found;
+    if (!ok) {
+        if (lane == 0) set_status(a.status, IDX_ERR_DEVICE_CHECK);
         return;
     }
-    const Share s = share_of(a.num_blocks);
-    const int lane = lane_id();
-    int mine = 0;
-    for (int k = 0; k < s.steps; ++k) {
-        const int4 v = counts_at(a.refs, a.num_blocks, s.first + 128 * k + 4 * lane);
-        mine += (v.x == 0) + (v.y == 0) + (v.z == 0) + (v.w == 0);
+    int32_t* row = a.new_table + static_cast<int64_t>(i) * a.mbps + pages_of(r.length, a.block_size);
+    for (int j = lane; j < r.need; j += 32) {
+        const int page = __ldcg(a.taken.list + before + j);
+        row[j] = page;
+        a.refs[page] = 1;
     }
-    int in_cta, found, in_warp;
-    const int at_thread = block_scan(mine, warp_sums, in_cta);
-    const int at_cta = cluster_scan(in_cta, &slot, found);
-    int at = at_cta + __shfl_sync(~0u, at_thread, 0);
-    if (blockIdx.x == 0 && threadIdx.x == 0) *a.taken.found = found;
+    __syncwarp();          // every lane has read the length
+    if (lane == 0) a.new_lens[i] = r.after;
+}
+
+__global__ void __launch_bounds__(kScanThreads, 1) take_kernel(const Rows a) {
+    __shared__ ScanMemory m;
+    cluster_arrive_relaxed();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const Share s = share_of(a.num_blocks);
+    const int lane = lane_id(), thread = static_cast<int>(cluster_rank()) * kScanThreads + threadIdx.x;
+    // a thread's rows, one after the other
+    const int per = (a.rows + kScanCtas * kScanThreads - 1) / (kScanCtas * kScanThreads);
+    const int r0 = min(thread * per, a.rows), r1 = min(r0 + per, a.rows);
+    RowNeed r{0, 0, 0, 0};
+    int free = 0, need = 0;
+    for (int i = r0; i < r1; ++i) {
+        if (row_need(a, i, r)) need += r.need;
+    }
+#pragma unroll 4
+    for (int k = 0; k < s.steps; ++k) free += free_in(counts_at(a.refs, a.num_blocks, s.first + 128 * k + 4 * lane));
+    u64 all;
+    const u64 before = cluster_before(two(free, need), 0, m, &all);
+    const int found = first_of(all);
+    if (thread == 0) *a.taken.found = found;
+    int at_row = second_of(before);
+    for (int i = r0; i < r1; ++i) {
+        a.taken.before[i] = at_row;
+        if (row_need(a, i, r)) at_row += r.need;
+    }
+    int at = __shfl_sync(~0u, first_of(before), 0), in_warp;
+#pragma unroll 2
     for (int k = 0; k < s.steps && at < a.cap; ++k) {
         const int p = s.first + 128 * k + 4 * lane;
         const int4 v = counts_at(a.refs, a.num_blocks, p);
-        const int c = (v.x == 0) + (v.y == 0) + (v.z == 0) + (v.w == 0);
-        int to = at + warp_before(c, in_warp);
+        int to = at + warp_before(free_in(v), in_warp);
         if (v.x == 0 && to < a.cap) a.taken.list[to] = p;
         to += v.x == 0;
         if (v.y == 0 && to < a.cap) a.taken.list[to] = p + 1;
@@ -203,77 +275,28 @@ __global__ void __launch_bounds__(kScanThreads, 1) take_kernel(const Rows a) {
         if (v.w == 0 && to < a.cap) a.taken.list[to] = p + 3;
         at += in_warp;
     }
-}
-
-// Row blockIdx.x, columns [blockIdx.y * kRowThreads, ...) and every
-// gridDim.y-th such piece.
-__global__ void __launch_bounds__(kRowThreads) fork_kernel(const Rows a) {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int i = blockIdx.x;
-    RowNeed r;
-    bool ok = row_need(a, i, r);
-    const int before = a.taken.before[i];
-    if (ok && r.need > 0) ok = before < *a.taken.found;
-    if (!ok) r.length = r.need = 0;
-    const int full = r.length / a.block_size;
-    const int32_t* old = a.table + static_cast<int64_t>(r.length > 0 ? r.parent : 0) * a.mbps;
-    int32_t* row = a.new_table + static_cast<int64_t>(i) * a.new_mbps;
-    for (int j = blockIdx.y * kRowThreads + threadIdx.x; j < a.new_mbps; j += gridDim.y * kRowThreads) {
-        int page = -1;
-        if (j < full) {
-            page = old[j];
-            if (page < 0 || page >= a.num_blocks) {
-                set_status(a.status, IDX_ERR_DEVICE_CHECK);
-                page = -1;
-            } else {
-                atomicAdd(a.refs + page, 1);
-            }
-        } else if (j == full && r.need > 0) {
-            page = a.taken.list[before];
-            a.refs[page] = 1;
-        }
-        row[j] = page;
-    }
-    if (blockIdx.y == 0 && threadIdx.x == 0) {
-        if (!ok) set_status(a.status, IDX_ERR_DEVICE_CHECK);
-        a.new_lens[i] = r.length;
-        int from = -1, to = -1;
-        if (r.need > 0) {
-            from = old[full];
-            to = a.taken.list[before];
-            if (from < 0 || from >= a.num_blocks) {
-                set_status(a.status, IDX_ERR_DEVICE_CHECK);
-                from = to = -1;
-            }
-        }
-        a.pairs[2 * i] = from;
-        a.pairs[2 * i + 1] = to;
+    if (!a.finish) return;
+    // the list and the sums of the rows are complete
+    cluster_arrive();
+    cluster_wait();
+    // a warp a row, or a piece of a forked one
+    const int pieces = a.longer == nullptr ? (a.new_mbps + 32 * kCols - 1) / (32 * kCols) : 1;
+    for (int x = thread >> 5; x < a.rows * pieces; x += kScanCtas * kScanWarps) {
+        const int i = x / pieces, first = (x - i * pieces) * 32 * kCols;
+        const int b = __ldcg(a.taken.before + i);
+        if (a.longer == nullptr)
+            fork_cols(a, i, b, found, first + lane, 32, a.new_mbps);
+        else
+            extend_row(a, i, b, found);
     }
 }
 
-// A warp a row.
-__global__ void __launch_bounds__(kRowThreads) extend_kernel(const Rows a) {
+// A piece of kCols * kRowThreads columns of a row a CTA.
+__global__ void __launch_bounds__(kRowThreads) fork_kernel(const Rows a, int pieces) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int i = blockIdx.x * (kRowThreads / 32) + warp_id(), lane = lane_id();
-    if (i >= a.rows) return;
-    RowNeed r;
-    bool ok = row_need(a, i, r);
-    const int before = a.taken.before[i];
-    if (ok && r.need > 0) ok = before + r.need <= *a.taken.found;
-    if (!ok) {
-        if (lane == 0) set_status(a.status, IDX_ERR_DEVICE_CHECK);
-        return;
-    }
-    int32_t* row = a.new_table + static_cast<int64_t>(i) * a.mbps + pages_of(r.length, a.block_size);
-    for (int j = lane; j < r.need; j += 32) {
-        const int page = a.taken.list[before + j];
-        row[j] = page;
-        a.refs[page] = 1;
-    }
-    __syncwarp();          // every lane has read the length
-    if (lane == 0) a.new_lens[i] = r.after;
+    const int i = blockIdx.x / pieces, first = (blockIdx.x - i * pieces) * kCols * kRowThreads;
+    fork_cols(a, i, a.taken.before[i], *a.taken.found, first + threadIdx.x, kRowThreads, a.new_mbps);
 }
 
 struct FreeArgs {
@@ -318,102 +341,115 @@ struct CompactArgs {
     int2* pairs;
     int32_t* count;
     int32_t* status;
-    int num_blocks;
+    int num_blocks, finish;
     int64_t cells;
 };
+
+__device__ __forceinline__ void remap(const CompactArgs& a, int64_t i) {
+    int page = a.table[i];
+    if (page >= 0) {
+        page = page < a.num_blocks ? __ldcg(a.map + page) : -1;
+        if (page < 0) set_status(a.status, IDX_ERR_DEVICE_CHECK);
+    } else {
+        page = -1;
+    }
+    a.new_table[i] = page;
+}
 
 // One cluster.  Pages in use are counted (n); then those from n on and the
 // free ones below n are ranked, each list in the order of the ids.
 __global__ void __launch_bounds__(kScanThreads, 1) compact_kernel(const CompactArgs a) {
-    __shared__ int warp_sums[32];
-    __shared__ int slot;
+    __shared__ ScanMemory m;
+    cluster_arrive_relaxed();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const Share s = share_of(a.num_blocks);
-    const int lane = lane_id();
-    int mine = 0, in_cta, n, moves, holes, in_warp;
+    const int lane = lane_id(), thread = static_cast<int>(cluster_rank()) * kScanThreads + threadIdx.x;
+    int used = 0;
+#pragma unroll 4
     for (int k = 0; k < s.steps; ++k) {
         const int4 v = counts_at(a.refs, a.num_blocks, s.first + 128 * k + 4 * lane);
-        mine += (v.x > 0) + (v.y > 0) + (v.z > 0) + (v.w > 0);
+        used += (v.x > 0) + (v.y > 0) + (v.z > 0) + (v.w > 0);
     }
-    block_scan(mine, warp_sums, in_cta);
-    cluster_scan(in_cta, &slot, n);
-    int from = 0, to = 0;
-    for (int k = 0; k < s.steps; ++k) {
-        const int p = s.first + 128 * k + 4 * lane;
-        const int4 v = counts_at(a.refs, a.num_blocks, p);
+    u64 all;
+    cluster_before(two(used, 0), 0, m, &all);
+    const int n = first_of(all);
+    // of a lane's four pages: those that move away, and the free ones to move to
+    auto from_to = [&](const int4& v, int p) {
         const int c[4] = {v.x, v.y, v.z, v.w};
+        int from = 0, to = 0;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             from += c[e] > 0 && p + e >= n;
             to += c[e] <= 0 && p + e < n;
         }
+        return two(from, to);
+    };
+    u64 mine = 0;
+#pragma unroll 4
+    for (int k = 0; k < s.steps; ++k) {
+        const int p = s.first + 128 * k + 4 * lane;
+        mine += from_to(counts_at(a.refs, a.num_blocks, p), p);
     }
-    int at_from = __shfl_sync(~0u, block_scan(from, warp_sums, in_cta), 0);
-    at_from += cluster_scan(in_cta, &slot, moves);
-    int at_to = __shfl_sync(~0u, block_scan(to, warp_sums, in_cta), 0);
-    at_to += cluster_scan(in_cta, &slot, holes);       // as many
-    if (blockIdx.x == 0 && threadIdx.x == 0) *a.count = moves;
+    u64 at = __shfl_sync(~0u, cluster_before(mine, 1, m, &all), 0);
+    const int moves = first_of(all);       // as many holes
+    if (thread == 0) *a.count = moves;
+#pragma unroll 1
     for (int k = 0; k < s.steps; ++k) {
         const int p = s.first + 128 * k + 4 * lane;
         const int4 v = counts_at(a.refs, a.num_blocks, p);
         const int c[4] = {v.x, v.y, v.z, v.w};
-        int cf = 0, ct = 0;
+        const u64 here = from_to(v, p);
+        u64 x = here;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            cf += c[e] > 0 && p + e >= n;
-            ct += c[e] <= 0 && p + e < n;
+        for (int d = 1; d < 32; d <<= 1) {
+            const u64 u = __shfl_up_sync(~0u, x, d);
+            if (lane >= d) x += u;
         }
-        int f = at_from + warp_before(cf, in_warp);
-        at_from += in_warp;
-        int t = at_to + warp_before(ct, in_warp);
-        at_to += in_warp;
+        int f = first_of(at + x - here), t = second_of(at + x - here);
+        at += __shfl_sync(~0u, x, 31);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             if (p + e >= a.num_blocks) continue;
-            const bool used = c[e] > 0;
-            if (p + e >= n && used) {
+            const bool held = c[e] > 0;
+            if (p + e >= n && held) {
                 a.pairs[f++].x = p + e;                // its count moves below
                 continue;
             }
-            a.map[p + e] = used ? p + e : -1;
-            if (p + e < n && !used) {
+            a.map[p + e] = held ? p + e : -1;
+            if (p + e < n && !held) {
                 a.pairs[t++].y = p + e;
                 continue;
             }
-            a.new_refs[p + e] = used ? c[e] : 0;
+            a.new_refs[p + e] = held ? c[e] : 0;
         }
     }
     // the cluster's lists are complete
     cluster_arrive();
     cluster_wait();
-    for (int k = blockIdx.x * kScanThreads + threadIdx.x; k < a.num_blocks / 2; k += kScanCtas * kScanThreads) {
+    for (int k = thread; k < a.num_blocks / 2; k += kScanCtas * kScanThreads) {
         if (k >= moves) {
             a.pairs[k] = make_int2(-1, -1);
             continue;
         }
         const int2 v = __ldcg(a.pairs + k);
-        const int held = a.refs[v.x];
+        const int held = __ldcg(a.refs + v.x);
         a.map[v.x] = v.y;
         a.new_refs[v.y] = held;
         a.new_refs[v.x] = 0;
     }
+    if (!a.finish) return;
+    cluster_arrive();
+    cluster_wait();
+    for (int64_t i = thread; i < a.cells; i += kScanCtas * kScanThreads) remap(a, i);
 }
 
 __global__ void __launch_bounds__(kRowThreads) remap_kernel(const CompactArgs a) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * kRowThreads + threadIdx.x; i < a.cells;
-         i += static_cast<int64_t>(gridDim.x) * kRowThreads) {
-        int page = a.table[i];
-        if (page >= 0) {
-            page = page < a.num_blocks ? a.map[page] : -1;
-            if (page < 0) set_status(a.status, IDX_ERR_DEVICE_CHECK);
-        } else {
-            page = -1;
-        }
-        a.new_table[i] = page;
-    }
+         i += static_cast<int64_t>(gridDim.x) * kRowThreads)
+        remap(a, i);
 }
 
 struct CopyArgs {
@@ -544,11 +580,14 @@ idx_status idx_pages_fork(int32_t* refs_dev, int64_t num_blocks, int block_size,
     const Rows a{refs_dev, table_dev, seq_lens_dev, parents_dev, nullptr, new_table_dev, new_lens_dev, pairs_dev,
                  static_cast<int32_t*>(workspace_dev), static_cast<int>(num_blocks), block_size, old_rows,
                  max_blocks_per_seq, rows, new_max_blocks_per_seq,
-                 static_cast<int>(rows < num_blocks ? rows : num_blocks), taken_of(workspace_dev, rows)};
+                 static_cast<int>(rows < num_blocks ? rows : num_blocks),
+                 int64_t(rows) * new_max_blocks_per_seq <= kFewCells, taken_of(workspace_dev, rows)};
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = launch(take_kernel, dim3(2 * kScanCtas), kScanThreads, kScanCtas, st, a);
-    if (e != cudaSuccess) return status_of(e);
-    return status_of(launch(fork_kernel, dim3(rows, row_pieces(rows, new_max_blocks_per_seq)), kRowThreads, 1, st, a));
+    const cudaError_t e = launch(take_kernel, dim3(kScanCtas), kScanThreads, kScanCtas, st, a);
+    if (e != cudaSuccess || a.finish) return status_of(e);
+    // rows * pieces < 2^21, as the table has at most IDX_PAGES_MAX_CELLS entries
+    const int pieces = (new_max_blocks_per_seq - 1) / (kCols * kRowThreads) + 1;
+    return status_of(launch(fork_kernel, dim3(static_cast<unsigned>(rows * pieces)), kRowThreads, 1, st, a, pieces));
 }
 
 idx_status idx_pages_extend(int32_t* refs_dev, int64_t num_blocks, int block_size, int32_t* table_dev, int rows,
@@ -568,11 +607,8 @@ idx_status idx_pages_extend(int32_t* refs_dev, int64_t num_blocks, int block_siz
     if (ws_bytes < workspace(num_blocks, rows)) return IDX_ERR_WORKSPACE_TOO_SMALL;
     const Rows a{refs_dev, table_dev, seq_lens_dev, nullptr, longer_dev, table_dev, seq_lens_dev, nullptr,
                  static_cast<int32_t*>(workspace_dev), static_cast<int>(num_blocks), block_size, rows,
-                 max_blocks_per_seq, rows, max_blocks_per_seq, static_cast<int>(num_blocks), taken_of(workspace_dev, rows)};
-    const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = launch(take_kernel, dim3(2 * kScanCtas), kScanThreads, kScanCtas, st, a);
-    if (e != cudaSuccess) return status_of(e);
-    return status_of(launch(extend_kernel, dim3((rows + kRowThreads / 32 - 1) / (kRowThreads / 32)), kRowThreads, 1, st, a));
+                 max_blocks_per_seq, rows, max_blocks_per_seq, static_cast<int>(num_blocks), 1, taken_of(workspace_dev, rows)};
+    return status_of(launch(take_kernel, dim3(kScanCtas), kScanThreads, kScanCtas, static_cast<cudaStream_t>(stream), a));
 }
 
 idx_status idx_pages_free(int32_t* refs_dev, int64_t num_blocks, int32_t* table_dev, int rows,
@@ -611,10 +647,10 @@ idx_status idx_pages_compact(const int32_t* refs_dev, int64_t num_blocks, const 
         }
     if (ws_bytes < kWsHeaderBytes) return IDX_ERR_WORKSPACE_TOO_SMALL;
     const CompactArgs a{refs_dev, table_dev, new_refs_dev, new_table_dev, map_dev, reinterpret_cast<int2*>(pairs_dev),
-                        count_dev, static_cast<int32_t*>(workspace_dev), static_cast<int>(num_blocks), cells};
+                        count_dev, static_cast<int32_t*>(workspace_dev), static_cast<int>(num_blocks), cells <= kFewCells, cells};
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const cudaError_t e = launch(compact_kernel, dim3(kScanCtas), kScanThreads, kScanCtas, st, a);
-    if (e != cudaSuccess || cells == 0) return status_of(e);
+    if (e != cudaSuccess || a.finish) return status_of(e);
     const int64_t grid = (cells + kRowThreads - 1) / kRowThreads;
     return status_of(launch(remap_kernel, dim3(static_cast<unsigned>(grid < 1216 ? grid : 1216)), kRowThreads, 1, st, a));
 }

@@ -1081,38 +1081,41 @@ float room_of(int64_t n) {
     return std::exp2(15.0f - g);
 }
 
-// What joining cut rows costs, in tiles.
-constexpr int kJoinTiles = 14;
-
-// Rows of N heads each over CTAs; *cost in ns.
+// How rows of N heads each are spread over CTAs, and what that takes in ns
+// beyond the launch.  Measured on calls of few tiles: a tile of 64 keys x 64
+// heads takes 1670, of 128 keys x 32 and 16 heads 2190 and 1720; a row's
+// beginning and end about 6000, 4000 and 2500; joining it over a cluster 2000
+// (64 heads 5000), through memory 9000 (13000).
 Shape shape_n(int64_t rows, int heads, int N, int64_t max_keys, bool paged, int64_t* cost) {
     Shape s{};
     s.N = N;
     s.hgs = (heads + N - 1) / N;
     s.cluster = 1;
-    const int64_t g = kMaxCtas;
     const int kKeys = keys_of(N);
+    const int64_t g = kMaxCtas, tile = N == 64 ? 1670 : N == 32 ? 2190 : 1720, ends = N == 64 ? 6000 : N == 32 ? 4000 : 2500;
     const int64_t items = rows * s.hgs, nt = max_keys > 0 ? (max_keys + kKeys - 1) / kKeys : 1;
-    int64_t best = (items + g - 1) / g * nt;
+    *cost = (items + g - 1) / g * (nt * tile + ends);
     s.ctas = static_cast<int>(items < g ? items : g);
+    // A cluster for a row while all fit at once (of eight: 64 CTAs).  A paged batch
+    // is ragged, which the cut evens out, so long contexts take no clusters.
     for (int c = 2; c <= 8; c *= 2) {
-        const int64_t cost = (nt + c - 1) / c + 1;
-        if (items * c <= (c == 8 ? 64 : c == 4 ? 128 : g) && c <= nt && cost < best && !(paged && nt > 16)) {
-            best = cost;
+        const int64_t t = (nt + c - 1) / c * tile + ends + (N == 64 ? 5000 : 2000);
+        if (items * c <= (c == 8 ? 64 : c == 4 ? 128 : g) && c <= nt && t < *cost && !(paged && max_keys > 1024)) {
+            *cost = t;
             s.split = 2;
             s.cluster = c;
             s.ctas = static_cast<int>(items) * c;
         }
     }
-    const int64_t cut = (items * nt + g - 1) / g + kJoinTiles;
-    if (cut < best) {
-        best = cut;
+    // (no row of ten tiles of 64 keys or fewer is cut: a workspace of such a call has no room)
+    const int64_t run = (items * nt + g - 1) / g, cut = run * tile + (run / nt + 2) * ends + (N == 64 ? 13000 : 9000);
+    if (cut < *cost && max_keys > 640) {
+        *cost = cut;
         s.split = 1;
         s.cluster = 1;
         const int64_t n = (items * nt + kMinRun - 1) / kMinRun;
         s.ctas = static_cast<int>(n < g ? n : g);
     }
-    *cost = best * (N == 64 ? 20 : N == 32 ? 22 : 17);
     return s;
 }
 
