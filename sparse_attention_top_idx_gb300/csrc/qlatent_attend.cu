@@ -10,8 +10,9 @@
 //   queries   a bf16 under a power of two of its head is the sum of two e4m3,
 //             the second times 16 (to 2^-22 of the head's largest);
 //   weights   9 significant bits are the sum of three e5m2, whose 32 binades
-//             hold weights down to 2^-24 of the largest (two e4m3 would hold 8
-//             bits down to 2^-9 of it and lose a long context's small weights).
+//             leave room for a running maximum to rise and for weights far below
+//             it (two e4m3 would hold 8 bits down to 2^-9 of the largest and
+//             lose a long context's small weights).
 // The parts are further columns of the same product, up to 32 heads: a step
 // of 64 keys x 32 columns takes 12.3 ns, of 64 columns 16.4, of 128 columns
 // 32.7; of 128 dimensions x 48, 64 and 96 columns 22.6, 24.7 and 28.7.  At 64
@@ -30,11 +31,9 @@
 //              codes of 64 keys, one of the position parts), and split the other
 //              half of a row's queries while its first tiles are on their way
 //
-// The running maximum of a head and the largest scale move only when a weight
-// times its scale is about to leave e5m2's range, 2^8 above them, so most tiles
-// need neither a maximum over keys nor a rescaled accumulator.  (Moving at 2^4
-// would hold weights down to 2^-28, and took 2.33 us a tile against 1.59 at 64
-// heads: nearly every tile moved some head's maximum.)
+// A head's reference, to which its weights are relative, moves only when a
+// weight times its scale is about to leave e5m2's range (room_of), so most tiles
+// need neither a maximum over keys nor a rescaled accumulator.
 // Statistics, sums and accumulators are fp32.  Rows are whole, shared by a
 // cluster or cut into equal runs as in latent_rows.cuh.
 #include <cuda_fp16.h>
@@ -350,14 +349,15 @@ __device__ __forceinline__ bool weigh(const f2 (&dot)[kH / 2], const float* fact
     return max(most & 0xFFFFu, most >> 16) > kMost16;
 }
 // The products as the sum of three e5m2 each: the three leading bits, the next
-// three significant ones and the rest rounded, 2^-9 of a product off at most.
+// three significant ones, and what is left rounded, up or down by `dither` (one
+// of 0..255 in each half): 2^-8 of a product off, or the smallest e5m2, 2^-16.
 template <int kH>
-__device__ __forceinline__ void in_parts(uint32_t (&r)[kH / 2], uint32_t (&part)[3][kH / 4]) {
+__device__ __forceinline__ void in_parts(uint32_t (&r)[kH / 2], uint32_t dither, uint32_t (&part)[3][kH / 4]) {
 #pragma unroll
     for (int i = 0; i < kH / 4; ++i) {
 #pragma unroll
         for (int k = 0; k < 3; ++k) {
-            const uint32_t a = k == 2 ? r[2 * i] + 0x00800080u : r[2 * i], b = k == 2 ? r[2 * i + 1] + 0x00800080u : r[2 * i + 1];
+            const uint32_t a = k == 2 ? r[2 * i] + dither : r[2 * i], b = k == 2 ? r[2 * i + 1] + dither : r[2 * i + 1];
             part[k][i] = __byte_perm(a, b, 0x7531);
             if (k == 2) break;
             r[2 * i] = sub_f16x2(r[2 * i], a & kUpper);
@@ -873,7 +873,8 @@ __global__ void __launch_bounds__(threads_of(N), 1)
 #pragma unroll
                 for (int i = 0; i < kH / 2; ++i) sum[i] = f2_add(sum[i], e[i]);
                 uint32_t part[3][kH / 4];
-                in_parts<kH>(r, part);
+                // 256 keys in a row have all the 256 values
+                in_parts<kH>(r, (__brev(static_cast<uint32_t>(t * kKeys + key)) >> 24) * 0x00010001u, part);
                 // the weight tile before last was read
                 if (it > 1) ok = wait(pv_done + (it & 1), ((it >> 1) & 1) ^ 1, p.status, abort_flag) && ok;
                 uint8_t* pt = smem + kPlan.p_off + (it & 1) * kPlan.p_bytes;
@@ -1071,13 +1072,18 @@ __global__ void __launch_bounds__(threads_of(N), 1)
     }
 }
 
-// Where references are held, by the keys n a CTA passes of a row: 2^(15 - G), G
-// binades below what a weight may reach, with n 2^-(32 - G) <= 2^-8: what is
-// lost of weights too small for e5m2 stays below a bf16 step of the largest
-// even if they all are.  The more room, the fewer references move.
+// Where references are held, by the keys n a CTA passes of a row: 2^(15 - G),
+// G binades below what a weight times its scale may reach.  The more room, the
+// fewer references move (1024 keys of 64 heads with scores of 3 bits' deviation:
+// 2.9 moves a row with G = 14, about 1.5 with 18; a move takes 2.5 us).  The
+// price is paid by small weights, whose steps are 2^-16.  They are rounded up as
+// often as they are worth, by offsets that run through all values from key to
+// key, so that their sum's error grows with sqrt(n): 2^-(32 - G) sqrt(n) <= 2^-9
+// of the reference.  What fp16 itself cannot hold (below 2^-25) is lost:
+// n 2^-(40 - G) <= 2^-9.
 float room_of(int64_t n) {
-    int g = 16;
-    while (g > 8 && n > (int64_t(1) << (24 - g))) --g;
+    int g = 20;
+    while (g > 8 && (n > (int64_t(1) << 2 * (23 - g)) || n > (int64_t(1) << (31 - g)))) --g;
     return std::exp2(15.0f - g);
 }
 

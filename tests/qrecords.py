@@ -90,11 +90,13 @@ def attend64(q, rec, s, scale):
 
     * A score sums 2 * 576 products in fp32 (the query is held as two numbers), each exact: terms * 2^-23 of the sum of
       magnitudes; a query element is off by 2^-22 of its head's largest.  Together delta; a weight changes by exp(delta).
-    * Weights are held in 9 significant bits and rounded once before, 2^-9 + 2^-11 < 2^-8 of sum p |c|.  The smallest
-      e5m2 is 2^-16, so that a weight times its scale is never closer than 2^-17.  The largest of a head's over n keys
-      worked on together is held at 2^(15 - G) or more, G <= 16 and n 2^-(32 - G) <= 2^-8: 2^-16 of the largest p s for
-      every code, and together no more than 2^-8 of it times the largest code.  Where a row is worked on in pieces, each
-      relative to its own largest, the latter is no more than 2^-8 of sum p s.
+    * Weights times scales are rounded to fp16 and then, up or down, to the third of three e5m2: 2^-11 + 2^-8 of sum
+      p |c| at most.  The smallest e5m2 is 2^-16, and the largest product of a head over the n keys worked on together is
+      held at 2^(15 - G) or more, G <= 20, n <= 4^(23 - G): smaller products w are off by up to a step
+      q = 2^-(31 - G) of it.  Which way is set by the key's place, independent of its values: independent errors of zero
+      mean and variance min(q / 4, w) q.  A sum of them with variance V, none above M, passes 9 sqrt(V) + 20 M with a
+      probability below 1e-13 (Bernstein).  The step is 2^-11 for 64 keys and halves at most where their number
+      quadruples; so for any pieces V is at most 4 times what pieces of 64 keys have.
     * The result is rounded to bf16: 2^-8.
     """
     H = q.shape[0]
@@ -108,9 +110,15 @@ def attend64(q, rec, s, scale):
     p = torch.exp(y - lse[:, None])
     v = rec[:, :LAT]
     o = p @ v
-    codes = v.abs() / torch.where(s > 0, s, 1.0)[:, None]
-    floor = torch.minimum(2.0 ** -16 * (p * s).amax(1, keepdim=True) * codes.sum(0), 2.0 ** -8 * (p @ s)[:, None] * codes.amax(0))
-    tol = (2.0 ** -8 + 2 * (2 * delta).expm1())[:, None] * (p @ v.abs()) + floor + 2.0 ** -8 * o.abs() + 1e-30
+    codes = v / torch.where(s > 0, s, 1.0)[:, None]
+    var, most = torch.zeros_like(o), torch.zeros_like(o)
+    for a in range(0, len(s), 64):
+        w = (p * s)[:, a:a + 64]
+        c, step = codes[a:a + 64], 2.0 ** -11 * w.amax(1, keepdim=True)
+        var += 4 * torch.minimum(step / 4, w) * step @ c.square()
+        most = torch.maximum(most, step * c.abs().amax(0))
+    floor = 9 * var.sqrt() + 20 * most
+    tol = (2.0 ** -8 + 2.0 ** -11 + 2 * (2 * delta).expm1())[:, None] * (p @ v.abs()) + floor + 2.0 ** -8 * o.abs() + 1e-30
     return o, lse, tol, delta + lse.abs() * 2.0 ** -22 + 2.0 ** -19
 
 

@@ -284,6 +284,22 @@ def test_attend_queries_of_any_size(size):
     assert bool(out[1, [7, 9]].isnan().all()) and bool(lse[1, [7, 9]].isnan().all())
 
 
+@pytest.mark.parametrize("T,H,topk,spread", [(50, 128, 64, 0.4), (20, 64, 512, 0.4), (9, 16, 2048, 0.0), (3, 20, 700, 1.0)])
+def test_attend_errors_of_a_head_together(T, H, topk, spread):
+    """A head's 512 results together: independent errors of at most 2^-9 (results), 2^-8 / sqrt(3) (weights) and 2^-9
+    (small weights, whose steps are chosen for it) of sum p |c|, less than 2^-7 of it."""
+    g = gen(16)
+    cache = filled(g, 60, 64, spread=spread)
+    ql, qp = queries(g, T, H)
+    slots = torch.randint(0, 3840, (T, topk), generator=g, device="cuda")
+    out, _ = slots_call(cache, ql, qp, slots)
+    for t in range(T):
+        rec, _ = qr.records(cache.pool, 64, slots[t])
+        p = torch.softmax(torch.cat([ql[t], qp[t]], 1).double() @ rec.T * SCALE, 1)
+        err = (out[t].double() - p @ rec[:, :LAT]).norm(dim=1)
+        assert bool((err <= 2.0 ** -7 * (p @ rec[:, :LAT].abs()).norm(dim=1)).all())
+
+
 def paged_inputs(g, lens, bs, extra=3):
     """As test_gpu_latent's: blocks at random, NaN everywhere but in the sequences' own records."""
     nblk = [(n + bs - 1) // bs for n in lens]
