@@ -5,16 +5,18 @@ attention, through the public calls:
 
 The index keys and the latent records of a token share its slot: both pools
 have the same blocks, so the slots the score call returns name the records
-the attention reads.  Inputs are seeded and synthetic.
+the attention reads, and one block table and one count a page serve both.
+Records are bf16 or 8 bits.  Inputs are seeded and synthetic.
 """
 from __future__ import annotations
 
 import dataclasses
 import math
+from typing import Optional, Union
 
 import torch
 
-from . import dsaidx, latent
+from . import dsaidx, latent, pages
 from . import workloads as wl
 from .host import bf16_tensor
 
@@ -25,26 +27,32 @@ SCALE = 1.0 / math.sqrt(latent.NOPE_DIM + latent.PE_DIM)
 class SparseLayer:
     """The caches of one layer and what a serving process keeps beside them."""
     index: dsaidx.IndexCache
-    records: latent.LatentCache
+    records: Union[latent.LatentCache, latent.QuantLatentCache]
     plan: latent.RopePlan
     block_table: torch.Tensor
     topk: int
     scale: float = SCALE
+    page_set: Optional[pages.PageSet] = None      # counts of the pages: track_pages
 
     @staticmethod
     def allocate(num_blocks: int, block_size: int, block_table: torch.Tensor, topk: int, key_dtype: int = dsaidx.FP8,
-                 temperature: str = "logit"):
-        """YaRN's temperature multiplies the whole logit by amplitude^2.  Where all of a head is turned, turning it to
+                 temperature: str = "logit", records: str = "bf16"):
+        """records: "bf16" (1152 bytes a token) or "fp8" (644).
+
+        YaRN's temperature multiplies the whole logit by amplitude^2.  Where all of a head is turned, turning it to
         the length amplitude does that; here 64 of a key's 576 elements are turned, so the turned elements keep their
         length and the softmax scale carries it.  temperature="turn" is for a model whose turned elements alone are
         lengthened (their part of the logit then counts amplitude^2 times as much against the latent's)."""
         if temperature not in ("logit", "turn"):
             raise ValueError('temperature must be "logit" or "turn"')
         yarn = dict(base=160000.0, scaling="yarn", factor=40.0, original_max_pos=4096)
+        if records not in ("bf16", "fp8"):
+            raise ValueError('records must be "bf16" or "fp8"')
+        kind = latent.LatentCache if records == "bf16" else latent.QuantLatentCache
         amplitude = latent.rope_steps(latent.PE_DIM, **yarn)[1]
         whole = temperature == "logit"
         return SparseLayer(dsaidx.IndexCache.allocate(num_blocks, block_size, key_dtype),
-                           latent.LatentCache.allocate(num_blocks, block_size),
+                           kind.allocate(num_blocks, block_size),
                            latent.rope_plan(latent.PE_DIM, amplitude=1.0 if whole else amplitude, **yarn),
                            block_table, topk, SCALE * amplitude ** 2 if whole else SCALE)
 
@@ -80,6 +88,54 @@ class SparseLayer:
                                    out, ws, lse=lse)
         return out, lse
 
+    def track_pages(self):
+        """Count the pages the block table names (entries >= 0, which end each row), so that rows can be forked, grown,
+        ended and compacted.  Layers with the same block table share one set: give it the pools of all of them."""
+        refs = torch.zeros(self.records.num_blocks, dtype=torch.int32, device=self.block_table.device)
+        held = self.block_table[self.block_table >= 0].long()
+        refs.index_add_(0, held, torch.ones_like(held, dtype=torch.int32))
+        self.page_set = pages.PageSet(refs, self.records.block_size, [self.index.pool, self.records.pool])
+
+    def fork(self, seq_lens, parents, max_blocks_per_seq: Optional[int] = None):
+        """A layer over the same caches whose row i continues row parents[i] (-1: an empty row), and its lengths.  Full
+        pages are shared, partly filled ones copied; the rows here stay."""
+        n, dev = parents.shape[0], self.block_table.device
+        table = torch.full((n, max_blocks_per_seq or self.block_table.shape[1]), -1, dtype=torch.int32, device=dev)
+        lens, pairs = torch.zeros(n, dtype=torch.int32, device=dev), torch.empty(n, 2, dtype=torch.int32, device=dev)
+        pages.fork(self.page_set, self.block_table, seq_lens, parents, table, lens, pairs, self._page_workspace(n))
+        pages.copy(self.page_set, pairs)
+        return dataclasses.replace(self, block_table=table), lens
+
+    def grow(self, seq_lens, longer):
+        """Pages for rows that go from seq_lens to longer tokens; seq_lens becomes longer."""
+        pages.extend(self.page_set, self.block_table, seq_lens, longer, self._page_workspace(seq_lens.shape[0]))
+
+    def end(self, seq_lens, which=None):
+        """The rows named (None: all) end: pages that no other row holds are free again."""
+        pages.free(self.page_set, self.block_table, seq_lens, which)
+
+    def compact(self):
+        """Moves the pages in use to the front of the pools.  Returns every page's new id (-1: free): block tables of
+        other layers forked from this one follow through it."""
+        ps, i32 = self.page_set, dict(dtype=torch.int32, device=self.block_table.device)
+        page_map, count = torch.empty(ps.num_blocks, **i32), torch.empty(1, **i32)
+        pairs = torch.empty(max(ps.num_blocks // 2, 1), 2, **i32)
+        pages.compact(ps, self.block_table, ps.refs, self.block_table, page_map, pairs, count, self._page_workspace(0))
+        pages.copy(ps, pairs, count=count)
+        return page_map
+
+    def _page_workspace(self, rows: int):
+        return dsaidx.new_workspace(pages.workspace_bytes(self.page_set.num_blocks, rows))
+
+    def cached(self, slots):
+        """The records at slots [n], bf16: c [n, 512] and the turned k_pe [n, 64]."""
+        if isinstance(self.records, latent.QuantLatentCache):
+            rec = torch.empty(slots.shape[0], latent.RECORD, dtype=torch.bfloat16, device=slots.device)
+            latent.latent_read(self.records, slots, rec)
+        else:
+            rec = self.records.pool.view(-1, latent.RECORD)[slots]
+        return rec[:, :latent.LATENT_DIM], rec[:, latent.LATENT_DIM:]
+
 
 def prompt(layer: SparseLayer, q, k_up, v_up, c, k_pe, positions, cu_seqlens, in_place: bool = True):
     """Prompts no longer than the top-k select every key: expanded attention, without the indexer.  q [tokens,
@@ -99,14 +155,27 @@ def prompt(layer: SparseLayer, q, k_up, v_up, c, k_pe, positions, cu_seqlens, in
     return out
 
 
+def chunk(layer: SparseLayer, q, k_up, v_up, positions, slots, cu_seqlens_q, cu_seqlens_k):
+    """Chunks of prompts behind what is cached of them: every key of each sequence is read back from its record, the
+    chunk's own among them (append them first).  q [tokens, heads, 192] as for prompt (turned where it is), slots
+    [keys] of every sequence's tokens in order, cu_seqlens_q and _k where each sequence's queries and keys begin."""
+    latent.rope(q[:, :, latent.NOPE_DIM:], positions, layer.plan)
+    c, kp = layer.cached(slots)
+    k_nope = torch.einsum("tc,hcd->thd", c, k_up)
+    v = torch.einsum("tc,hcd->thd", c, v_up)
+    out = torch.empty(q.shape[0], *v.shape[1:], dtype=torch.bfloat16, device=q.device)
+    latent.latent_attend_expanded(q, k_nope, kp, v, cu_seqlens_q, cu_seqlens_k, layer.scale, out)
+    return out
+
+
 def demo_layer(seq_lens, topk: int, heads: int, seed: int = 0, block_size: int = 64,
-               temperature: str = "turn"):
+               temperature: str = "turn", records: str = "bf16"):
     """A layer filled with seq_lens tokens a sequence and the inputs of one decode step.  The records are synthetic;
-    temperature is SparseLayer.allocate's."""
+    temperature and records are SparseLayer.allocate's."""
     W = wl.make_workload("step", seq_lens, [1] * len(seq_lens), topk=topk, bs=block_size, seed=seed)
     dev = "cuda"
     layer = SparseLayer.allocate(W.num_blocks, block_size, torch.from_numpy(W.block_table).to(dev), topk,
-                                 temperature=temperature)
+                                 temperature=temperature, records=records)
     g = torch.Generator(device=dev).manual_seed(seed)
     n = sum(seq_lens)
     kv = torch.randn(n, latent.RECORD, generator=g, device=dev).bfloat16()
@@ -122,14 +191,27 @@ def demo_layer(seq_lens, topk: int, heads: int, seed: int = 0, block_size: int =
 
 
 def main():
-    layer, step, _, _ = demo_layer([4500, 10000] * 4, topk=512, heads=128, temperature="logit")
-    out, lse, idx, _ = layer.decode(**step)
-    turned = latent.rope(step["q_pe"], step["positions"], layer.plan, out=torch.empty_like(step["q_pe"]))
-    dense, dense_lse = layer.decode_dense(step["q_latent"], turned, step["seq_lens"], step["max_seq_len"])
-    torch.cuda.synchronize()
-    share = torch.exp(lse - dense_lse).mean()
-    print("8 sequences of 4500 / 10000 keys, top-512, 128 heads: selected keys hold %.1f%% of the softmax weight, "
-          "|sparse - dense| / |dense| = %.3f" % (100 * float(share), float((out - dense).norm() / dense.norm())))
+    lens = [4500, 10000] * 4
+    results = {}
+    for records in ("bf16", "fp8"):
+        layer, step, _, _ = demo_layer(lens, topk=512, heads=128, temperature="logit", records=records)
+        out, lse, idx, _ = layer.decode(**step)
+        turned = latent.rope(step["q_pe"], step["positions"], layer.plan, out=torch.empty_like(step["q_pe"]))
+        dense, dense_lse = layer.decode_dense(step["q_latent"], turned, step["seq_lens"], step["max_seq_len"])
+        torch.cuda.synchronize()
+        results[records] = out
+        share = torch.exp(lse - dense_lse).mean()
+        print("%s records, 8 sequences of 4500 / 10000 keys, top-512, 128 heads: selected keys hold %.1f%% of the softmax "
+              "weight, |sparse - dense| / |dense| = %.3f" % (records, 100 * float(share), float((out - dense).norm() / dense.norm())))
+    diff = (results["fp8"].float() - results["bf16"].float()).norm() / results["bf16"].float().norm()
+    print("fp8 against bf16 records: %.3f of the results" % float(diff))
+    # two continuations of each sequence, on shared pages
+    layer.track_pages()
+    held = int((layer.page_set.refs > 0).sum())
+    parents = torch.arange(16, dtype=torch.int32, device="cuda") // 2
+    both, both_lens = layer.fork(step["seq_lens"], parents)
+    print("forked in two: %d pages in use instead of %d" % (int((layer.page_set.refs > 0).sum()), held))
+    both.end(both_lens)
 
 
 if __name__ == "__main__":
