@@ -32,7 +32,8 @@ class SparseLayer:
     block_table: torch.Tensor
     topk: int
     scale: float = SCALE
-    page_set: Optional[pages.PageSet] = None      # counts of the pages: track_pages
+    page_set: Optional[pages.PageSet] = None      # counts of the pages and what their calls work in: track_pages
+    page_ws: Optional[torch.Tensor] = None
 
     @staticmethod
     def allocate(num_blocks: int, block_size: int, block_table: torch.Tensor, topk: int, key_dtype: int = dsaidx.FP8,
@@ -88,13 +89,20 @@ class SparseLayer:
                                    out, ws, lse=lse)
         return out, lse
 
-    def track_pages(self):
+    def track_pages(self, max_rows: int):
         """Count the pages the block table names (entries >= 0, which end each row), so that rows can be forked, grown,
-        ended and compacted.  Layers with the same block table share one set: give it the pools of all of them."""
+        ended and compacted: of at most max_rows rows a call, one call behind the other.  Layers with the same block
+        table share one set: give it the pools of all of them."""
         refs = torch.zeros(self.records.num_blocks, dtype=torch.int32, device=self.block_table.device)
         held = self.block_table[self.block_table >= 0].long()
         refs.index_add_(0, held, torch.ones_like(held, dtype=torch.int32))
         self.page_set = pages.PageSet(refs, self.records.block_size, [self.index.pool, self.records.pool])
+        self.page_ws = dsaidx.new_workspace(pages.workspace_bytes(self.page_set.num_blocks, max_rows))
+
+    def page_status(self) -> int:
+        """Waits; 0, or what the page calls found so far: rows for which no pages were left (they keep what they had, a
+        forked one is empty), entries that are none."""
+        return dsaidx.read_device_status(self.page_ws)
 
     def fork(self, seq_lens, parents, max_blocks_per_seq: Optional[int] = None):
         """A layer over the same caches whose row i continues row parents[i] (-1: an empty row), and its lengths.  Full
@@ -102,17 +110,17 @@ class SparseLayer:
         n, dev = parents.shape[0], self.block_table.device
         table = torch.full((n, max_blocks_per_seq or self.block_table.shape[1]), -1, dtype=torch.int32, device=dev)
         lens, pairs = torch.zeros(n, dtype=torch.int32, device=dev), torch.empty(n, 2, dtype=torch.int32, device=dev)
-        pages.fork(self.page_set, self.block_table, seq_lens, parents, table, lens, pairs, self._page_workspace(n))
-        pages.copy(self.page_set, pairs)
+        pages.fork(self.page_set, self.block_table, seq_lens, parents, table, lens, pairs, self.page_ws)
+        pages.copy(self.page_set, pairs, status=self._page_flag())
         return dataclasses.replace(self, block_table=table), lens
 
     def grow(self, seq_lens, longer):
         """Pages for rows that go from seq_lens to longer tokens; seq_lens becomes longer."""
-        pages.extend(self.page_set, self.block_table, seq_lens, longer, self._page_workspace(seq_lens.shape[0]))
+        pages.extend(self.page_set, self.block_table, seq_lens, longer, self.page_ws)
 
     def end(self, seq_lens, which=None):
         """The rows named (None: all) end: pages that no other row holds are free again."""
-        pages.free(self.page_set, self.block_table, seq_lens, which)
+        pages.free(self.page_set, self.block_table, seq_lens, which, status=self._page_flag())
 
     def compact(self):
         """Moves the pages in use to the front of the pools.  Returns every page's new id (-1: free): block tables of
@@ -120,12 +128,12 @@ class SparseLayer:
         ps, i32 = self.page_set, dict(dtype=torch.int32, device=self.block_table.device)
         page_map, count = torch.empty(ps.num_blocks, **i32), torch.empty(1, **i32)
         pairs = torch.empty(max(ps.num_blocks // 2, 1), 2, **i32)
-        pages.compact(ps, self.block_table, ps.refs, self.block_table, page_map, pairs, count, self._page_workspace(0))
-        pages.copy(ps, pairs, count=count)
+        pages.compact(ps, self.block_table, ps.refs, self.block_table, page_map, pairs, count, self.page_ws)
+        pages.copy(ps, pairs, count=count, status=self._page_flag())
         return page_map
 
-    def _page_workspace(self, rows: int):
-        return dsaidx.new_workspace(pages.workspace_bytes(self.page_set.num_blocks, rows))
+    def _page_flag(self):
+        return self.page_ws[:4].view(torch.int32)
 
     def cached(self, slots):
         """The records at slots [n], bf16: c [n, 512] and the turned k_pe [n, 64]."""
@@ -169,12 +177,12 @@ def chunk(layer: SparseLayer, q, k_up, v_up, positions, slots, cu_seqlens_q, cu_
 
 
 def demo_layer(seq_lens, topk: int, heads: int, seed: int = 0, block_size: int = 64,
-               temperature: str = "turn", records: str = "bf16"):
-    """A layer filled with seq_lens tokens a sequence and the inputs of one decode step.  The records are synthetic;
-    temperature and records are SparseLayer.allocate's."""
+               temperature: str = "turn", records: str = "bf16", spare_blocks: int = 0):
+    """A layer filled with seq_lens tokens a sequence (and spare_blocks more) and the inputs of one decode step.  The
+    records are synthetic; temperature and records are SparseLayer.allocate's."""
     W = wl.make_workload("step", seq_lens, [1] * len(seq_lens), topk=topk, bs=block_size, seed=seed)
     dev = "cuda"
-    layer = SparseLayer.allocate(W.num_blocks, block_size, torch.from_numpy(W.block_table).to(dev), topk,
+    layer = SparseLayer.allocate(W.num_blocks + spare_blocks, block_size, torch.from_numpy(W.block_table).to(dev), topk,
                                  temperature=temperature, records=records)
     g = torch.Generator(device=dev).manual_seed(seed)
     n = sum(seq_lens)
@@ -194,7 +202,7 @@ def main():
     lens = [4500, 10000] * 4
     results = {}
     for records in ("bf16", "fp8"):
-        layer, step, _, _ = demo_layer(lens, topk=512, heads=128, temperature="logit", records=records)
+        layer, step, _, _ = demo_layer(lens, topk=512, heads=128, temperature="logit", records=records, spare_blocks=16)
         out, lse, idx, _ = layer.decode(**step)
         turned = latent.rope(step["q_pe"], step["positions"], layer.plan, out=torch.empty_like(step["q_pe"]))
         dense, dense_lse = layer.decode_dense(step["q_latent"], turned, step["seq_lens"], step["max_seq_len"])
@@ -206,10 +214,12 @@ def main():
     diff = (results["fp8"].float() - results["bf16"].float()).norm() / results["bf16"].float().norm()
     print("fp8 against bf16 records: %.3f of the results" % float(diff))
     # two continuations of each sequence, on shared pages
-    layer.track_pages()
+    layer.track_pages(max_rows=16)
     held = int((layer.page_set.refs > 0).sum())
     parents = torch.arange(16, dtype=torch.int32, device="cuda") // 2
     both, both_lens = layer.fork(step["seq_lens"], parents)
+    if both.page_status():
+        raise RuntimeError("no pages left")
     print("forked in two: %d pages in use instead of %d" % (int((layer.page_set.refs > 0).sum()), held))
     both.end(both_lens)
 

@@ -197,7 +197,7 @@ def test_rows_forked_grown_ended_and_compacted(records):
     for a, b in ((big.index.pool, layer.index.pool), (big.records.pool, layer.records.pool)):
         a.view(nb + more, -1)[9:9 + nb] = b.view(nb, -1)
     layer = big
-    layer.track_pages()
+    layer.track_pages(max_rows=7)
     before = rows_of(layer, step["seq_lens"])
     held = int((layer.page_set.refs > 0).sum())
     assert held == sum((n + 63) // 64 for n in lens)
@@ -253,5 +253,22 @@ def test_rows_forked_grown_ended_and_compacted(records):
     assert all(torch.equal(a, b) for a, b in zip(rows_of(rows, now), was))
     second = rows.decode(**s)
     assert all(torch.equal(a, b) for a, b in zip(first[:3], second[:3]))
+    assert rows.page_status() == 0
     rows.end(now)
     assert bool((rows.page_set.refs == 0).all())
+
+
+def test_pages_that_run_out():
+    """Rows for which none are left keep what they had, a forked one is empty, and the layer says so."""
+    layer, step, _, _ = sparse_step.demo_layer([130, 64], 128, 16, seed=17, temperature="logit", records="fp8", spare_blocks=1)
+    layer.track_pages(max_rows=3)
+    free = int((layer.page_set.refs == 0).sum())
+    lens = step["seq_lens"]
+    before = rows_of(layer, lens)
+    rows, now = layer.fork(lens, torch.tensor([1, 0, 1], dtype=torch.int32, device="cuda"), max_blocks_per_seq=40)
+    assert rows.page_status() == 0 and now.tolist() == [64, 130, 64]      # one copy
+    longer = torch.tensor([64 + 64 * free, 130, 65], dtype=torch.int32, device="cuda")
+    rows.grow(now, longer)
+    assert rows.page_status() != 0
+    assert now.tolist() == [64, 130, 64]            # no row behind the first that finds too few gets any
+    assert all(torch.equal(a[:len(b)], b) for a, b in zip(rows_of(rows, now), (before[1], before[0], before[1])))
