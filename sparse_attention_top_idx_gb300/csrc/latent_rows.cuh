@@ -105,8 +105,9 @@ struct Walk {
             return true;
         }
         if (!p.split) {
-            w.row = pos / p.hgs;
-            w.hg = static_cast<int>(pos - w.row * p.hgs);
+            const uint32_t item = static_cast<uint32_t>(pos), r = item / p.hgs;      // fewer than 2^31 items
+            w.row = r;
+            w.hg = static_cast<int>(item - r * p.hgs);
             w.keys = row_keys(p, w.row);
             w.t0 = 0;
             w.t1 = tiles_of<kTile>(w.keys);

@@ -286,6 +286,10 @@ __device__ __noinline__ void split_heads(uint8_t* q, int first, int n, float sca
     }
 }
 
+__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* map, int c0, int c1, int c2) {
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(map), "r"(c0), "r"(c1), "r"(c2) : "memory");
+}
+
 // What a wait does that is not over at once, and a step to the next piece of
 // work: one copy each, out of the loops' code (see the note on its size).
 __device__ __noinline__ bool wait_longer(uint64_t* bar, uint32_t parity, int32_t* status, volatile int* abort_flag) {
@@ -504,10 +508,10 @@ __global__ void __launch_bounds__(threads_of(N), 1)
                            : static_cast<int64_t>(__ldg(p.block_table + w.row * p.mbps + block_of(p, key)));
             };
             int64_t entry = entry_of(w.t0 + two), next = entry_of(w.t0 + kPer + two);
-            // the queries are written behind the copies of the second tile, or of
-            // the first where the ring does not hold two: its slots come free by
-            // products with these queries
-            const int split_at = kSlots >= 2 * kTileChunks ? min(w.t0 + 1, w.t1 - 1) : w.t0;
+            // The queries are written behind the copies of the first tile; of the
+            // second for a CTA's first row, where every warp splits, if the ring
+            // holds two: its slots come free by products with these queries.
+            const int split_at = kSlots >= 2 * kTileChunks && turn.item == 0 ? min(w.t0 + 1, w.t1 - 1) : w.t0;
             for (int t0 = w.t0; ok && t0 < w.t1; t0 += kPer) {
                 // block and place of this lane's key
                 const int key = (t0 + two) * kKeys + j;
@@ -605,6 +609,17 @@ __global__ void __launch_bounds__(threads_of(N), 1)
             fence_proxy_async_smem();
             mbar_arrive(q_full);
             turn.next(w);
+            // the next row's queries on their way from memory to L2
+            if (warp == 3 && kCl == 1) {
+                Pieces<kKeys> ahead = walk;
+                Work then;
+                if (ahead.next(then) && elect_one()) {
+                    const int h = then.hg * N, row = static_cast<int>(then.row);
+                    for (int c = 0; c < 8; ++c) tma_prefetch_3d(&ql_map, 64 * c, p.ql_swap ? row : h, p.ql_swap ? h : row);
+                    tma_prefetch_3d(&qp_map, 0, p.qp_swap ? row : h, p.qp_swap ? h : row);
+                }
+                __syncwarp();
+            }
         }
         // no copy may be on its way when the shared memory goes
         if (!ok && warp == 1) wait(q_raw, turn.item & 1, p.status, nullptr);
@@ -708,7 +723,8 @@ __global__ void __launch_bounds__(threads_of(N), 1)
             fence_proxy_async_smem();
             mbar_arrive(q_full);
         }
-        while (walk.next(w)) {
+        bool more = walk.next(w);
+        while (more) {
             // reference and this thread's share of the sum of head hb + i; the
             // unit of the scales (a power of two) and what brings it to p.room
             f2 minus_m[kH / 2], sum[kH / 2];
@@ -899,6 +915,10 @@ __global__ void __launch_bounds__(threads_of(N), 1)
             }
             // A wait may have run out in some threads alone.  None of them leaves
             // before the vote below, whose barrier counts every thread.
+            // (The next piece is looked up while the last values are formed: behind
+            // the results it took 2.6k cycles of a row's 55k.)
+            Work after;
+            if (kCl == 1) more = walk.next(after);
             // sums over the warp's keys, then over the four warps
             ok = ok && wait(pv_done + ((it - 1) & 1), ((it - 1) >> 1) & 1, p.status, abort_flag);
             tc_fence_after();
@@ -980,17 +1000,19 @@ __global__ void __launch_bounds__(threads_of(N), 1)
                 // neighbouring lanes swap so that each stores two dimensions of one head
                 const bool odd = lane & 1;
                 const int left = p.heads - h0 - hc - odd;      // heads from this lane's first one on
+                const uint32_t pick = odd ? 0x3276u : 0x5410u;
                 __nv_bfloat16* dst = p.out + (w.row * p.heads + h0 + hc + odd) * IDX_LATENT_DIM + (d & ~1);
 #pragma unroll
                 for (int j = 0; j < 16; j += 2) {
-                    const float c = __shfl_xor_sync(~0u, odd ? o[j] : o[j + 1], 1);
-                    const uint32_t two = odd ? bf16x2(c, o[j + 1]) : bf16x2(o[j], c);
-                    if (j < left) *reinterpret_cast<uint32_t*>(dst + j * IDX_LATENT_DIM) = two;
+                    const uint32_t two = bf16x2(o[j], o[j + 1]);
+                    const uint32_t swapped = __byte_perm(two, __shfl_xor_sync(~0u, two, 1), pick);
+                    if (j < left) *reinterpret_cast<uint32_t*>(dst + j * IDX_LATENT_DIM) = swapped;
                 }
             }
             tc_fence_before();
             mbar_arrive(o_empty);
             named_sync<1, kSoftThreads>();   // the statistics' memory is reused
+            w = after;
             ++item;
         }
         // a share without tiles

@@ -9,7 +9,7 @@ def softmax_role():
     """The softmax role's loop over the pieces."""
     text = source("qlatent_attend.cu")
     role = text[text.index("else if (warp >= 4)"):text.index("if (kCl > 1 && it == 0")]
-    return role[role.index("while (walk.next(w))"):]
+    return role[role.index("while (more)"):]
 
 
 def test_softmax_threads_leave_together():
