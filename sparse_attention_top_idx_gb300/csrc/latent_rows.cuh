@@ -77,12 +77,58 @@ __device__ __forceinline__ void find_row(const RowParams& p, int64_t x, int64_t&
     base = acc;
 }
 
+// The run [start, end) of CTA c of g in the line of all tiles, and the row it
+// begins in (paged contexts).  A whole warp.  The lengths of up to 32 rows are
+// read once.
+template <int kTile>
+__device__ __forceinline__ void find_run(const RowParams& p, uint32_t c, uint32_t g, int64_t& start, int64_t& end, int64_t& row, int64_t& base) {
+    int64_t tt, v = 0;
+    if (p.block_table == nullptr) {
+        tt = p.rows * p.hgs * tiles_of<kTile>(p.max_keys);
+    } else if (p.rows <= 32) {
+        const int lane = lane_id();
+        // (32 rows of fewer than 2^25 tiles)
+        uint32_t n = lane < p.rows ? static_cast<uint32_t>(tiles_of<kTile>(row_keys(p, lane))) : 0u;
+        for (int d = 1; d < 32; d <<= 1) {
+            const uint32_t u = __shfl_up_sync(~0u, n, d);
+            if (lane >= d) n += u;
+        }
+        v = static_cast<int64_t>(n) * p.hgs;
+        tt = __shfl_sync(~0u, v, 31);
+    } else {
+        int64_t none;
+        find_row<kTile>(p, -1, none, tt);
+    }
+    if (tt >> 32 == 0) {      // c tt / g without a long division
+        const uint32_t q = static_cast<uint32_t>(tt) / g, r = static_cast<uint32_t>(tt) - q * g;
+        start = static_cast<int64_t>(c) * q + c * r / g;
+        end = static_cast<int64_t>(c + 1) * q + (c + 1) * r / g;
+    } else {
+        start = run_start(c, g, tt);
+        end = run_start(c + 1, g, tt);
+    }
+    if (p.block_table == nullptr || start >= end) return;
+    if (p.rows > 32) {
+        find_row<kTile>(p, start, row, base);
+        return;
+    }
+    const int k = __ffs(__ballot_sync(~0u, start < v)) - 1;      // (lanes behind the last row have its v)
+    const int64_t before = __shfl_sync(~0u, v, k > 0 ? k - 1 : 0);
+    row = k;
+    base = k > 0 ? before : 0;
+}
+
 // One piece of work: tiles [t0, t1) of a row's head group.
 struct Work {
     int64_t row;
     int hg, keys, t0, t1;
     int slot;       // where its partial sums go; -1: it has all tiles, write the result; -2: the cluster joins
 };
+
+// a / b, without a long division where a has 32 bits; both positive.
+__device__ __forceinline__ int64_t quotient(int64_t a, int b) {
+    return a >> 32 == 0 ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
+}
 
 // The pieces of this CTA, in order; every role walks them by itself.
 template <int kTile>
@@ -120,8 +166,8 @@ struct Walk {
         if (p.block_table == nullptr) {
             w.keys = p.max_keys;
             nt = tiles_of<kTile>(w.keys);
-            const int64_t item = pos / nt;
-            w.row = item / p.hgs;
+            const int64_t item = quotient(pos, nt);
+            w.row = quotient(item, p.hgs);
             w.hg = static_cast<int>(item - w.row * p.hgs);
             in = pos - item * nt;
         } else {
@@ -134,7 +180,7 @@ struct Walk {
                 nt = tiles_of<kTile>(w.keys);
             }
             w.row = row;
-            w.hg = static_cast<int>((pos - base) / nt);
+            w.hg = static_cast<int>(static_cast<uint32_t>(pos - base) / nt);      // (fewer than 2^31 tiles a row)
             in = pos - base - static_cast<int64_t>(w.hg) * nt;
         }
         w.t0 = static_cast<int>(in);

@@ -241,9 +241,10 @@ __device__ __forceinline__ T over_keys(T (&v)[kH], Op op) {
 // Two heads at once: a head is a chain of trips to shared memory and through the
 // warp (440 cycles).
 // One copy for the roles that call it: the kernel's code is larger than the
-// instruction caches.
+// instruction caches.  `pitch` (bytes of an eighth's heads) is N * 128, or 0 for
+// a call that only brings the code near.
 template <int N>
-__device__ __noinline__ void split_heads(uint8_t* q, int first, int n, float scale_log2, float* factor) {
+__device__ __noinline__ void split_heads(uint8_t* q, int pitch, int first, int n, float scale_log2, float* factor) {
     const int lane = lane_id();
 #pragma unroll 1
     for (int k0 = 0; k0 < n; k0 += 2) {
@@ -253,10 +254,10 @@ __device__ __noinline__ void split_heads(uint8_t* q, int first, int n, float sca
         for (int j = 0; j < 2; ++j) {
             h[j] = first + min(k0 + j, n - 1);      // (the last one twice: the same is written)
             // raw: pieces 2 (lane % 4) and the next of 64 values
-            const uint8_t* raw = q + (lane >> 2) * (N * 128) + h[j] * 128;
+            const uint8_t* raw = q + (lane >> 2) * pitch + h[j] * 128;
             const uint4 u = *reinterpret_cast<const uint4*>(raw + (((2 * (lane & 3)) ^ (h[j] & 7)) << 4));
             const uint4 v = *reinterpret_cast<const uint4*>(raw + (((2 * (lane & 3) + 1) ^ (h[j] & 7)) << 4));
-            p[j] = *reinterpret_cast<const uint32_t*>(q + 4 * (2 * N * 128) + h[j] * 128 + (((lane >> 2) ^ (h[j] & 7)) << 4) + 4 * (lane & 3));
+            p[j] = *reinterpret_cast<const uint32_t*>(q + 8 * pitch + h[j] * 128 + (((lane >> 2) ^ (h[j] & 7)) << 4) + 4 * (lane & 3));
             w[j][0] = u.x, w[j][1] = u.y, w[j][2] = u.z, w[j][3] = u.w;
             w[j][4] = v.x, w[j][5] = v.y, w[j][6] = v.z, w[j][7] = v.w;
         }
@@ -290,14 +291,14 @@ __device__ __noinline__ void split_heads(uint8_t* q, int first, int n, float sca
                 lo[i] = b[0] | b[1] << 16;
             }
             // split: piece lane % 8 of 128
-            uint8_t* row = q + (lane >> 3) * (2 * N * 128) + h[j] * 128 + (((lane & 7) ^ (h[j] & 7)) << 4);
+            uint8_t* row = q + 2 * (lane >> 3) * pitch + h[j] * 128 + (((lane & 7) ^ (h[j] & 7)) << 4);
             *reinterpret_cast<uint4*>(row) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4*>(row + N * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            *reinterpret_cast<uint4*>(row + pitch) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
             // half of the position part in the hi rows, the other half (times 16) in the lo rows
-            uint8_t* pe = q + 4 * (2 * N * 128) + h[j] * 128 + (((lane >> 2) ^ (h[j] & 7)) << 4) + 4 * (lane & 3);
+            uint8_t* pe = q + 8 * pitch + h[j] * 128 + (((lane >> 2) ^ (h[j] & 7)) << 4) + 4 * (lane & 3);
             const float p0 = __uint_as_float(p[j] << 16) * (0.5f * down), p1 = __uint_as_float(p[j] & 0xFFFF0000u) * (0.5f * down);
             *reinterpret_cast<uint32_t*>(pe) = bf16x2(p0, p1);
-            *reinterpret_cast<uint32_t*>(pe + N * 128) = bf16x2(16.0f * p0, 16.0f * p1);
+            *reinterpret_cast<uint32_t*>(pe + pitch) = bf16x2(16.0f * p0, 16.0f * p1);
             if (lane == 0)
                 factor[h[j]] = top[j] >= 0x7F80u ? __uint_as_float(0x7FFFFFFFu) : scale_log2 * __uint_as_float((e - 7u) << 23);
         }
@@ -316,15 +317,28 @@ __device__ __noinline__ bool wait_longer(uint64_t* bar, uint32_t parity, int32_t
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int32_t* status, volatile int* abort_flag) {
     return mbar_try_wait(bar, parity) || wait_longer(bar, parity, status, abort_flag);
 }
+// (The parameters it needs come in registers: behind a pointer they are global
+// memory, and a CTA's first piece took 3 us.)
 template <int kTile>
-__device__ __noinline__ bool next_piece(const QParams* p, Walk<kTile>* walk, Work* w) { return walk->next(*p, *w); }
+__device__ __noinline__ bool next_piece(const int32_t* seq_lens, const int32_t* block_table, int hgs, int max_keys, int mbps, int block_size,
+                                        int split, Walk<kTile>* walk, Work* w) {
+    RowParams p;
+    p.seq_lens = seq_lens;
+    p.block_table = block_table;
+    p.hgs = hgs;
+    p.max_keys = max_keys;
+    p.mbps = mbps;
+    p.block_size = block_size;
+    p.split = split;
+    return walk->next(p, *w);
+}
 template <int kTile>
 struct Pieces {
     const QParams* p;
     Walk<kTile> walk;
     __device__ __forceinline__ bool next(Work& w) {
         Work got;
-        const bool more = next_piece(p, &walk, &got);
+        const bool more = next_piece(p->seq_lens, p->block_table, p->hgs, p->max_keys, p->mbps, p->block_size, p->split, &walk, &got);
         w = got;
         return more;
     }
@@ -469,16 +483,7 @@ __global__ void __launch_bounds__(threads_of(N), 1)
             start = blockIdx.x;
             end = p.rows * p.hgs;
         } else {
-            int64_t tt;
-            if (p.block_table == nullptr) {
-                tt = p.rows * p.hgs * tiles_of<kKeys>(p.max_keys);
-            } else {
-                int64_t none;
-                find_row<kKeys>(p, -1, none, tt);
-            }
-            start = run_start(blockIdx.x, gridDim.x, tt);
-            end = run_start(blockIdx.x + 1, gridDim.x, tt);
-            if (p.block_table != nullptr && start < end) find_row<kKeys>(p, start, row, base);
+            find_run<kKeys>(p, blockIdx.x, gridDim.x, start, end, row, base);
         }
         if (lane == 0) {
             sh_run[0] = start;
@@ -596,7 +601,7 @@ __global__ void __launch_bounds__(threads_of(N), 1)
                     if (t0 + i == split_at) {
                         if (!(ok = turn.wait(q_empty, p_full, p.status, abort_flag))) break;
                         if (!(ok = __all_sync(~0u, wait(q_raw, turn.item & 1, p.status, abort_flag)))) break;
-                        split_heads<N>(smem, wq * (turn.item ? kSplit : kFirst), turn.item ? kSplit : kFirst, p.scale_log2,
+                        split_heads<N>(smem, N * 128, wq * (turn.item ? kSplit : kFirst), turn.item ? kSplit : kFirst, p.scale_log2,
                                        factors + turn.item % kFactors * N);
                         fence_proxy_async_smem();
                         mbar_arrive(q_full);
@@ -608,6 +613,9 @@ __global__ void __launch_bounds__(threads_of(N), 1)
         copy_wait_all();
     } else if (warp == 1 || warp == 3) {
         // ---- queries: their copies, and the other heads ----
+        // The code that splits them comes from memory: it is fetched while the
+        // first are on their way, by a call on the weight tiles' memory.
+        if (warp == 3) split_heads<N>(smem + kPlan.p_off, 0, 0, 1, 0.0f, reinterpret_cast<float*>(smem + kPlan.p_off + 128));
         QueryTurn turn;
         bool ok = true;
         while (ok && walk.next(w)) {
@@ -623,7 +631,7 @@ __global__ void __launch_bounds__(threads_of(N), 1)
             __syncwarp();
             if (!(ok = __all_sync(~0u, wait(q_raw, turn.item & 1, p.status, abort_flag)))) break;
             const int n = turn.item ? kSplitAux : kFirstAux;
-            split_heads<N>(smem, 4 * (turn.item ? kSplit : kFirst) + (warp >> 1) * n, n, p.scale_log2, factors + turn.item % kFactors * N);
+            split_heads<N>(smem, N * 128, 4 * (turn.item ? kSplit : kFirst) + (warp >> 1) * n, n, p.scale_log2, factors + turn.item % kFactors * N);
             fence_proxy_async_smem();
             mbar_arrive(q_full);
             turn.next(w);
@@ -737,7 +745,7 @@ __global__ void __launch_bounds__(threads_of(N), 1)
         if (sh_run[0] < sh_run[1]) {
             ok = wait(q_raw, 0, p.status, abort_flag);
             if (__all_sync(~0u, ok))
-                split_heads<N>(smem, 4 * kFirst + 2 * kFirstAux + (tid >> 5) * kFirstSoft, kFirstSoft, p.scale_log2, factors);
+                split_heads<N>(smem, N * 128, 4 * kFirst + 2 * kFirstAux + (tid >> 5) * kFirstSoft, kFirstSoft, p.scale_log2, factors);
             fence_proxy_async_smem();
             mbar_arrive(q_full);
         }
