@@ -29,8 +29,8 @@ constexpr int kRowThreads = 256;      // table kernels: columns a CTA
 // Table entries that the cluster's eight CTAs write themselves: at eight a
 // thread that takes as long as another kernel's start.
 constexpr int64_t kFewCells = 8 * kScanCtas * kScanThreads;
-constexpr int kCopyThreads = 256;
-constexpr int kCopyVecs = 4;          // 16-byte vectors a thread has in flight
+constexpr int kCopyThreads = 128;
+constexpr int kCopyVecs = 8;          // 16-byte vectors a thread has in flight
 constexpr int kSlice = kCopyThreads * kCopyVecs * 16;
 
 __host__ __device__ __forceinline__ int pages_of(int64_t tokens, int block_size) {
@@ -345,15 +345,22 @@ struct CompactArgs {
     int64_t cells;
 };
 
-__device__ __forceinline__ void remap(const CompactArgs& a, int64_t i) {
-    int page = a.table[i];
-    if (page >= 0) {
-        page = page < a.num_blocks ? __ldcg(a.map + page) : -1;
-        if (page < 0) set_status(a.status, IDX_ERR_DEVICE_CHECK);
-    } else {
-        page = -1;
+// Table entries first, first + step, ... through the map, four trips to memory
+// on their way at once.
+__device__ __forceinline__ void remap(const CompactArgs& a, int64_t first, int64_t step) {
+    for (int64_t i = first; i < a.cells; i += 4 * step) {
+        int page[4], to[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) page[k] = i + k * step < a.cells ? a.table[i + k * step] : -1;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) to[k] = page[k] >= 0 && page[k] < a.num_blocks ? __ldcg(a.map + page[k]) : -1;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (i + k * step >= a.cells) break;
+            if (page[k] >= 0 && to[k] < 0) set_status(a.status, IDX_ERR_DEVICE_CHECK);
+            a.new_table[i + k * step] = to[k];
+        }
     }
-    a.new_table[i] = page;
 }
 
 // One cluster.  Pages in use are counted (n); then those from n on and the
@@ -441,15 +448,13 @@ __global__ void __launch_bounds__(kScanThreads, 1) compact_kernel(const CompactA
     if (!a.finish) return;
     cluster_arrive();
     cluster_wait();
-    for (int64_t i = thread; i < a.cells; i += kScanCtas * kScanThreads) remap(a, i);
+    remap(a, thread, kScanCtas * kScanThreads);
 }
 
 __global__ void __launch_bounds__(kRowThreads) remap_kernel(const CompactArgs a) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kRowThreads + threadIdx.x; i < a.cells;
-         i += static_cast<int64_t>(gridDim.x) * kRowThreads)
-        remap(a, i);
+    remap(a, static_cast<int64_t>(blockIdx.x) * kRowThreads + threadIdx.x, static_cast<int64_t>(gridDim.x) * kRowThreads);
 }
 
 struct CopyArgs {
@@ -464,17 +469,28 @@ struct CopyArgs {
 };
 
 // Bound by memory: each page read and written once.  A unit of work is 16 KB of
-// a page in one pool, every thread four 16-byte vectors in flight.
+// a page in one pool, every thread eight 16-byte vectors in flight.  More CTAs
+// than fit at once, as few units each leave short ends: with 64 an SM the
+// compaction of 16,384 pages (407 MB to move) takes 74 us, with the eight that
+// fit 78, with eight of 256 threads and four vectors 84.
 __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const __grid_constant__ CopyArgs a) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     int64_t n = a.n;
     if (a.count != nullptr) n = max(int64_t(0), min(n, static_cast<int64_t>(*a.count)));
     const int slices = a.first[a.pools];
-    for (int64_t u = blockIdx.x; u < n * slices; u += gridDim.x) {
-        const int64_t i = u / slices;
-        const int s = static_cast<int>(u - i * slices);
-        const int2 pair = a.pairs[i];
+    // pair and slice; the next ones' pair is read while this slice is copied
+    int64_t i = blockIdx.x / slices;
+    int next = static_cast<int>(blockIdx.x - i * slices);
+    const int di = gridDim.x / slices, ds = gridDim.x - di * slices;
+    int2 ahead = i < n ? a.pairs[i] : make_int2(-1, -1);
+    while (i < n) {
+        const int2 pair = ahead;
+        const int s = next;
+        i += di;
+        next += ds;
+        if (next >= slices) next -= slices, ++i;
+        if (i < n) ahead = a.pairs[i];
         if (pair.x < 0 || pair.y < 0) continue;
         if (pair.x >= a.num_blocks || pair.y >= a.num_blocks) {
             if (threadIdx.x == 0) set_status(a.status, IDX_ERR_DEVICE_CHECK);
@@ -681,7 +697,7 @@ idx_status idx_pages_copy(const idx_page_pool* pools, int num_pools, int64_t num
     a.n = n;
     a.num_blocks = num_blocks;
     a.pools = num_pools;
-    const int64_t units = n * slices, most = 152 * 8;
+    const int64_t units = n * slices, most = 152 * 64;
     return status_of(launch(copy_pages_kernel, dim3(static_cast<unsigned>(units < most ? units : most)), kCopyThreads, 1,
                             static_cast<cudaStream_t>(stream), a));
 }
