@@ -23,11 +23,12 @@
  *
  * Accuracy: scores are products of the stored values with the query held as
  * two e4m3 numbers under a power of two of each (row, head), which leaves
- * 2^-22 of the head's largest |ql| at most; sums and softmax statistics are
- * fp32; a key's weight times its scale is held in 8 to 9 significant bits (three
- * e5m2 numbers) for the product with its codes, small ones in steps of 2^-11 (up
- * to 64 keys) to 2^-22 (millions) of the largest, rounded up as often as they
- * are worth.  A non-finite ql makes its head's results NaN.
+ * 2^-22 of the head's largest |ql| at most (or 2^-74, if that is more); sums
+ * and softmax statistics are fp32; a key's weight times its scale is held in 8
+ * to 9 significant bits (three e5m2 numbers) for the product with its codes,
+ * small ones in steps of 2^-11 (up to 64 keys) to 2^-22 (millions) of the
+ * largest, rounded up as often as they are worth.  A non-finite ql makes its
+ * head's results NaN.
  */
 #ifndef DSAIDX_QLATENT_H
 #define DSAIDX_QLATENT_H

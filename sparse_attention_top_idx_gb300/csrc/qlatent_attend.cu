@@ -867,18 +867,21 @@ __global__ void __launch_bounds__(threads_of(N), 1)
                     // the four warps where that lies kNear above the old one.  (Each
                     // thread for its own heads is shorter in steps and longer in
                     // code, which comes from memory: it ran 3.2k cycles.)
-                    const float unit = __log2f(top), more = exp2_fast(fall);
+                    // (The sums by the difference itself: its parts pass the range.)
+                    const float unit = __log2f(top);
+                    float of_sum[2];
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         const int h = (lane + 32 * k) & (N - 1);
                         const float m = fmaxf(fmaxf(stat[h], stat[N + h]), fmaxf(stat[2 * N + h], stat[3 * N + h])) - unit;
-                        const float old = ref[k] - fall;
+                        const float was = ref[k], old = was - fall;
                         ref[k] = m - old > kNear ? m : old;
+                        of_sum[k] = exp2_fast(was - ref[k]);
                         factor_of[k] = exp2_fast(old - ref[k]);
                         which[k] = __ballot_sync(~0u, factor_of[k] != 1.0f && (N == 64 || (k == 0 && lane < N)));
                     }
                     // a thread's heads begin at lane hb & 31 of one of the two
-                    const float of = hb >= 32 ? ref[1] : ref[0], f = (hb >= 32 ? factor_of[1] : factor_of[0]) * more;
+                    const float of = hb >= 32 ? ref[1] : ref[0], f = hb >= 32 ? of_sum[1] : of_sum[0];
 #pragma unroll
                     for (int i = 0; i < kH / 2; ++i) {
                         const int l = (hb & 31) + 2 * i;

@@ -89,7 +89,9 @@ def attend64(q, rec, s, scale):
     """q [H, 576], rec [n, 576] and its scales [n] in 64 bits: out, lse and their tolerances.
 
     * A score sums 2 * 576 products in fp32 (the query is held as two numbers), each exact: terms * 2^-23 of the sum of
-      magnitudes; a query element is off by 2^-22 of its head's largest.  Together delta; a weight changes by exp(delta).
+      magnitudes; a query element is off by 2^-22 of its head's largest, or by 2^-74: the power of two that brings the
+      largest to [128, 256) is 2^60 at most, and of the lower e4m3, held times 16, half of the least step 2^-9 is
+      2^-14 2^-60.  Together delta; a weight changes by exp(delta).
     * Weights times scales are rounded to fp16 and then, up or down, to the third of three e5m2: 2^-11 + 2^-8 of sum
       p |c| at most.  The smallest e5m2 is 2^-16, and the largest product of a head over the n keys worked on together is
       held at 2^(15 - G) or more, G <= 20, n <= 4^(23 - G): smaller products w are off by up to a step
@@ -105,7 +107,7 @@ def attend64(q, rec, s, scale):
         return z, q.new_full((H,), -math.inf), z, q.new_zeros(H)
     y = q @ rec.T * scale
     big = q[:, :LAT].abs().amax(1)
-    delta = ((q.abs() @ rec.abs().T) * (2 * REC * 2.0 ** -23) + big[:, None] * rec[:, :LAT].abs().sum(1) * 2.0 ** -22).amax(1) * abs(scale)
+    delta = ((q.abs() @ rec.abs().T) * (2 * REC * 2.0 ** -23) + (big * 2.0 ** -22).clamp_min(2.0 ** -74)[:, None] * rec[:, :LAT].abs().sum(1)).amax(1) * abs(scale)
     lse = torch.logsumexp(y, 1)
     p = torch.exp(y - lse[:, None])
     v = rec[:, :LAT]

@@ -284,6 +284,27 @@ def test_attend_queries_of_any_size(size):
     assert bool(out[1, [7, 9]].isnan().all()) and bool(lse[1, [7, 9]].isnan().all())
 
 
+@pytest.mark.parametrize("H", [16, 32, 64])
+@pytest.mark.parametrize("T,n", [(2, 300), (170, 520)])
+@pytest.mark.parametrize("size", [1e-9, 1e12, 1e34])
+def test_attend_records_of_any_size(size, T, n, H):
+    """Queries as small as the records are large: scales from the least to 2^106, a first tile of small ones included."""
+    g = gen(44)
+    pool = torch.zeros(12, qr.block_bytes(64), dtype=torch.uint8, device="cuda")
+    at = torch.arange(768, device="cuda")
+    c = torch.randn(768, LAT, generator=g, device="cuda") * size
+    c[:100] *= 2.0 ** -20
+    qr.put(pool, 64, at, *qr.encode(c.to(BF), (torch.randn(768, PE, generator=g, device="cuda") * size).to(BF)))
+    cache = latent.QuantLatentCache(pool, 64)
+    ql, qp = queries(g, T, H)
+    ql, qp = (ql.float() / size).to(BF), (qp.float() / size).to(BF)
+    slots = torch.randint(100, 768, (T, n), generator=g, device="cuda")
+    slots[::2, :140] %= 100
+    got = slots_call(cache, ql, qp, slots)
+    rows = sorted({0, 1, T - 1})
+    check_attend(got[0][rows], got[1][rows], want_slots(cache, ql[rows], qp[rows], slots[rows]))
+
+
 @pytest.mark.parametrize("T,H,topk,spread", [(50, 128, 64, 0.4), (20, 64, 512, 0.4), (9, 16, 2048, 0.0), (3, 20, 700, 1.0)])
 def test_attend_errors_of_a_head_together(T, H, topk, spread):
     """A head's 512 results together: independent errors of at most 2^-9 (results), 2^-8 / sqrt(3) (weights) and 2^-9
