@@ -251,70 +251,53 @@ __device__ __forceinline__ T over_keys(T (&v)[kH], Op op) {
 // its hi and lo rows take: a warp reads a head and writes it back split, 16
 // values a lane.  (Read by plain loads instead, two heads ahead, a head took
 // 500 to 1200 cycles: trips to L2.)
-// Two heads at once: a head is a chain of trips to shared memory and through the
-// warp (440 cycles).
-// One copy for the roles that call it: the kernel's code is larger than the
-// instruction caches.  `pitch` (bytes of an eighth's heads) is N * 128, or 0 for
-// a call that only brings the code near.
+// One copy for the roles that call it, a head at a time: the kernel's code is
+// larger than the instruction caches (two heads at once took as long).  `pitch`
+// (bytes of an eighth's heads) is N * 128, or 0 for a call that only brings the
+// code near.
 template <int N>
 __device__ __noinline__ void split_heads(uint8_t* q, int pitch, int first, int n, float scale_log2, float* factor) {
     const int lane = lane_id();
 #pragma unroll 1
-    for (int k0 = 0; k0 < n; k0 += 2) {
-        int h[2];
-        uint32_t w[2][8], p[2], top[2];
+    for (int h = first; h < first + n; ++h) {
+        // raw: pieces 2 (lane % 4) and the next of 64 values; split: piece lane % 8 of 128
+        const uint8_t* raw = q + (lane >> 2) * pitch + h * 128;
+        uint8_t* row = q + 2 * (lane >> 3) * pitch + h * 128 + (((lane & 7) ^ (h & 7)) << 4);
+        uint8_t* pe = q + 8 * pitch + h * 128 + (((lane >> 2) ^ (h & 7)) << 4) + 4 * (lane & 3);
+        const uint4 u = *reinterpret_cast<const uint4*>(raw + (((2 * (lane & 3)) ^ (h & 7)) << 4));
+        const uint4 v = *reinterpret_cast<const uint4*>(raw + (((2 * (lane & 3) + 1) ^ (h & 7)) << 4));
+        const uint32_t p = *reinterpret_cast<const uint32_t*>(pe);
+        const uint32_t w[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+        uint32_t top = 0;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            h[j] = first + min(k0 + j, n - 1);      // (the last one twice: the same is written)
-            // raw: pieces 2 (lane % 4) and the next of 64 values
-            const uint8_t* raw = q + (lane >> 2) * pitch + h[j] * 128;
-            const uint4 u = *reinterpret_cast<const uint4*>(raw + (((2 * (lane & 3)) ^ (h[j] & 7)) << 4));
-            const uint4 v = *reinterpret_cast<const uint4*>(raw + (((2 * (lane & 3) + 1) ^ (h[j] & 7)) << 4));
-            p[j] = *reinterpret_cast<const uint32_t*>(q + 8 * pitch + h[j] * 128 + (((lane >> 2) ^ (h[j] & 7)) << 4) + 4 * (lane & 3));
-            w[j][0] = u.x, w[j][1] = u.y, w[j][2] = u.z, w[j][3] = u.w;
-            w[j][4] = v.x, w[j][5] = v.y, w[j][6] = v.z, w[j][7] = v.w;
-        }
+        for (int i = 0; i < 8; ++i) top = __vmaxu2(top, w[i] & 0x7FFF7FFFu);
+        top = __reduce_max_sync(~0u, max(top & 0xFFFFu, top >> 16));      // (also: every lane has read)
+        // 2^-a brings the largest to [128, 256); a <= 60, so that the position
+        // part stays finite
+        const uint32_t e = max(top >> 7, 74u);
+        const float down = __uint_as_float((261u - e) << 23);
+        uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            top[j] = 0;
+        for (int i = 0; i < 4; ++i) {
+            uint32_t a[2], b[2];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) top[j] = __vmaxu2(top[j], w[j][i] & 0x7FFF7FFFu);
-            top[j] = max(top[j] & 0xFFFFu, top[j] >> 16);
-        }
-#pragma unroll
-        for (int j = 0; j < 2; ++j) top[j] = __reduce_max_sync(~0u, top[j]);      // (also: every lane has read)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            // 2^-a brings the largest to [128, 256); a >= -60, so that the position
-            // part stays finite
-            const uint32_t e = max(top[j] >> 7, 74u);
-            const float down = __uint_as_float((261u - e) << 23);
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t a[2], b[2];
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const uint32_t x = w[j][2 * i + k];
-                    const uint32_t f = f16x2(__uint_as_float(x << 16) * down, __uint_as_float(x & 0xFFFF0000u) * down);
-                    a[k] = e4m3x2(f);
-                    b[k] = e4m3x2(mul_f16x2(sub_f16x2(f, from_e4m3x2(a[k])), 0x4C004C00u));      // 16
-                }
-                hi[i] = a[0] | a[1] << 16;
-                lo[i] = b[0] | b[1] << 16;
+            for (int k = 0; k < 2; ++k) {
+                const uint32_t x = w[2 * i + k];
+                const uint32_t f = f16x2(__uint_as_float(x << 16) * down, __uint_as_float(x & 0xFFFF0000u) * down);
+                a[k] = e4m3x2(f);
+                b[k] = e4m3x2(mul_f16x2(sub_f16x2(f, from_e4m3x2(a[k])), 0x4C004C00u));      // 16
             }
-            // split: piece lane % 8 of 128
-            uint8_t* row = q + 2 * (lane >> 3) * pitch + h[j] * 128 + (((lane & 7) ^ (h[j] & 7)) << 4);
-            *reinterpret_cast<uint4*>(row) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4*>(row + pitch) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-            // half of the position part in the hi rows, the other half (times 16) in the lo rows
-            uint8_t* pe = q + 8 * pitch + h[j] * 128 + (((lane >> 2) ^ (h[j] & 7)) << 4) + 4 * (lane & 3);
-            const float p0 = __uint_as_float(p[j] << 16) * (0.5f * down), p1 = __uint_as_float(p[j] & 0xFFFF0000u) * (0.5f * down);
-            *reinterpret_cast<uint32_t*>(pe) = bf16x2(p0, p1);
-            *reinterpret_cast<uint32_t*>(pe + pitch) = bf16x2(16.0f * p0, 16.0f * p1);
-            if (lane == 0)
-                factor[h[j]] = top[j] >= 0x7F80u ? __uint_as_float(0x7FFFFFFFu) : scale_log2 * __uint_as_float((e - 7u) << 23);
+            hi[i] = a[0] | a[1] << 16;
+            lo[i] = b[0] | b[1] << 16;
         }
+        *reinterpret_cast<uint4*>(row) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(row + pitch) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        // half of the position part in the hi rows, the other half (times 16) in the lo rows
+        const float p0 = __uint_as_float(p << 16) * (0.5f * down), p1 = __uint_as_float(p & 0xFFFF0000u) * (0.5f * down);
+        *reinterpret_cast<uint32_t*>(pe) = bf16x2(p0, p1);
+        *reinterpret_cast<uint32_t*>(pe + pitch) = bf16x2(16.0f * p0, 16.0f * p1);
+        if (lane == 0)
+            factor[h] = top >= 0x7F80u ? __uint_as_float(0x7FFFFFFFu) : scale_log2 * __uint_as_float((e - 7u) << 23);
     }
 }
 
@@ -817,7 +800,7 @@ __global__ void __launch_bounds__(threads_of(N), 1)
                         bool grow = weigh<kH>(dot, factor, scale, minus_m, by, e, r);
                         grow |= by > kMost * kMostScale && top < kTopUnit;
                         if (valid && scale < kLeast) {
-                            // such a key's weight has no product to judge it by
+                            // such a key's weight has no product to tell it by
 #pragma unroll
                             for (int i = 0; i < kH / 2; ++i) grow |= fmaxf(f2_unpack(e[i]).x, f2_unpack(e[i]).y) > kMostWeight;
                         }
