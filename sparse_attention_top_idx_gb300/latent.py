@@ -86,6 +86,9 @@ def header_functions(header: str = HEADER):
 # for speed: one pass over what has to hold, the message only where it fails.
 # Every tensor of a call has to be on the device of its first one (dev), which
 # has to be the current one: the kernels are launched there.
+_Tensor = torch.Tensor      # a name less to look up in each check
+
+
 def _refuse(t, dtype, name: str, shape, dense: bool, dev):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError("%s must be a CUDA tensor" % name)
@@ -100,7 +103,7 @@ def _refuse(t, dtype, name: str, shape, dense: bool, dev):
 
 def _dev(t, name: str) -> int:
     """Index of the device of a call's first tensor."""
-    dev = t.get_device() if isinstance(t, torch.Tensor) else -1
+    dev = t.get_device() if isinstance(t, _Tensor) else -1
     if dev < 0:
         raise TypeError("%s must be a CUDA tensor" % name)
     return dev
@@ -108,7 +111,7 @@ def _dev(t, name: str) -> int:
 
 def _dense(t: torch.Tensor, dtype, name: str, dev: int, shape=None) -> int:
     """Address of a contiguous tensor of that type (and shape) on that device."""
-    if not (isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype == dtype
+    if not (isinstance(t, _Tensor) and t.get_device() == dev and t.dtype is dtype
             and (shape is None or t.shape == shape) and t.is_contiguous()):
         _refuse(t, dtype, name, shape, True, dev)
     return t.data_ptr()
@@ -116,7 +119,7 @@ def _dense(t: torch.Tensor, dtype, name: str, dev: int, shape=None) -> int:
 
 def _strided(t: torch.Tensor, dtype, name: str, dev: int, shape):
     """Address and strides of a tensor of that type and shape on that device whose last dimension is contiguous."""
-    if not (isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype == dtype and t.shape == shape):
+    if not (isinstance(t, _Tensor) and t.get_device() == dev and t.dtype is dtype and t.shape == shape):
         _refuse(t, dtype, name, shape, False, dev)
     st = t.stride()
     if st[-1] != 1 and shape[-1] > 1 and t.numel():
