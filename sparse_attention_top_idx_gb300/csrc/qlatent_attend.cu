@@ -1149,11 +1149,13 @@ Shape shape_n(int64_t rows, int heads, int N, int64_t max_keys, bool paged, int6
     const int64_t items = rows * s.hgs, nt = max_keys > 0 ? (max_keys + kKeys - 1) / kKeys : 1;
     *cost = (items + g - 1) / g * (nt * tile + ends);
     s.ctas = static_cast<int>(items < g ? items : g);
-    // A cluster for a row while all fit at once (of eight: 64 CTAs).  A paged batch
-    // is ragged, which the cut evens out, so long contexts take no clusters.
+    // A cluster for a row while all fit at once: 76 of two do, 36 of four and 15 of
+    // eight (by the GPCs' sizes, so two and one fewer are counted on); one more
+    // takes another round (16 of eight 21 us instead of 12.8 as eight of four).  A
+    // paged batch is ragged, which the cut evens out, so long contexts take none.
     for (int c = 2; c <= 8; c *= 2) {
         const int64_t t = (nt + c - 1) / c * tile + ends + (N == 64 ? 5000 : 2000);
-        if (items * c <= (c == 8 ? 64 : c == 4 ? 128 : g) && c <= nt && t < *cost && !(paged && max_keys > 1024)) {
+        if (items * c <= (c == 8 ? 112 : c == 4 ? 136 : g) && c <= nt && t < *cost && !(paged && max_keys > 1024)) {
             *cost = t;
             s.split = 2;
             s.cluster = c;
