@@ -4,6 +4,7 @@ before any CUDA call, so no GPU is needed: pointers are made-up addresses that
 are never read)."""
 import ctypes
 import math
+import random
 
 import pytest
 import torch
@@ -99,6 +100,28 @@ def test_attend_refusals(lib):
     paged[9] = 0
     assert lib.idx_qlatent_attend_slots(pool(), *slots) == OK
     assert lib.idx_qlatent_attend_paged(pool(), *paged) == OK
+
+
+def ws_answers(lib, rows, heads, keys, size):
+    """What calls without slots or a table answer, which is looked at behind the workspace's size."""
+    head = [A, 512 * heads, 512, A, 64 * heads, 64]
+    return (lib.idx_qlatent_attend_slots(pool(), *head, None, keys, rows, heads, keys, 1.0, A, None, A, size, None),
+            lib.idx_qlatent_attend_paged(pool(), *head, None, 1, A, rows, keys, heads, 1.0, A, None, A, size, None))
+
+
+def test_a_workspace_of_the_largest_call_serves_every_smaller_one(lib):
+    r = random.Random(3)
+    sizes = [(rows, heads, keys) for rows in (1, 7, 14, 18, 19, 37, 38, 75, 76, 77, 152, 153, 300, 4096)
+             for heads in (1, 16, 17, 32, 33, 64, 65, 128, 1024) for keys in (1, 128, 640, 641, 1024, 1025, 4096, 131072, 1 << 24)]
+    sizes += [(r.randint(1, 700), r.randint(1, 300), int(2 ** r.uniform(0, 18))) for _ in range(3000)]
+    for c in sizes:
+        size = latent.workspace_bytes(*c)
+        assert ws_answers(lib, *c, size) == (INVALID, INVALID), c
+        smaller = [r.randint(1, x) for x in c]
+        assert ws_answers(lib, *smaller, size) == (INVALID, INVALID), (smaller, c)
+    # a cut one needs room, and says so (32 rows of selected slots lie over clusters, which need none)
+    assert ws_answers(lib, 32, 16, 10000, 256) == (INVALID, TOO_SMALL)
+    assert ws_answers(lib, 200, 16, 1024, 256) == (TOO_SMALL, TOO_SMALL)
 
 
 def test_fork_refusals(lib):
