@@ -81,7 +81,11 @@ class SlotsCluster(Slots):
 
 
 class SlotsCut(Slots):
-    T, H, topk = 200, 16, 1024
+    T, H, topk = 160, 16, 1024
+
+
+class SlotsCutWide(Slots):
+    T, H, topk = 39, 64, 2048
 
 
 class SlotsWide(Slots):
@@ -115,7 +119,7 @@ class PagedCut(Paged):
     lens = [4000, 17, 9000]
 
 
-CALLS = [Append, Read, Slots, SlotsCluster, SlotsCut, SlotsWide, Paged, PagedCut]
+CALLS = [Append, Read, Slots, SlotsCluster, SlotsCut, SlotsCutWide, SlotsWide, Paged, PagedCut]
 
 
 @pytest.mark.parametrize("make", CALLS)
@@ -186,7 +190,7 @@ def first_position_element(c, values):
     return at.numel()
 
 
-@pytest.mark.parametrize("make", [Slots, SlotsCluster, SlotsCut, SlotsWide])
+@pytest.mark.parametrize("make", [Slots, SlotsCluster, SlotsCut, SlotsCutWide, SlotsWide])
 def test_infinite_scores_of_selected_keys(make):
     """A score of -inf is a weight of 0, a row of them alone an empty one; +inf leaves no finite softmax: NaN.  Heads beside
     it are not touched."""
@@ -215,7 +219,7 @@ def test_infinite_scores_of_selected_keys(make):
     check_attend(c.out[1:2, heads], c.lse[1:2, heads], [tuple(x[heads] for x in want)])
 
 
-@pytest.mark.parametrize("make", [Slots, SlotsCluster, SlotsCut, SlotsWide])
+@pytest.mark.parametrize("make", [Slots, SlotsCluster, SlotsCut, SlotsCutWide, SlotsWide])
 def test_some_keys_at_minus_infinity(make):
     """Records with -inf in an element that every query weighs positively: their weights are 0, the others' as without them."""
     c = make()
@@ -234,7 +238,7 @@ def test_some_keys_at_minus_infinity(make):
     assert bool((c.out[0] == 0).all())
 
 
-@pytest.mark.parametrize("make", [Slots, SlotsCluster, SlotsCut, SlotsWide])
+@pytest.mark.parametrize("make", [Slots, SlotsCluster, SlotsCut, SlotsCutWide, SlotsWide])
 def test_keys_and_queries_that_are_no_numbers(make):
     """A NaN latent makes every result of the rows that select it NaN and of no other; one in a query that of its head."""
     c = make()

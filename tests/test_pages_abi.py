@@ -121,7 +121,7 @@ def test_a_workspace_of_the_largest_call_serves_every_smaller_one(lib):
         assert ws_answers(lib, *smaller, size) == (INVALID, INVALID), (smaller, c)
     # a cut one needs room, and says so (32 rows of selected slots lie over clusters, which need none)
     assert ws_answers(lib, 32, 16, 10000, 256) == (INVALID, TOO_SMALL)
-    assert ws_answers(lib, 200, 16, 1024, 256) == (TOO_SMALL, TOO_SMALL)
+    assert ws_answers(lib, 160, 16, 1024, 256) == (TOO_SMALL, TOO_SMALL)
 
 
 def test_fork_refusals(lib):
