@@ -275,11 +275,28 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const RowParams p
             ml[r] = make_float2(kNone, 0.0f);
             if (k >= pieces) continue;
             const int64_t start = run_start(c0 + k, ctas, tt);
-            if (start == run_start(c0 + k + 1, ctas, tt)) continue;
-            from[warp][k] = static_cast<int>(2 * (c0 + k) + (start < a ? 1 : 0)) * N + h;
-            ml[r] = p.part_ml[from[warp][k]];
-            if (ml[r].y != 0.0f) m = fmaxf(m, ml[r].x);
+            const bool empty = start == run_start(c0 + k + 1, ctas, tt);
+            const int at = empty ? -1 : static_cast<int>(2 * (c0 + k) + (start < a ? 1 : 0)) * N + h;
+            from[warp][k] = at;
+            if (!empty) ml[r] = p.part_ml[at];
         }
+        __syncwarp();
+        // the first pieces' sums are on their way beside their statistics
+        float4 v[4][4];
+        auto load = [&](int k0) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int k = k0 + u * kW, at = k < pieces ? from[warp][k] : -1;
+                if (at < 0) continue;
+                const float4* src = reinterpret_cast<const float4*>(p.part_o + static_cast<int64_t>(at) * IDX_LATENT_DIM);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) v[u][q] = __ldg(src + 32 * q + lane);
+            }
+        };
+        load(wh);
+#pragma unroll
+        for (int r = 0; r < kRounds; ++r)
+            if (ml[r].y != 0.0f) m = fmaxf(m, ml[r].x);
         for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
 #pragma unroll
         for (int r = 0; r < kRounds; ++r) {
@@ -290,26 +307,18 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const RowParams p
         for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(~0u, l, d);
         __syncwarp();
         for (int k0 = wh; k0 < pieces; k0 += 4 * kW) {
-            float4 v[4][4];
-            float f[4];
+            if (k0 != wh) load(k0);
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 const int k = k0 + u * kW;
-                f[u] = k < pieces ? factor[warp][k] : 0.0f;
-                if (f[u] == 0.0f) continue;
-                const float4* src = reinterpret_cast<const float4*>(p.part_o + static_cast<int64_t>(from[warp][k]) * IDX_LATENT_DIM);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) v[u][q] = __ldg(src + 32 * q + lane);
-            }
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                if (f[u] == 0.0f) continue;
+                const float f = k < pieces ? factor[warp][k] : 0.0f;      // (0: there is nothing)
+                if (f == 0.0f) continue;
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    o[q].x += v[u][q].x * f[u];
-                    o[q].y += v[u][q].y * f[u];
-                    o[q].z += v[u][q].z * f[u];
-                    o[q].w += v[u][q].w * f[u];
+                    o[q].x += v[u][q].x * f;
+                    o[q].y += v[u][q].y * f;
+                    o[q].z += v[u][q].z * f;
+                    o[q].w += v[u][q].w * f;
                 }
             }
         }
