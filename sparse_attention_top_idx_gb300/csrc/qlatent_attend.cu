@@ -41,14 +41,15 @@
 // Statistics, sums and accumulators are fp32.  Rows are whole, shared by a
 // cluster or cut into equal runs as in latent_rows.cuh.
 //
-// Measured: 4096 rows of 1024 keys x 128 heads take 1.49 ms (786 TFLOP/s of the
+// Measured: 4096 rows of 1024 keys x 128 heads take 1.49 ms (784 TFLOP/s of the
 // definition's products).  A tile of 64 keys x 64 heads takes 1.34 us, its 20 score
-// and 24 value steps 1.25 of them; a row's beginning and end another 4.5 us, as
-// the next queries can be written only behind the last scores: 1 us their copy,
-// 3 us their split, beside the epilogue (3 us) in the other warps, 1.3 us the first
-// scores.  Long contexts of 16 heads are read at 6.1 TB/s.  Calls of few tiles are
-// a chain of first times: half of a 17 us call has passed when the first weights
-// are there, most of it code and records from memory.
+// and 24 value steps 1.25 of them (and the softmax's chain of waits, loads, votes
+// and fences about as much); a row's beginning and end another 6 us, as the next
+// queries can be written only behind the last scores: 1 us their copy, 3 us their
+// split, beside the epilogue (3 us) in the other warps, 1.2 us the first scores,
+// 1.4 us their softmax.  Long contexts of 16 heads are read at 6.1 TB/s.  Calls of
+// few tiles are a chain of first times: half of a 17 us call has passed when the
+// first weights are there, most of it code and records from memory.
 #include <cuda_fp16.h>
 
 #include <algorithm>
